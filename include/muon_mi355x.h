@@ -272,6 +272,146 @@ int32_t muon_adamw_batched(int32_t batch, const int64_t* numel, void* const* p,
                            const muon_adamw_params* params, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/*
+ * Gradient clipping by the global norm, the usual step between the backward
+ * pass and the optimizer: one norm over every gradient of the model (the
+ * matrices Muon steps and the tensors AdamW steps together), and one factor
+ *     n = sqrt(sum_i sum_j g_ij^2)         MUON_NORM_L2
+ *     n = max_ij |g_ij|                    MUON_NORM_MAX
+ *     s = min(1, max_norm / (n + eps))     (1 when clip = 0 or n + eps = 0)
+ * Squares are formed and summed in double; n and s are rounded once, to fp32.
+ * A NaN gradient gives n = s = NaN, an infinite one n = inf and s = 0.  The
+ * library never looks at n on the host: every call stays asynchronous.
+ *
+ * The factor can be applied in two ways:
+ *  - muon_grad_clip_batched, or muon_grad_scale_batched with a factor that was
+ *    formed elsewhere (a norm over several ranks): out_ij = s * g_ij in fp32,
+ *    rounded to out's type.  out[i] may be g[i] (of the same type; a factor of
+ *    exactly 1 then leaves it untouched), or another buffer of either type: the
+ *    fp32 sums of gradients over micro-batches go into the bf16 gradients that
+ *    the step reads in the same pass.
+ *  - muon_step_batched_scaled and muon_adamw_batched_scaled, which multiply
+ *    each gradient by the factor in fp32 as they read it: no extra pass, and no
+ *    rounding of s * g to the gradient's type.
+ *
+ * These tensors may have different types: dtype[i] (and out_dtype[i]) is
+ * MUON_BF16 or MUON_FP32 for tensor i.  Other conventions are those at the top
+ * of this header; in addition these calls enqueue kernel launches only, so they
+ * can be captured into a HIP graph (with per-kernel timing off) and replayed.
+ * A captured call uses its workspace at every replay.
+ */
+typedef enum { MUON_NORM_L2 = 0, MUON_NORM_MAX = 1 } muon_norm_kind;
+
+typedef struct {
+  int32_t kind;   /* muon_norm_kind */
+  int32_t clip;   /* 1: form s from max_norm; 0: s = 1 (max_norm is not read) */
+  float max_norm; /* >= 0, finite */
+  float eps;      /* >= 0, finite; 1e-6 is usual */
+} muon_grad_norm_params;
+
+/* Bytes of device workspace the three calls below need.  numel[i] >= 0.
+ * Returns SIZE_MAX on invalid arguments.  Host-only. */
+size_t muon_grad_workspace_bytes(int32_t batch, const int64_t* numel);
+
+/*
+ * The global norm: result[0] = n, result[1] = s (device memory, 4-byte
+ * aligned).  batch == 0 gives n = 0, s = 1.
+ *   numel[i]   element count of tensor i (0 allowed)
+ *   g[i]       16-byte aligned device pointer (not read when numel[i] is 0)
+ *   workspace  at least muon_grad_workspace_bytes() bytes, 256-byte aligned
+ */
+int32_t muon_grad_norm_batched(int32_t batch, const int64_t* numel, const void* const* g,
+                               const int32_t* dtype, const muon_grad_norm_params* p, float* result,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* out[i] = scale * g[i], scale[0] in device memory. */
+int32_t muon_grad_scale_batched(int32_t batch, const int64_t* numel, const void* const* g,
+                                const int32_t* dtype, void* const* out, const int32_t* out_dtype,
+                                const float* scale, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Both: result as muon_grad_norm_batched (p->clip must be 1), then
+ * out[i] = result[1] * g[i].  result must lie outside every g[i] and out[i]. */
+int32_t muon_grad_clip_batched(int32_t batch, const int64_t* numel, const void* const* g,
+                               const int32_t* dtype, void* const* out, const int32_t* out_dtype,
+                               const muon_grad_norm_params* p, float* result, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* muon_step_batched with every gradient multiplied by grad_scale[0] (fp32,
+ * device memory, 4-byte aligned) in fp32 as it is read:
+ *     M' = beta*M + s*G;  U = s*G + beta*M' if nesterov, else M'.
+ * grad_scale is read on the stream, so it may be the result of an earlier call
+ * there.  The workspace is that of muon_step_batched. */
+int32_t muon_step_batched_scaled(int32_t batch, const int64_t* rows, const int64_t* cols,
+                                 void* const* w, const void* const* g, void* const* m,
+                                 int32_t dtype, const muon_step_params* p, const float* grad_scale,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* muon_adamw_batched with g replaced by grad_scale[0] * g, likewise. */
+int32_t muon_adamw_batched_scaled(int32_t batch, const int64_t* numel, void* const* p,
+                                  const void* const* g, float* const* m, float* const* v,
+                                  int32_t dtype, const muon_adamw_params* params,
+                                  const float* grad_scale, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * Block-scaled e4m3 operands and their product, for the expert matrices whose
+ * gradients the step takes: FP8 for expert matrix math is an open question on
+ * "Domyn is training a 1T-parameter MoE on Europe's Jupiter supercomputer, and
+ * published the recipe" (§What moved the number, closing paragraph).
+ *
+ * An operand of R rows, contracted over K columns, is two arrays, with
+ * Kp = K rounded up to a multiple of MUON_F8_BLOCK and Rp = R rounded up to a
+ * multiple of 16:
+ *   values  R x Kp bytes, row-major: OCP e4m3 (no infinity, largest 448),
+ *           columns K .. Kp-1 zero
+ *   scales  Kp/MUON_F8_BLOCK x Rp bytes, row-major: byte [kb][r] = e + 127, the
+ *           power of two 2^e that scales columns 128 kb .. 128 kb + 127 of row r;
+ *           entries r >= R zero
+ * Both 16-byte aligned.  A value stands for e4m3 * 2^e.
+ *
+ * muon_f8_quantize_batched forms the operands of a ragged batch of matrices
+ * x[i] (rows[i] x cols[i], row-major, contiguous, `dtype`), of their
+ * transposes, or of both from one read:
+ *   block_rows  1: a scale of its own for each 1 x 128 block along the contracted
+ *               side (activations, gradients); MUON_F8_BLOCK: one for each
+ *               128 x 128 block of the matrix, written out for every row
+ *               (weights: the operand and its transpose then hold the same values)
+ *   q, s        values and scales of x[i] (contracted over its columns); both
+ *               arrays null: not formed
+ *   qt, st      those of x[i] transposed (contracted over its rows); likewise
+ * e is the smallest exponent, at least -127, with the block's largest finite
+ * magnitude at most 448 * 2^e, so nothing saturates; values are rounded to
+ * nearest even.  An infinity or NaN becomes NaN and takes no part in the scale.
+ *
+ * muon_f8_matmul_batched: c[i] = A_i B_i^T (+ c[i] when accumulate = 1), A_i of
+ * m[i] rows and B_i of n[i] rows, both contracted over k[i]:
+ *   c[i]   m[i] x n[i], row-major, contiguous, `dtype` (MUON_BF16 or MUON_FP32)
+ * summed in fp32 and rounded once, at the store (the old c is added in fp32
+ * before it).  k[i] = 0 gives zeros (or leaves c).  Of Y = X W^T, the backward
+ * products take the same call: dX = dY W with operands dY and W^T, and
+ * dW = dY^T X with operands dY^T and X^T.
+ *
+ * Every size lies in [0, MUON_F8_MAX_DIM]; pointers of empty operands are not
+ * read.  workspace: at least muon_f8_workspace_bytes(batch) bytes, 256-byte
+ * aligned.  Like the calls above, both can be captured into a HIP graph.
+ */
+#define MUON_F8_BLOCK 128
+#define MUON_F8_MAX_DIM 1048576
+
+size_t muon_f8_workspace_bytes(int32_t batch);
+
+int32_t muon_f8_quantize_batched(int32_t batch, const int64_t* rows, const int64_t* cols,
+                                 const void* const* x, int32_t dtype, int32_t block_rows,
+                                 void* const* q, void* const* s, void* const* qt, void* const* st,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const int64_t* n,
+                               const int64_t* k, const void* const* a, const void* const* sa,
+                               const void* const* b, const void* const* sb, void* const* c,
+                               int32_t dtype, int32_t accumulate, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* Kernels of the step, and the momentum copies of a step with the momentum in
  * host memory, for per-kernel timing. */
 typedef enum {
@@ -290,7 +430,11 @@ typedef enum {
   MUON_K_PROD8 = 12,      /* e4m3 steps: X <- a X + B X */
   MUON_K_MOM_IN = 13,     /* momentum_host: one chunk's momentum copied to the device (DMA) */
   MUON_K_MOM_OUT = 14,    /* momentum_host: one chunk's momentum copied back to the host (DMA) */
-  MUON_K_COUNT = 15
+  MUON_K_GRAD_NORM = 15,  /* the global gradient norm */
+  MUON_K_GRAD_SCALE = 16, /* gradients times a factor */
+  MUON_K_F8_QUANTIZE = 17, /* muon_f8_quantize_batched */
+  MUON_K_F8_PROD = 18,    /* muon_f8_matmul_batched */
+  MUON_K_COUNT = 19
 } muon_kernel;
 
 /*

@@ -7,8 +7,9 @@ library is missing the calls raise; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
-from typing import List, Optional, Sequence, Tuple
+from typing import List, NamedTuple, Optional, Sequence, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libmuon_mi355x.so")
@@ -28,9 +29,13 @@ EXPORTED = ("muon_workspace_bytes", "muon_workspace_bytes_ex", "muon_ns_batched"
             "muon_step_batched",
             "muon_adamw_workspace_bytes", "muon_adamw_batched",
             "muon_status_string", "muon_last_error_detail", "muon_timing_enable",
-            "muon_timing_read", "muon_timing_reset", "muon_hbm_stream")
+            "muon_timing_read", "muon_timing_reset", "muon_hbm_stream",
+            "muon_grad_workspace_bytes", "muon_grad_norm_batched", "muon_grad_scale_batched",
+            "muon_grad_clip_batched", "muon_step_batched_scaled", "muon_adamw_batched_scaled",
+            "muon_f8_workspace_bytes", "muon_f8_quantize_batched", "muon_f8_matmul_batched")
 KERNELS = ("prepare", "norm", "gram", "poly", "prod", "finish", "adamw", "prod_finish", "prod_first",
-           "quant8", "gram8", "poly8", "prod8", "mom_in", "mom_out")
+           "quant8", "gram8", "poly8", "prod8", "mom_in", "mom_out",
+           "grad_norm", "grad_scale", "f8_quantize", "f8_prod")
 
 
 class MuonError(RuntimeError):
@@ -56,6 +61,11 @@ class AdamWParams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
                 ("step", ctypes.c_int32)]
+
+
+class GradNormParams(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("clip", ctypes.c_int32), ("max_norm", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 _lib_handle: Optional[ctypes.CDLL] = None
@@ -111,6 +121,31 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_timing_reset.restype = i32
     lib.muon_hbm_stream.argtypes = [i32, vpp, i32, vpp, sz, i32, vp]
     lib.muon_hbm_stream.restype = i32
+    i32p = ctypes.POINTER(i32)
+    lib.muon_grad_workspace_bytes.argtypes = [i32, i64p]
+    lib.muon_grad_workspace_bytes.restype = sz
+    lib.muon_grad_norm_batched.argtypes = [i32, i64p, vpp, i32p, ctypes.POINTER(GradNormParams), vp,
+                                           vp, sz, vp]
+    lib.muon_grad_norm_batched.restype = i32
+    lib.muon_grad_scale_batched.argtypes = [i32, i64p, vpp, i32p, vpp, i32p, vp, vp, sz, vp]
+    lib.muon_grad_scale_batched.restype = i32
+    lib.muon_grad_clip_batched.argtypes = [i32, i64p, vpp, i32p, vpp, i32p,
+                                           ctypes.POINTER(GradNormParams), vp, vp, sz, vp]
+    lib.muon_grad_clip_batched.restype = i32
+    lib.muon_step_batched_scaled.argtypes = [i32, i64p, i64p, vpp, vpp, vpp, i32,
+                                             ctypes.POINTER(StepParams), vp, vp, sz, vp]
+    lib.muon_step_batched_scaled.restype = i32
+    lib.muon_adamw_batched_scaled.argtypes = [i32, i64p, vpp, vpp, vpp, vpp, i32,
+                                              ctypes.POINTER(AdamWParams), vp, vp, sz, vp]
+    lib.muon_adamw_batched_scaled.restype = i32
+    lib.muon_f8_workspace_bytes.argtypes = [i32]
+    lib.muon_f8_workspace_bytes.restype = sz
+    lib.muon_f8_quantize_batched.argtypes = [i32, i64p, i64p, vpp, i32, i32, vpp, vpp, vpp, vpp, vp,
+                                             sz, vp]
+    lib.muon_f8_quantize_batched.restype = i32
+    lib.muon_f8_matmul_batched.argtypes = [i32, i64p, i64p, i64p, vpp, vpp, vpp, vpp, vpp, i32, i32,
+                                           vp, sz, vp]
+    lib.muon_f8_matmul_batched.restype = i32
     _lib_handle = lib
     return lib
 
@@ -274,8 +309,12 @@ def ns_batched_noalloc(xs: Sequence, out: Sequence, steps: int = 5, coeffs=QUINT
 def step_batched(ws: Sequence, gs: Sequence, ms: Sequence, lr: float = 0.02, beta: float = 0.95,
                  nesterov: bool = False, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7,
                  workspace=None, momentum_host: bool = False, cu_budget: int = 0,
-                 fp8_steps: int = 0) -> None:
+                 fp8_steps: int = 0, grad_scale=None) -> None:
     """One Muon step over a ragged batch, in place on ws (weights) and ms (momentum).
+
+    grad_scale: a one-element float32 tensor on the weights' device (the clip
+    factor of grad_norm_batched); every gradient is multiplied by it in fp32 as
+    it is read.
 
     momentum_host: the momenta are pinned host tensors (pin_memory), updated in
     place: the step copies them to the device and back in chunks, overlapped
@@ -309,15 +348,25 @@ def step_batched(ws: Sequence, gs: Sequence, ms: Sequence, lr: float = 0.02, bet
     p = StepParams(float(lr), float(beta), 1 if nesterov else 0,
                    NsParams(int(steps), a, b, c, float(eps), int(cu_budget), int(fp8_steps)),
                    1 if momentum_host else 0)
+    fn, scale = lib.muon_step_batched, ()
+    if grad_scale is not None:
+        fn, scale = lib.muon_step_batched_scaled, (_scale_pointer(grad_scale, dev),)
     with torch.cuda.device(dev):
-        st = lib.muon_step_batched(len(ws), _i64_array([s[0] for s in shapes]),
-                                   _i64_array([s[1] for s in shapes]),
-                                   _ptr_array([w.data_ptr() for w in ws]),
-                                   _ptr_array([g.data_ptr() for g in gs]),
-                                   _ptr_array([m.data_ptr() for m in ms]), code, ctypes.byref(p),
-                                   ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                   ctypes.c_void_p(_stream_handle(dev)))
-    _check(st, "muon_step_batched")
+        st = fn(len(ws), _i64_array([s[0] for s in shapes]), _i64_array([s[1] for s in shapes]),
+                _ptr_array([w.data_ptr() for w in ws]), _ptr_array([g.data_ptr() for g in gs]),
+                _ptr_array([m.data_ptr() for m in ms]), code, ctypes.byref(p), *scale,
+                ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+                ctypes.c_void_p(_stream_handle(dev)))
+    _check(st, fn.__name__)
+
+
+def _scale_pointer(t, dev):
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != torch.float32 or \
+            t.numel() != 1:
+        raise ValueError("grad_scale: a float32 tensor of one element on the device of the weights")
+    return ctypes.c_void_p(t.data_ptr())
 
 
 def adamw_workspace_bytes(numels: Sequence[int]) -> int:
@@ -331,8 +380,13 @@ def adamw_workspace_bytes(numels: Sequence[int]) -> int:
 
 def adamw_batched(params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg_sqs: Sequence,
                   lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
-                  weight_decay: float = 1e-2, step: int = 1, workspace=None) -> None:
+                  weight_decay: float = 1e-2, step: int = 1, workspace=None,
+                  grad_scale=None) -> None:
     """One AdamW step over a ragged batch of tensors, in place on params and the moments.
+
+    grad_scale: a one-element float32 tensor on the parameters' device (the clip
+    factor of grad_norm_batched); every gradient is multiplied by it in fp32 as
+    it is read.
 
     params/grads: bf16 or fp32 (one dtype for all), contiguous; exp_avgs and
     exp_avg_sqs: fp32, same shapes.  `step` is the number of the step being
@@ -367,15 +421,354 @@ def adamw_batched(params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg
         workspace = ws[off:off + max(n, 1)]
     b1, b2 = (float(b) for b in betas)
     prm = AdamWParams(float(lr), b1, b2, float(eps), float(weight_decay), int(step))
+    fn, scale = lib.muon_adamw_batched, ()
+    if grad_scale is not None:
+        fn, scale = lib.muon_adamw_batched_scaled, (_scale_pointer(grad_scale, dev),)
     with torch.cuda.device(dev):
-        st = lib.muon_adamw_batched(len(ps), _i64_array(numels),
-                                    _ptr_array([t.data_ptr() for t in ps]),
-                                    _ptr_array([t.data_ptr() for t in gs]),
-                                    _ptr_array([t.data_ptr() for t in ms]),
-                                    _ptr_array([t.data_ptr() for t in vs]), code,
-                                    ctypes.byref(prm), ctypes.c_void_p(workspace.data_ptr()),
-                                    workspace.numel(), ctypes.c_void_p(_stream_handle(dev)))
-    _check(st, "muon_adamw_batched")
+        st = fn(len(ps), _i64_array(numels), _ptr_array([t.data_ptr() for t in ps]),
+                _ptr_array([t.data_ptr() for t in gs]), _ptr_array([t.data_ptr() for t in ms]),
+                _ptr_array([t.data_ptr() for t in vs]), code, ctypes.byref(prm), *scale,
+                ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+                ctypes.c_void_p(_stream_handle(dev)))
+    _check(st, fn.__name__)
+
+
+# ---------------------------------------------------------------------------
+# Gradient norm and clip
+# ---------------------------------------------------------------------------
+
+_NORM_KINDS = {2: 0, math.inf: 1}  # MUON_NORM_L2, MUON_NORM_MAX
+
+
+def _byte_workspace(nbytes: int, dev):
+    import torch
+
+    ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + nbytes] if off else ws[:nbytes]
+
+
+def _flat_tensors(ts, name, dev=None):
+    """(device, dtype codes, element counts, pointers) of contiguous bf16 / fp32 tensors."""
+    import torch
+
+    codes = {torch.bfloat16: MUON_BF16, torch.float32: MUON_FP32}
+    dev = ts[0].device if dev is None else dev
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: tensors must live on a HIP device, got {dev}")
+    got, numels, ptrs = [], [], []
+    for t in ts:
+        code = codes.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{name}: unsupported dtype {t.dtype}: use torch.bfloat16 or torch.float32")
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous on one device")
+        got.append(code)
+        numels.append(t.numel())
+        ptrs.append(t.data_ptr())
+    return dev, got, numels, ptrs
+
+
+def _i32_array(vals: Sequence[int]):
+    return (ctypes.c_int32 * max(1, len(vals)))(*vals)
+
+
+def grad_workspace_bytes(numels: Sequence[int]) -> int:
+    """Device workspace bytes of a gradient norm, scale or clip call."""
+    numels = list(numels)
+    n = load_library().muon_grad_workspace_bytes(len(numels), _i64_array(numels))
+    if n == SIZE_MAX:
+        raise MuonError(MUON_ERR_INVALID_ARG, "muon_grad_workspace_bytes", last_error_detail())
+    return int(n)
+
+
+def _norm_params(max_norm, norm_type, eps) -> GradNormParams:
+    kind = _NORM_KINDS.get(norm_type)
+    if kind is None:
+        raise ValueError(f"norm_type {norm_type!r}: use 2 or math.inf")
+    return GradNormParams(kind, 0 if max_norm is None else 1,
+                          0.0 if max_norm is None else float(max_norm), float(eps))
+
+
+def _norm_result(result, dev):
+    import torch
+
+    if result is None:
+        return torch.empty(2, dtype=torch.float32, device=dev)
+    if result.device != dev or result.dtype != torch.float32 or tuple(result.shape) != (2,) or \
+            not result.is_contiguous():
+        raise ValueError("result: a contiguous float32 tensor of 2 elements on the gradients' device")
+    return result
+
+
+def grad_norm_batched(grads: Sequence, max_norm: Optional[float] = None, norm_type: float = 2.0,
+                      eps: float = 1e-6, result=None, workspace=None):
+    """Global norm over a ragged batch of gradients, and the clip factor.
+
+    Returns a float32 tensor of 2 on the gradients' device (`result`, if given):
+    the norm (norm_type 2, or math.inf: the largest magnitude), and the factor
+    min(1, max_norm / (norm + eps)), 1 without max_norm.  grads: contiguous
+    bf16 and fp32 tensors, mixed as they come, on one device.  Runs on the
+    current HIP stream; nothing waits for the GPU.
+    """
+    import torch
+
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads: at least one tensor (its device holds the result)")
+    p = _norm_params(max_norm, norm_type, eps)
+    dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
+    result = _norm_result(result, dev)
+    if workspace is None:
+        workspace = _byte_workspace(grad_workspace_bytes(numels), dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.muon_grad_norm_batched(len(ptrs), _i64_array(numels), _ptr_array(ptrs),
+                                        _i32_array(codes), ctypes.byref(p),
+                                        ctypes.c_void_p(result.data_ptr()),
+                                        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+                                        ctypes.c_void_p(_stream_handle(dev)))
+    _check(st, "muon_grad_norm_batched")
+    return result
+
+
+def _grad_outputs(grads, out, dev, codes, numels, ptrs):
+    """(outputs, their dtype codes, their pointers)."""
+    if out is None:
+        return grads, codes, ptrs
+    out = list(out)
+    if len(out) != len(grads):
+        raise ValueError("out must have one tensor per gradient")
+    _, ocodes, onumels, optrs = _flat_tensors(out, "out", dev)
+    if onumels != numels:
+        raise ValueError("out must have the gradients' sizes")
+    return out, ocodes, optrs
+
+
+def grad_scale_batched(grads: Sequence, scale, out: Optional[Sequence] = None,
+                       workspace=None) -> List:
+    """out[i] = scale * grads[i]; scale: a one-element float32 tensor on their
+    device.  In place without `out`; out[i] may have the other dtype.  Returns
+    the outputs."""
+    import torch
+
+    grads = list(grads)
+    if not grads:
+        return []
+    dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
+    out, ocodes, optrs = _grad_outputs(grads, out, dev, codes, numels, ptrs)
+    factor = _scale_pointer(scale, dev)
+    if workspace is None:
+        workspace = _byte_workspace(grad_workspace_bytes(numels), dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.muon_grad_scale_batched(len(ptrs), _i64_array(numels), _ptr_array(ptrs),
+                                         _i32_array(codes), _ptr_array(optrs), _i32_array(ocodes),
+                                         factor, ctypes.c_void_p(workspace.data_ptr()),
+                                         workspace.numel(), ctypes.c_void_p(_stream_handle(dev)))
+    _check(st, "muon_grad_scale_batched")
+    return out
+
+
+def grad_clip_batched(grads: Sequence, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6,
+                      out: Optional[Sequence] = None, result=None, workspace=None):
+    """Clips a ragged batch of gradients by their global norm: in place, or into
+    `out` (whose tensors may have the other dtype: fp32 sums into bf16
+    gradients).  Returns the float32 tensor (norm, factor) of grad_norm_batched.
+    Nothing waits for the GPU."""
+    import torch
+
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads: at least one tensor (its device holds the result)")
+    if max_norm is None:
+        raise ValueError("max_norm is needed")
+    p = _norm_params(max_norm, norm_type, eps)
+    dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
+    _, ocodes, optrs = _grad_outputs(grads, out, dev, codes, numels, ptrs)
+    result = _norm_result(result, dev)
+    if workspace is None:
+        workspace = _byte_workspace(grad_workspace_bytes(numels), dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.muon_grad_clip_batched(len(ptrs), _i64_array(numels), _ptr_array(ptrs),
+                                        _i32_array(codes), _ptr_array(optrs), _i32_array(ocodes),
+                                        ctypes.byref(p), ctypes.c_void_p(result.data_ptr()),
+                                        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+                                        ctypes.c_void_p(_stream_handle(dev)))
+    _check(st, "muon_grad_clip_batched")
+    return result
+
+
+# ---------------------------------------------------------------------------
+# Block-scaled e4m3 operands and their product
+# ---------------------------------------------------------------------------
+
+F8_BLOCK = 128
+F8_MAX_DIM = 1 << 20
+
+
+class F8Operand(NamedTuple):
+    """An operand of f8_matmul_batched: R rows, contracted over Kp columns (a
+    multiple of F8_BLOCK).  q: float8_e4m3fn, R x Kp; scales: uint8,
+    Kp/128 x Rp (Rp: R up to a multiple of 16), byte [kb][r] = e + 127 for the
+    power of two 2^e of columns 128 kb .. 128 kb + 127 of row r.  Columns and
+    scale entries past the matrix are zero."""
+
+    q: object
+    scales: object
+
+
+def f8_empty(rows: int, cols: int, device) -> F8Operand:
+    """Room for the operand of a rows x cols matrix (contracted over cols)."""
+    import torch
+
+    kp, rp = -(-cols // F8_BLOCK) * F8_BLOCK, -(-rows // 16) * 16
+    return F8Operand(torch.empty((rows, kp), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn),
+                     torch.empty((kp // F8_BLOCK, rp), dtype=torch.uint8, device=device))
+
+
+def _f8_pointers(ops, name, dev, shapes=None):
+    """(shapes, value pointers, scale pointers) of operands; shapes: what they must be."""
+    import torch
+
+    got, qs, ss = [], [], []
+    for i, (q, s) in enumerate(ops):
+        if q.dtype != torch.float8_e4m3fn or s.dtype != torch.uint8:
+            raise TypeError(f"{name}: an operand is a float8_e4m3fn tensor and a uint8 tensor")
+        if q.device != dev or s.device != dev or not q.is_contiguous() or not s.is_contiguous() \
+                or q.dim() != 2 or s.dim() != 2:
+            raise ValueError(f"{name}: operands must be contiguous 2-D tensors on one HIP device")
+        r, kp = q.shape
+        if kp % F8_BLOCK or tuple(s.shape) != (kp // F8_BLOCK, -(-r // 16) * 16):
+            raise ValueError(f"{name}: operand {i} has values {tuple(q.shape)} and scales "
+                             f"{tuple(s.shape)}: want (R, Kp) with Kp a multiple of {F8_BLOCK}, and "
+                             "(Kp / 128, R up to a multiple of 16)")
+        if shapes is not None and (r, kp) != shapes[i]:
+            raise ValueError(f"{name}: operand {i} has values {(r, kp)}, want {shapes[i]}")
+        got.append((r, kp))
+        qs.append(q.data_ptr())
+        ss.append(s.data_ptr())
+    return got, qs, ss
+
+
+def f8_workspace_bytes(batch: int) -> int:
+    """Device workspace bytes of an f8_quantize_batched or f8_matmul_batched call."""
+    n = load_library().muon_f8_workspace_bytes(int(batch))
+    if n == SIZE_MAX:
+        raise MuonError(MUON_ERR_INVALID_ARG, "muon_f8_workspace_bytes", last_error_detail())
+    return int(n)
+
+
+def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
+                        transpose: bool = False, out: Optional[Sequence] = None,
+                        out_t: Optional[Sequence] = None, workspace=None):
+    """Block-scaled e4m3 operands of a ragged batch of matrices.
+
+    xs: contiguous 2-D bf16 or fp32 tensors (one dtype).  normal: the operands
+    of the matrices (contracted over their columns); transpose: those of their
+    transposes (contracted over their rows); both come from one read.
+    block_rows: 1 for a scale per 1 x 128 block along the contracted side
+    (activations, gradients), 128 for one per 128 x 128 block (weights).
+    Returns the operands, the transposes' operands, or a pair of both lists, in
+    `out` and `out_t` where given.
+    """
+    import torch
+
+    xs = list(xs)
+    if not normal and not transpose:
+        raise ValueError("one of normal and transpose must be set")
+    if (out is not None and not normal) or (out_t is not None and not transpose):
+        raise ValueError("out goes with normal, out_t with transpose")
+    if not xs:
+        return ([], []) if normal and transpose else []
+    dev = _check_tensors(xs, "xs")
+    code = _dtype_code(xs[0].dtype)
+    shapes = [tuple(x.shape) for x in xs]
+
+    def side(wanted, given, name, dims):
+        if not wanted:
+            return None, None, None
+        ops = [f8_empty(r, k, dev) for r, k in dims] if given is None else list(given)
+        if len(ops) != len(xs):
+            raise ValueError(f"{name} must have one operand per matrix")
+        _, q, s = _f8_pointers(ops, name, dev, [(r, -(-k // F8_BLOCK) * F8_BLOCK) for r, k in dims])
+        return ops, _ptr_array(q), _ptr_array(s)
+
+    ops, q, s = side(normal, out, "out", shapes)
+    ops_t, qt, st_ = side(transpose, out_t, "out_t", [(c, r) for r, c in shapes])
+    if workspace is None:
+        workspace = _byte_workspace(f8_workspace_bytes(len(xs)), dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.muon_f8_quantize_batched(len(xs), _i64_array([r for r, _ in shapes]),
+                                          _i64_array([c for _, c in shapes]),
+                                          _ptr_array([x.data_ptr() for x in xs]), code,
+                                          int(block_rows), q, s, qt, st_,
+                                          ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+                                          ctypes.c_void_p(_stream_handle(dev)))
+    _check(st, "muon_f8_quantize_batched")
+    return (ops, ops_t) if normal and transpose else ops if normal else ops_t
+
+
+def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, out_dtype=None,
+                      accumulate: bool = False, workspace=None) -> List:
+    """out[i] = A_i B_i^T over block-scaled e4m3 operands, ragged over the batch.
+
+    a, b: sequences of F8Operand (or (values, scales) pairs) with equal
+    contracted sides.  out: contiguous bf16 or fp32 tensors of (A's rows, B's
+    rows); without it new ones of out_dtype (bfloat16).  accumulate: the
+    products are added to `out`.  Sums are fp32, rounded once.  For
+    Y = X W^T: dX = dY W takes the operands of dY and W^T, and dW = dY^T X those
+    of dY^T and X^T (f8_quantize_batched's transpose).  Returns the outputs.
+    """
+    import torch
+
+    a, b = list(a), list(b)
+    if len(a) != len(b):
+        raise ValueError("a and b must have the same length")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if not a:
+        return [] if out is None else list(out)
+    dev = a[0][0].device
+    if dev.type != "cuda":
+        raise ValueError(f"a: operands must live on a HIP device, got {dev}")
+    ash, aq, asc = _f8_pointers(a, "a", dev)
+    bsh, bq, bsc = _f8_pointers(b, "b", dev)
+    for i, (x, y) in enumerate(zip(ash, bsh)):
+        if x[1] != y[1]:
+            raise ValueError(f"product {i}: contracted sides {x[1]} and {y[1]} differ")
+    shapes = [(x[0], y[0]) for x, y in zip(ash, bsh)]
+    if out is None:
+        dt = torch.bfloat16 if out_dtype is None else out_dtype
+        _dtype_code(dt)
+        out = [torch.empty(s, dtype=dt, device=dev) for s in shapes]
+    else:
+        out = list(out)
+        if len(out) != len(a):
+            raise ValueError("out must have one tensor per product")
+        if out_dtype is not None and any(o.dtype != out_dtype for o in out):
+            raise ValueError("out has another dtype than out_dtype")
+    if _check_tensors(out, "out") != dev:
+        raise ValueError("out must live on the operands' device")
+    if any(tuple(o.shape) != s for o, s in zip(out, shapes)):
+        raise ValueError("out must have the shape (rows of a, rows of b)")
+    code = _dtype_code(out[0].dtype)
+    if workspace is None:
+        workspace = _byte_workspace(f8_workspace_bytes(len(a)), dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.muon_f8_matmul_batched(len(a), _i64_array([s[0] for s in shapes]),
+                                        _i64_array([s[1] for s in shapes]),
+                                        _i64_array([s[1] for s in ash]), _ptr_array(aq),
+                                        _ptr_array(asc), _ptr_array(bq), _ptr_array(bsc),
+                                        _ptr_array([o.data_ptr() for o in out]), code,
+                                        1 if accumulate else 0,
+                                        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+                                        ctypes.c_void_p(_stream_handle(dev)))
+    _check(st, "muon_f8_matmul_batched")
+    return out
 
 
 def hbm_stream(ins: Sequence, outs: Sequence, nontemporal: bool = False) -> None:

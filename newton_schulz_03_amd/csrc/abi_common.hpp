@@ -1,0 +1,32 @@
+// Host helpers shared by the C ABI's translation units (muon_abi.hip defines
+// them): the error detail of a thread, alignment, per-kernel timing.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace muon {
+
+// Records the detail string of this thread's last error; returns `status`.
+int32_t fail(int32_t status, const char* fmt, ...);
+int32_t hip_fail(hipError_t e, const char* what);
+void clear_detail();
+
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Null, too small or misaligned workspaces, as every entry point reports them.
+int32_t check_workspace(const void* ws, size_t ws_bytes, size_t need);
+
+// Brackets one launch with timing events when timing is enabled (and allowed:
+// the allocation-free entry point never creates events).
+struct TimedLaunch {
+  int kernel;
+  hipStream_t stream;
+  hipEvent_t start = nullptr, stop = nullptr;
+  TimedLaunch(int k, hipStream_t s, bool allowed = true);
+  void done();
+};
+
+}  // namespace muon

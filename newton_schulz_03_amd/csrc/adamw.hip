@@ -6,6 +6,8 @@
 //   m <- beta1 * m + (1 - beta1) * g
 //   v <- beta2 * v + (1 - beta2) * g^2
 //   p <- p - (lr / (1 - beta1^t)) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+// SCALED: g is first multiplied by a factor in device memory (the clip factor
+// of the global norm), so that clipping costs no pass of its own.
 // Bandwidth-bound: each block reads its whole span (p, g, m, v) before the
 // first store.  Blocks find their tensor through the prefix table in one round
 // of loads, as the other elementwise kernels do.
@@ -47,9 +49,10 @@ __device__ __forceinline__ void adamw_update(const AdamParams& a, float& p, floa
   p -= a.step_size * (m / denom);
 }
 
-template <typename T>
+template <typename T, bool SCALED>
 __global__ __launch_bounds__(kThreads) void k_adamw(AdamCtx c, AdamParams a) {
   __shared__ int slot;
+  const float gs = SCALED ? *a.g_scale : 1.f;
   constexpr int64_t kSpan = static_cast<int64_t>(kThreads) * kAdamVec * kAdamIters;
   const int32_t b = blockIdx.x;
   const int j = __builtin_amdgcn_readfirstlane(locate_matrix(c.prefix, c.batch, b, &slot));
@@ -75,7 +78,8 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamCtx c, AdamParams a) {
     for (int it = 0; it < kAdamIters; ++it) {
       const int64_t off = (static_cast<int64_t>(it) * kThreads + threadIdx.x) * kAdamVec;
 #pragma unroll
-      for (int e = 0; e < kAdamVec; ++e) adamw_update(a, p[it][e], g[it][e], m[it][e], v[it][e]);
+      for (int e = 0; e < kAdamVec; ++e)
+        adamw_update(a, p[it][e], SCALED ? gs * g[it][e] : g[it][e], m[it][e], v[it][e]);
       store8<T>(pp + off, p[it]);
       store8<float>(mp + off, m[it]);
       store8<float>(vp + off, v[it]);
@@ -86,7 +90,8 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamCtx c, AdamParams a) {
     for (int64_t i = threadIdx.x; i < n; i += kThreads) {
       float p = Elt<T>::to_f32(pp[i]);
       float m = mp[i], v = vp[i];
-      adamw_update(a, p, Elt<T>::to_f32(gp[i]), m, v);
+      const float g = Elt<T>::to_f32(gp[i]);
+      adamw_update(a, p, SCALED ? gs * g : g, m, v);
       pp[i] = Elt<T>::from_f32(p);
       mp[i] = m;
       vp[i] = v;
@@ -101,13 +106,22 @@ int64_t adamw_blocks(int64_t numel) {
   return (numel + span - 1) / span;
 }
 
+namespace {
+
+template <typename T, bool SCALED>
+hipError_t run_adamw(const AdamCtx& c, int32_t nblocks, const AdamParams& a) {
+  hipLaunchKernelGGL((k_adamw<T, SCALED>), dim3(nblocks), dim3(kThreads), 0, c.stream, c, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_adamw(const AdamCtx& c, int32_t nblocks, bool is_bf16, const AdamParams& a) {
   if (nblocks <= 0) return hipSuccess;
+  const bool scaled = a.g_scale != nullptr;
   if (is_bf16)
-    hipLaunchKernelGGL(k_adamw<uint16_t>, dim3(nblocks), dim3(kThreads), 0, c.stream, c, a);
-  else
-    hipLaunchKernelGGL(k_adamw<float>, dim3(nblocks), dim3(kThreads), 0, c.stream, c, a);
-  return hipGetLastError();
+    return scaled ? run_adamw<uint16_t, true>(c, nblocks, a) : run_adamw<uint16_t, false>(c, nblocks, a);
+  return scaled ? run_adamw<float, true>(c, nblocks, a) : run_adamw<float, false>(c, nblocks, a);
 }
 
 }  // namespace muon

@@ -19,8 +19,9 @@ namespace muon {
 namespace {
 
 // One 16-byte vector (V elements) of the user's matrix: the loads, then M', U
-// and the momentum store.
-template <typename T>
+// and the momentum store.  SCALED (the step): G is multiplied by gs in fp32 as
+// it is read.
+template <typename T, bool SCALED>
 struct UVec {
   static constexpr int V = Elt<T>::kVec;
   u32x4_t a, m;  // G (or x) and M
@@ -38,7 +39,7 @@ struct UVec {
 
   // u <- U over the vector (zeros outside the matrix); stores M' (step).  U is
   // formed from the stored, rounded M', as the oracle's bf16 reading has it.
-  __device__ __forceinline__ void finish(const MatDesc& d, const ElemParams& p, int64_t r,
+  __device__ __forceinline__ void finish(const MatDesc& d, const ElemParams& p, float gs, int64_t r,
                                          int64_t c0, float* u) const {
     if (full) {
       if (p.mode == MODE_NS) {
@@ -48,6 +49,10 @@ struct UVec {
       float g[V], mo[V], mn[V];
       vec_to_f32<T>(a, g);
       vec_to_f32<T>(m, mo);
+      if constexpr (SCALED) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[e] *= gs;
+      }
 #pragma unroll
       for (int e = 0; e < V; ++e) mn[e] = p.beta * mo[e] + g[e];
       const u32x4_t packed = f32_to_vec<T>(mn);
@@ -68,7 +73,8 @@ struct UVec {
     T* mom = static_cast<T*>(d.mom) + off;
 #pragma unroll 1
     for (int e = 0; e < V && c0 + e < d.cols; ++e) {
-      const float g = Elt<T>::to_f32(src[c0 + e]);
+      float g = Elt<T>::to_f32(src[c0 + e]);
+      if constexpr (SCALED) g *= gs;
       if (p.mode == MODE_NS) {
         u[e] = g;
         continue;
@@ -100,11 +106,11 @@ namespace {
 // Loads, momentum and U for the tile's kVecs vectors per thread; returns the
 // thread's sum of squares.  The tile is read as rows of vpr vectors starting
 // at the user's (r0, c0).
-template <typename T, int kVecs>
-__device__ __forceinline__ float prepare_vectors(const MatDesc& d, const ElemParams& p, int64_t r0,
-                                                 int64_t c0, int vpr, u32x4_t* up) {
+template <typename T, int kVecs, bool SCALED>
+__device__ __forceinline__ float prepare_vectors(const MatDesc& d, const ElemParams& p, float gs,
+                                                 int64_t r0, int64_t c0, int vpr, u32x4_t* up) {
   constexpr int V = Elt<T>::kVec;
-  UVec<T> uv[kVecs];
+  UVec<T, SCALED> uv[kVecs];
 #pragma unroll
   for (int it = 0; it < kVecs; ++it) {
     const int v = it * kThreads + threadIdx.x;
@@ -115,7 +121,7 @@ __device__ __forceinline__ float prepare_vectors(const MatDesc& d, const ElemPar
   for (int it = 0; it < kVecs; ++it) {
     const int v = it * kThreads + threadIdx.x;
     float u[V];
-    uv[it].finish(d, p, r0 + v / vpr, c0 + (v % vpr) * V, u);
+    uv[it].finish(d, p, gs, r0 + v / vpr, c0 + (v % vpr) * V, u);
 #pragma unroll
     for (int e = 0; e < V; ++e) acc += u[e] * u[e];
     up[it] = f32_to_vec<T>(u);
@@ -180,7 +186,7 @@ __device__ __forceinline__ void transpose_tall_bf16(char* lds, const u32x4_t* up
 
 }  // namespace
 
-template <typename T>
+template <typename T, bool SCALED>
 __global__ __launch_bounds__(kThreads) void k_prepare(LaunchCtx c, ElemParams p) {
   constexpr int V = Elt<T>::kVec;
   constexpr int kTallRows = kPrepTallL, kTallCols = kPrepTallS;  // the user's tile of a tall matrix
@@ -197,6 +203,7 @@ __global__ __launch_bounds__(kThreads) void k_prepare(LaunchCtx c, ElemParams p)
   const MatDesc& d = c.desc[j];
   const int32_t t = per > 0 ? b - j * per : b - pre[j];
   T* xu = static_cast<T*>(iterate(d, 0));  // the first iterate buffer, holding U
+  const float gs = SCALED ? *p.g_scale : 1.f;
   float acc;
   if (!d.tall) {
     // the user's rows are the iterate's: read and write the same vectors
@@ -205,7 +212,7 @@ __global__ __launch_bounds__(kThreads) void k_prepare(LaunchCtx c, ElemParams p)
     const int64_t j0 = static_cast<int64_t>(t % tpr) * kWideTileCols;
     constexpr int vpr = kWideTileCols / V;
     u32x4_t up[kVecsWide];
-    acc = prepare_vectors<T, kVecsWide>(d, p, i0, j0, vpr, up);
+    acc = prepare_vectors<T, kVecsWide, SCALED>(d, p, gs, i0, j0, vpr, up);
     // V consecutive columns starting at a multiple of V stay inside one slab row,
     // and the tile's rows inside one band.
     // Nontemporal: U is far larger than the caches, and the first Gram reads it
@@ -228,7 +235,7 @@ __global__ __launch_bounds__(kThreads) void k_prepare(LaunchCtx c, ElemParams p)
       u32x4_t v;
       T e[V];
     } up[kVecsTall];
-    acc = prepare_vectors<T, kVecsTall>(d, p, j0, i0, vpr, &up[0].v);
+    acc = prepare_vectors<T, kVecsTall, SCALED>(d, p, gs, j0, i0, vpr, &up[0].v);
     if constexpr (sizeof(T) == 2) {
       transpose_tall_bf16(reinterpret_cast<char*>(&tile[0][0]), &up[0].v, xu, i0, j0, d.l_pad);
       const float total = block_sum(acc, scratch);
@@ -374,13 +381,22 @@ __global__ __launch_bounds__(kThreads) void k_finish(LaunchCtx c, ElemParams p) 
 // ---------------------------------------------------------------------------
 // Launchers.
 // ---------------------------------------------------------------------------
+namespace {
+
+template <typename T, bool SCALED>
+hipError_t run_prepare(const LaunchCtx& c, int32_t nblocks, const ElemParams& p) {
+  hipLaunchKernelGGL((k_prepare<T, SCALED>), dim3(nblocks), dim3(kThreads), 0, c.stream, c, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_prepare(const LaunchCtx& c, int32_t nblocks, bool is_bf16, const ElemParams& p) {
   if (nblocks <= 0) return hipSuccess;
+  const bool scaled = p.g_scale != nullptr;
   if (is_bf16)
-    hipLaunchKernelGGL(k_prepare<uint16_t>, dim3(nblocks), dim3(kThreads), 0, c.stream, c, p);
-  else
-    hipLaunchKernelGGL(k_prepare<float>, dim3(nblocks), dim3(kThreads), 0, c.stream, c, p);
-  return hipGetLastError();
+    return scaled ? run_prepare<uint16_t, true>(c, nblocks, p) : run_prepare<uint16_t, false>(c, nblocks, p);
+  return scaled ? run_prepare<float, true>(c, nblocks, p) : run_prepare<float, false>(c, nblocks, p);
 }
 
 hipError_t launch_finalize(const LaunchCtx& c, const ElemParams& p) {

@@ -12,6 +12,7 @@
 #include <utility>
 #include <vector>
 
+#include "abi_common.hpp"
 #include "gemm_common.hpp"
 #include "muon_internal.hpp"
 #include "muon_mi355x.h"
@@ -20,6 +21,8 @@ namespace muon {
 namespace {
 
 thread_local std::string g_detail;
+
+}  // namespace
 
 int32_t fail(int32_t status, const char* fmt, ...) {
   char buf[512];
@@ -31,7 +34,23 @@ int32_t fail(int32_t status, const char* fmt, ...) {
   return status;
 }
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+int32_t hip_fail(hipError_t e, const char* what) {
+  return fail(MUON_ERR_HIP, "%s: %s (%s)", what, hipGetErrorName(e), hipGetErrorString(e));
+}
+
+void clear_detail() { g_detail.clear(); }
+
+int32_t check_workspace(const void* ws, size_t ws_bytes, size_t need) {
+  if (ws == nullptr || ws_bytes < need)
+    return fail(MUON_ERR_WORKSPACE, "workspace of %zu bytes at %p; %zu bytes needed", ws_bytes, ws,
+                need);
+  if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0)
+    return fail(MUON_ERR_INVALID_ARG, "workspace pointer %p is not 256-byte aligned", ws);
+  return MUON_OK;
+}
+
+namespace {
+
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
@@ -273,10 +292,6 @@ struct Pool {
 std::mutex g_pool_mu;
 std::map<int, Pool> g_pools;
 
-int32_t hip_fail(hipError_t e, const char* what) {
-  return fail(MUON_ERR_HIP, "%s: %s (%s)", what, hipGetErrorName(e), hipGetErrorString(e));
-}
-
 // A slot of `pool` whose previous copy (if any) has completed; index in *idx.
 int32_t free_slot(Pool& pool, size_t* idx) {
   const size_t n = pool.slot.size();
@@ -438,27 +453,25 @@ hipEvent_t take_event() {
   return e;
 }
 
-// Brackets one launch with timing events when timing is enabled (and allowed:
-// the allocation-free entry point never creates events).
-struct TimedLaunch {
-  int kernel;
-  hipStream_t stream;
-  hipEvent_t start = nullptr, stop = nullptr;
-  TimedLaunch(int k, hipStream_t s, bool allowed = true) : kernel(k), stream(s) {
-    if (!allowed) return;
-    std::lock_guard<std::mutex> lock(g_timing_mu);
-    if (!g_timing_on) return;
-    start = take_event();
-    stop = take_event();
-    if (start && stop) (void)hipEventRecord(start, stream);
-  }
-  void done() {
-    if (!start || !stop) return;
-    (void)hipEventRecord(stop, stream);
-    std::lock_guard<std::mutex> lock(g_timing_mu);
-    g_pending.push_back({kernel, start, stop});
-  }
-};
+}  // namespace
+
+TimedLaunch::TimedLaunch(int k, hipStream_t s, bool allowed) : kernel(k), stream(s) {
+  if (!allowed) return;
+  std::lock_guard<std::mutex> lock(g_timing_mu);
+  if (!g_timing_on) return;
+  start = take_event();
+  stop = take_event();
+  if (start && stop) (void)hipEventRecord(start, stream);
+}
+
+void TimedLaunch::done() {
+  if (!start || !stop) return;
+  (void)hipEventRecord(stop, stream);
+  std::lock_guard<std::mutex> lock(g_timing_mu);
+  g_pending.push_back({kernel, start, stop});
+}
+
+namespace {
 
 int32_t drain_timing() {
   for (const TimingRec& r : g_pending) {
@@ -475,8 +488,6 @@ int32_t drain_timing() {
   g_pending.clear();
   return MUON_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int32_t check_ns_params(const muon_ns_params* p, int32_t dtype) {
   if (p == nullptr) return fail(MUON_ERR_INVALID_ARG, "params pointer is null");
@@ -501,12 +512,7 @@ int32_t check_ns_params(const muon_ns_params* p, int32_t dtype) {
 }
 
 int32_t check_ws(const Plan& pl, void* ws, size_t ws_bytes) {
-  if (ws == nullptr || ws_bytes < pl.total_bytes)
-    return fail(MUON_ERR_WORKSPACE, "workspace of %zu bytes at %p; %zu bytes needed", ws_bytes, ws,
-                pl.total_bytes);
-  if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0)
-    return fail(MUON_ERR_INVALID_ARG, "workspace pointer %p is not 256-byte aligned", ws);
-  return MUON_OK;
+  return check_workspace(ws, ws_bytes, pl.total_bytes);
 }
 
 // Enqueue the whole step after the table is in place.
@@ -948,10 +954,14 @@ extern "C" int32_t muon_ns_batched_noalloc(int32_t batch, const int64_t* rows, c
   }
 }
 
-extern "C" int32_t muon_step_batched(int32_t batch, const int64_t* rows, const int64_t* cols,
-                                     void* const* w, const void* const* g, void* const* m,
-                                     int32_t dtype, const muon_step_params* p, void* workspace,
-                                     size_t workspace_bytes, void* stream) {
+namespace muon {
+namespace {
+
+// The step; g_scale: device factor of the gradients, or null.
+int32_t step_batched(int32_t batch, const int64_t* rows, const int64_t* cols, void* const* w,
+                     const void* const* g, void* const* m, int32_t dtype,
+                     const muon_step_params* p, const float* g_scale, void* workspace,
+                     size_t workspace_bytes, void* stream) {
   try {
     g_detail.clear();
     Plan pl;
@@ -982,6 +992,7 @@ extern "C" int32_t muon_step_batched(int32_t batch, const int64_t* rows, const i
     ep.beta = p->beta;
     ep.eps = p->ns.eps;
     ep.lr = p->lr;
+    ep.g_scale = g_scale;
     char* ws = static_cast<char*>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (p->momentum_host) {
@@ -1017,6 +1028,37 @@ extern "C" int32_t muon_step_batched(int32_t batch, const int64_t* rows, const i
   }
 }
 
+int32_t check_scale(const float* g_scale) {
+  if (g_scale == nullptr) return fail(MUON_ERR_INVALID_ARG, "grad_scale pointer is null");
+  if ((reinterpret_cast<uintptr_t>(g_scale) & 3u) != 0)
+    return fail(MUON_ERR_INVALID_ARG, "grad_scale pointer not 4-byte aligned");
+  return MUON_OK;
+}
+
+}  // namespace
+}  // namespace muon
+
+extern "C" int32_t muon_step_batched(int32_t batch, const int64_t* rows, const int64_t* cols,
+                                     void* const* w, const void* const* g, void* const* m,
+                                     int32_t dtype, const muon_step_params* p, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  return step_batched(batch, rows, cols, w, g, m, dtype, p, nullptr, workspace, workspace_bytes,
+                      stream);
+}
+
+extern "C" int32_t muon_step_batched_scaled(int32_t batch, const int64_t* rows,
+                                            const int64_t* cols, void* const* w,
+                                            const void* const* g, void* const* m, int32_t dtype,
+                                            const muon_step_params* p, const float* grad_scale,
+                                            void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+  clear_detail();
+  const int32_t st = check_scale(grad_scale);
+  if (st != MUON_OK) return st;
+  return step_batched(batch, rows, cols, w, g, m, dtype, p, grad_scale, workspace, workspace_bytes,
+                      stream);
+}
+
 extern "C" size_t muon_adamw_workspace_bytes(int32_t batch, const int64_t* numel) {
   g_detail.clear();
   AdamPlan pl;
@@ -1024,10 +1066,14 @@ extern "C" size_t muon_adamw_workspace_bytes(int32_t batch, const int64_t* numel
   return pl.total_bytes;
 }
 
-extern "C" int32_t muon_adamw_batched(int32_t batch, const int64_t* numel, void* const* p,
-                                      const void* const* g, float* const* m, float* const* v,
-                                      int32_t dtype, const muon_adamw_params* prm,
-                                      void* workspace, size_t workspace_bytes, void* stream) {
+namespace muon {
+namespace {
+
+// The AdamW step; g_scale: device factor of the gradients, or null.
+int32_t adamw_batched(int32_t batch, const int64_t* numel, void* const* p, const void* const* g,
+                      float* const* m, float* const* v, int32_t dtype,
+                      const muon_adamw_params* prm, const float* g_scale, void* workspace,
+                      size_t workspace_bytes, void* stream) {
   try {
     g_detail.clear();
     AdamPlan pl;
@@ -1089,6 +1135,7 @@ extern "C" int32_t muon_adamw_batched(int32_t batch, const int64_t* numel, void*
     a.step_size = static_cast<float>(prm->lr / bc1);
     a.inv_bc2_sqrt = static_cast<float>(1.0 / std::sqrt(bc2));
     a.eps = prm->eps;
+    a.g_scale = g_scale;
     AdamCtx c{};
     c.desc = reinterpret_cast<const AdamDesc*>(ws);
     c.prefix = reinterpret_cast<const int32_t*>(ws + pl.prefix_off);
@@ -1102,6 +1149,30 @@ extern "C" int32_t muon_adamw_batched(int32_t batch, const int64_t* numel, void*
   } catch (...) {
     return fail(MUON_ERR_HIP, "unexpected host exception");
   }
+}
+
+}  // namespace
+}  // namespace muon
+
+extern "C" int32_t muon_adamw_batched(int32_t batch, const int64_t* numel, void* const* p,
+                                      const void* const* g, float* const* m, float* const* v,
+                                      int32_t dtype, const muon_adamw_params* params,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  return adamw_batched(batch, numel, p, g, m, v, dtype, params, nullptr, workspace,
+                       workspace_bytes, stream);
+}
+
+extern "C" int32_t muon_adamw_batched_scaled(int32_t batch, const int64_t* numel, void* const* p,
+                                             const void* const* g, float* const* m,
+                                             float* const* v, int32_t dtype,
+                                             const muon_adamw_params* params,
+                                             const float* grad_scale, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  clear_detail();
+  const int32_t st = check_scale(grad_scale);
+  if (st != MUON_OK) return st;
+  return adamw_batched(batch, numel, p, g, m, v, dtype, params, grad_scale, workspace,
+                       workspace_bytes, stream);
 }
 
 extern "C" const char* muon_status_string(int32_t status) {

@@ -124,6 +124,7 @@ struct ElemParams {
   float lr;
   int32_t cur;       // which X buffer holds the final iterate (finish)
   int32_t scale_x;   // finish: the iterate is still U (no iterations): scale by the norm factor
+  const float* g_scale;  // step: device factor of the gradients (prepare), or null
 };
 
 // Bytes of one e4m3 buffer of a matrix (s_pad * l_pad values and a scale byte
@@ -161,10 +162,89 @@ struct AdamParams {
   float step_size;        // lr / (1 - beta1^t)
   float inv_bc2_sqrt;     // 1 / sqrt(1 - beta2^t)
   float eps;
+  const float* g_scale;   // device: the factor of the gradients, or null
 };
 
 int64_t adamw_blocks(int64_t numel);
 hipError_t launch_adamw(const AdamCtx& c, int32_t nblocks, bool is_bf16, const AdamParams& a);
+
+// Global gradient norm, clip factor and scaled gradients over a ragged batch.
+// Every tensor is cut into chunks of kGradSpan elements, numbered through the
+// batch by the prefix table.
+constexpr int64_t kGradSpan = 16384;
+constexpr int32_t kNormBlocks = 2048;  // most blocks (and partials) of the norm pass
+struct GradDesc {
+  const void* g;
+  void* out;
+  int64_t numel;
+  int32_t in_bf16, out_bf16;  // element types: bf16 or fp32
+};
+struct GradCtx {
+  const GradDesc* desc;    // device copy of the descriptors
+  const int32_t* prefix;   // device: batch+1 chunk prefixes
+  int32_t batch;
+};
+// Up to kGradInline tensors travel as kernel arguments: no table to write first.
+constexpr int kGradInline = 32;
+struct GradInline {
+  GradDesc desc[kGradInline];
+  int32_t prefix[kGradInline + 1];
+  int32_t batch;
+};
+struct GradTable {
+  bool in_args;
+  GradCtx mem;
+  GradInline args;
+};
+struct GradNormArgs {
+  float* result;     // device: norm, clip factor
+  void* partials;    // device: 8 bytes per block of the norm pass
+  int32_t chunks;
+  int32_t clip;      // 0: the factor is 1
+  float max_norm, eps;
+};
+// kind 0: L2, 1: largest magnitude.
+hipError_t launch_grad_norm(const GradTable& t, const GradNormArgs& p, int32_t kind, hipStream_t s);
+hipError_t launch_grad_scale(const GradTable& t, int32_t chunks, const float* scale, hipStream_t s);
+
+// Block-scaled e4m3 operands for products outside the step.  An operand of
+// R rows contracted over K columns: values R x Kp bytes (Kp = K up to a
+// multiple of 128, zeros there), row-major, and scale bytes Kp/128 x Rp (Rp =
+// R up to a multiple of 16, zeros there): byte [kb][r] scales columns 128 kb ..
+// 128 kb + 127 of row r by 2^(byte - 127).
+constexpr int kF8Block = 128;
+struct F8QuantDesc {
+  const void* x;           // rows x cols, T
+  uint8_t *q, *s;          // operand of x, or null
+  uint8_t *qt, *st;        // operand of x^T, or null
+  int32_t rows, cols;
+};
+struct F8QuantCtx {
+  const F8QuantDesc* desc;
+  const int32_t* prefix;   // device: batch+1 block prefixes
+  int32_t batch;
+  hipStream_t stream;
+};
+hipError_t launch_f8_quantize(const F8QuantCtx& c, int32_t nblocks, bool is_bf16,
+                              int32_t block_rows);
+
+// C = A B^T (+ C) over such operands.
+struct F8ProdDesc {
+  const uint8_t *a, *sa;   // m rows
+  const uint8_t *b, *sb;   // n rows
+  void* c;                 // m x n, bf16 or fp32
+  int32_t m, n, kp;        // kp: the operands' padded K
+  int32_t reserved;
+};
+struct F8ProdCtx {
+  const F8ProdDesc* desc;
+  const int32_t* prefix;   // device: batch+1 tile prefixes
+  int32_t batch;
+  int32_t accumulate;
+  hipStream_t stream;
+};
+hipError_t launch_f8_prod(const F8ProdCtx& c, int32_t ntiles, bool is_bf16);
+constexpr int kF8Tile = 256;  // output tile (both sides)
 
 // Host launchers (one per kernel family).  is_bf16 selects the element type.
 // Momentum (step), U into X ping and the per-block sums of U^2.

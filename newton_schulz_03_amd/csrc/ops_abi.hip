@@ -1,0 +1,432 @@
+// C ABI of the operators around the step: the gradient norm and clip, the
+// block-scaled e4m3 operands and their product.  Descriptor tables travel as
+// kernel arguments, so a call enqueues kernel launches only and can be captured
+// into a graph.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <vector>
+
+#include "abi_common.hpp"
+#include "muon_internal.hpp"
+#include "muon_mi355x.h"
+
+namespace muon {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clip
+// ---------------------------------------------------------------------------
+struct GradPlan {
+  std::vector<GradDesc> desc;
+  std::vector<int32_t> prefix;
+  size_t prefix_off = 0, partials_off = 0, total_bytes = 0;
+  int32_t chunks = 0;
+};
+
+int32_t make_grad_plan(int32_t batch, const int64_t* numel, GradPlan& pl) {
+  if (batch < 0) return fail(MUON_ERR_INVALID_ARG, "batch = %d is negative", batch);
+  if (batch > 0 && numel == nullptr) return fail(MUON_ERR_INVALID_ARG, "numel array is null");
+  pl.desc.assign(batch, GradDesc{});
+  pl.prefix.assign(static_cast<size_t>(batch) + 1, 0);
+  int64_t total = 0;
+  for (int32_t i = 0; i < batch; ++i) {
+    if (numel[i] < 0)
+      return fail(MUON_ERR_INVALID_ARG, "tensor %d: numel %lld is negative", i,
+                  static_cast<long long>(numel[i]));
+    pl.desc[i].numel = numel[i];
+    if (numel[i] / kGradSpan > INT32_MAX - total - 1)
+      return fail(MUON_ERR_UNSUPPORTED, "batch needs more than 2^31 blocks");
+    total += (numel[i] + kGradSpan - 1) / kGradSpan;
+    pl.prefix[i + 1] = static_cast<int32_t>(total);
+  }
+  pl.chunks = static_cast<int32_t>(total);
+  pl.prefix_off = align_up(sizeof(GradDesc) * batch, kAlign);
+  pl.partials_off = pl.prefix_off + align_up(sizeof(int32_t) * (static_cast<size_t>(batch) + 1), kAlign);
+  pl.total_bytes = pl.partials_off + align_up(8 * static_cast<size_t>(kNormBlocks), kAlign);
+  return MUON_OK;
+}
+
+int32_t known_dtype(int32_t dtype, int32_t i) {
+  if (dtype != MUON_BF16 && dtype != MUON_FP32)
+    return fail(MUON_ERR_INVALID_ARG, "tensor %d: unknown dtype %d", i, dtype);
+  return MUON_OK;
+}
+
+// out == nullptr: nothing is written (the norm), or, with in_place, g itself.
+int32_t bind_grads(int32_t batch, const void* const* g, const int32_t* dtype, void* const* out,
+                   const int32_t* out_dtype, GradPlan& pl) {
+  if (batch == 0) return MUON_OK;
+  if (g == nullptr || dtype == nullptr) return fail(MUON_ERR_INVALID_ARG, "g/dtype array is null");
+  if (out != nullptr && out_dtype == nullptr)
+    return fail(MUON_ERR_INVALID_ARG, "out_dtype array is null");
+  for (int32_t i = 0; i < batch; ++i) {
+    GradDesc& d = pl.desc[i];
+    int32_t st = known_dtype(dtype[i], i);
+    if (st != MUON_OK) return st;
+    d.g = g[i];
+    d.in_bf16 = dtype[i] == MUON_BF16;
+    d.out = const_cast<void*>(g[i]);
+    d.out_bf16 = d.in_bf16;
+    if (out != nullptr) {
+      if ((st = known_dtype(out_dtype[i], i)) != MUON_OK) return st;
+      d.out = out[i];
+      d.out_bf16 = out_dtype[i] == MUON_BF16;
+    }
+    if (d.numel == 0) continue;
+    if (d.g == nullptr || d.out == nullptr)
+      return fail(MUON_ERR_INVALID_ARG, "tensor %d: null device pointer", i);
+    if (!aligned16(d.g) || !aligned16(d.out))
+      return fail(MUON_ERR_INVALID_ARG, "tensor %d: device pointer not 16-byte aligned", i);
+    if (d.out == d.g && d.out_bf16 != d.in_bf16)
+      return fail(MUON_ERR_INVALID_ARG, "tensor %d: in place needs one dtype", i);
+  }
+  return MUON_OK;
+}
+
+int32_t check_norm_params(const muon_grad_norm_params* p) {
+  if (p == nullptr) return fail(MUON_ERR_INVALID_ARG, "params pointer is null");
+  if (p->kind != MUON_NORM_L2 && p->kind != MUON_NORM_MAX)
+    return fail(MUON_ERR_INVALID_ARG, "unknown norm kind %d", p->kind);
+  if (p->clip != 0 && p->clip != 1) return fail(MUON_ERR_INVALID_ARG, "clip must be 0 or 1");
+  if (p->clip && (!(p->max_norm >= 0.f) || !std::isfinite(p->max_norm)))
+    return fail(MUON_ERR_INVALID_ARG, "max_norm must be finite and >= 0");
+  if (!std::isfinite(p->eps) || p->eps < 0.f)
+    return fail(MUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  return MUON_OK;
+}
+
+int32_t check_float_ptr(const void* p, const char* what) {
+  if (p == nullptr) return fail(MUON_ERR_INVALID_ARG, "%s pointer is null", what);
+  if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0)
+    return fail(MUON_ERR_INVALID_ARG, "%s pointer not 4-byte aligned", what);
+  return MUON_OK;
+}
+
+// The table: among the kernel arguments, or written to the workspace.
+int32_t grad_table(const GradPlan& pl, char* ws, hipStream_t s, GradTable& t) {
+  const int32_t batch = static_cast<int32_t>(pl.desc.size());
+  t.in_args = batch <= kGradInline;
+  if (t.in_args) {
+    std::copy(pl.desc.begin(), pl.desc.end(), t.args.desc);
+    std::copy(pl.prefix.begin(), pl.prefix.end(), t.args.prefix);
+    t.args.batch = batch;
+    return MUON_OK;
+  }
+  t.mem.desc = reinterpret_cast<const GradDesc*>(ws);
+  t.mem.prefix = reinterpret_cast<const int32_t*>(ws + pl.prefix_off);
+  t.mem.batch = batch;
+  hipError_t e = launch_put_bytes(pl.desc.data(), sizeof(GradDesc) * batch, ws, s);
+  if (e == hipSuccess)
+    e = launch_put_bytes(pl.prefix.data(), sizeof(int32_t) * pl.prefix.size(), ws + pl.prefix_off, s);
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "launch descriptor copy");
+}
+
+int32_t run_norm(const GradPlan& pl, const GradTable& t, const muon_grad_norm_params& p,
+                 float* result, char* ws, hipStream_t s) {
+  GradNormArgs a{};
+  a.result = result;
+  a.partials = ws + pl.partials_off;
+  a.chunks = pl.chunks;
+  a.clip = p.clip;
+  a.max_norm = p.max_norm;
+  a.eps = p.eps;
+  TimedLaunch tl(MUON_K_GRAD_NORM, s);
+  const hipError_t e = launch_grad_norm(t, a, p.kind, s);
+  if (e != hipSuccess) return hip_fail(e, "launch gradient norm");
+  tl.done();
+  return MUON_OK;
+}
+
+int32_t run_scale(const GradPlan& pl, const GradTable& t, const float* scale, hipStream_t s) {
+  TimedLaunch tl(MUON_K_GRAD_SCALE, s);
+  const hipError_t e = launch_grad_scale(t, pl.chunks, scale, s);
+  if (e != hipSuccess) return hip_fail(e, "launch gradient scale");
+  tl.done();
+  return MUON_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Block-scaled e4m3
+// ---------------------------------------------------------------------------
+int32_t check_f8_dim(int64_t v, const char* what, int32_t i) {
+  if (v < 0)
+    return fail(MUON_ERR_INVALID_ARG, "matrix %d: %s = %lld is negative", i, what,
+                static_cast<long long>(v));
+  if (v > MUON_F8_MAX_DIM)
+    return fail(MUON_ERR_UNSUPPORTED, "matrix %d: %s = %lld; the maximum is %d", i, what,
+                static_cast<long long>(v), MUON_F8_MAX_DIM);
+  return MUON_OK;
+}
+
+size_t f8_desc_bytes(int32_t batch) {
+  return align_up(std::max(sizeof(F8QuantDesc), sizeof(F8ProdDesc)) * static_cast<size_t>(batch),
+                  kAlign);
+}
+size_t f8_ws_bytes(int32_t batch) {
+  return f8_desc_bytes(batch) + align_up(sizeof(int32_t) * (static_cast<size_t>(batch) + 1), kAlign);
+}
+
+int32_t check_ptr(const void* p, const char* what, int32_t i) {
+  if (p == nullptr) return fail(MUON_ERR_INVALID_ARG, "matrix %d: %s is null", i, what);
+  if (!aligned16(p))
+    return fail(MUON_ERR_INVALID_ARG, "matrix %d: %s not 16-byte aligned", i, what);
+  return MUON_OK;
+}
+
+int32_t add_blocks(int64_t a, int64_t b, int64_t& total) {
+  total += a * b;  // at most 2^27 blocks of one matrix
+  if (total > INT32_MAX) return fail(MUON_ERR_UNSUPPORTED, "batch needs more than 2^31 blocks");
+  return MUON_OK;
+}
+
+int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
+
+template <typename D>
+int32_t put_f8_table(const std::vector<D>& desc, const std::vector<int32_t>& prefix, char* ws,
+                     hipStream_t s) {
+  hipError_t e = launch_put_bytes(desc.data(), sizeof(D) * desc.size(), ws, s);
+  if (e == hipSuccess)
+    e = launch_put_bytes(prefix.data(), sizeof(int32_t) * prefix.size(),
+                         ws + f8_desc_bytes(static_cast<int32_t>(desc.size())), s);
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "launch descriptor copy");
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" size_t muon_grad_workspace_bytes(int32_t batch, const int64_t* numel) {
+  try {
+    clear_detail();
+    GradPlan pl;
+    if (make_grad_plan(batch, numel, pl) != MUON_OK) return SIZE_MAX;
+    return pl.total_bytes;
+  } catch (...) {
+    fail(MUON_ERR_HIP, "unexpected host exception");
+    return SIZE_MAX;
+  }
+}
+
+extern "C" int32_t muon_grad_norm_batched(int32_t batch, const int64_t* numel,
+                                          const void* const* g, const int32_t* dtype,
+                                          const muon_grad_norm_params* p, float* result,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    clear_detail();
+    GradPlan pl;
+    int32_t st = make_grad_plan(batch, numel, pl);
+    if (st != MUON_OK) return st;
+    if ((st = check_norm_params(p)) != MUON_OK) return st;
+    if ((st = check_float_ptr(result, "result")) != MUON_OK) return st;
+    if ((st = bind_grads(batch, g, dtype, nullptr, nullptr, pl)) != MUON_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, pl.total_bytes)) != MUON_OK) return st;
+    char* ws = static_cast<char*>(workspace);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    GradTable t;
+    if ((st = grad_table(pl, ws, s, t)) != MUON_OK) return st;
+    return run_norm(pl, t, *p, result, ws, s);
+  } catch (...) {
+    return fail(MUON_ERR_HIP, "unexpected host exception");
+  }
+}
+
+extern "C" int32_t muon_grad_scale_batched(int32_t batch, const int64_t* numel,
+                                           const void* const* g, const int32_t* dtype,
+                                           void* const* out, const int32_t* out_dtype,
+                                           const float* scale, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  try {
+    clear_detail();
+    GradPlan pl;
+    int32_t st = make_grad_plan(batch, numel, pl);
+    if (st != MUON_OK) return st;
+    if ((st = check_float_ptr(scale, "scale")) != MUON_OK) return st;
+    if (batch == 0) return MUON_OK;
+    if (out == nullptr) return fail(MUON_ERR_INVALID_ARG, "out array is null");
+    if ((st = bind_grads(batch, g, dtype, out, out_dtype, pl)) != MUON_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, pl.total_bytes)) != MUON_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    GradTable t;
+    if ((st = grad_table(pl, static_cast<char*>(workspace), s, t)) != MUON_OK) return st;
+    return run_scale(pl, t, scale, s);
+  } catch (...) {
+    return fail(MUON_ERR_HIP, "unexpected host exception");
+  }
+}
+
+extern "C" int32_t muon_grad_clip_batched(int32_t batch, const int64_t* numel,
+                                          const void* const* g, const int32_t* dtype,
+                                          void* const* out, const int32_t* out_dtype,
+                                          const muon_grad_norm_params* p, float* result,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    clear_detail();
+    GradPlan pl;
+    int32_t st = make_grad_plan(batch, numel, pl);
+    if (st != MUON_OK) return st;
+    if ((st = check_norm_params(p)) != MUON_OK) return st;
+    if (!p->clip) return fail(MUON_ERR_INVALID_ARG, "clip must be 1");
+    if ((st = check_float_ptr(result, "result")) != MUON_OK) return st;
+    if (batch > 0 && out == nullptr) return fail(MUON_ERR_INVALID_ARG, "out array is null");
+    if ((st = bind_grads(batch, g, dtype, out, out_dtype, pl)) != MUON_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, pl.total_bytes)) != MUON_OK) return st;
+    char* ws = static_cast<char*>(workspace);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    GradTable t;
+    if ((st = grad_table(pl, ws, s, t)) != MUON_OK) return st;
+    if ((st = run_norm(pl, t, *p, result, ws, s)) != MUON_OK) return st;
+    return run_scale(pl, t, result + 1, s);
+  } catch (...) {
+    return fail(MUON_ERR_HIP, "unexpected host exception");
+  }
+}
+
+extern "C" size_t muon_f8_workspace_bytes(int32_t batch) {
+  clear_detail();
+  if (batch < 0) {
+    fail(MUON_ERR_INVALID_ARG, "batch = %d is negative", batch);
+    return SIZE_MAX;
+  }
+  return f8_ws_bytes(batch);
+}
+
+extern "C" int32_t muon_f8_quantize_batched(int32_t batch, const int64_t* rows,
+                                            const int64_t* cols, const void* const* x,
+                                            int32_t dtype, int32_t block_rows, void* const* q,
+                                            void* const* s, void* const* qt, void* const* st_,
+                                            void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+  try {
+    clear_detail();
+    if (batch < 0) return fail(MUON_ERR_INVALID_ARG, "batch = %d is negative", batch);
+    if (dtype != MUON_BF16 && dtype != MUON_FP32)
+      return fail(MUON_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+    if (block_rows != 1 && block_rows != kF8Block)
+      return fail(MUON_ERR_INVALID_ARG, "block_rows = %d: must be 1 or %d", block_rows, kF8Block);
+    if ((q == nullptr) != (s == nullptr) || (qt == nullptr) != (st_ == nullptr))
+      return fail(MUON_ERR_INVALID_ARG, "values and scales of an operand go together");
+    if (batch == 0) return MUON_OK;
+    if (q == nullptr && qt == nullptr)
+      return fail(MUON_ERR_INVALID_ARG, "neither the operand nor its transpose is asked for");
+    if (rows == nullptr || cols == nullptr || x == nullptr)
+      return fail(MUON_ERR_INVALID_ARG, "rows/cols/x array is null");
+    std::vector<F8QuantDesc> desc(batch);
+    std::vector<int32_t> prefix(static_cast<size_t>(batch) + 1, 0);
+    int64_t total = 0;
+    int32_t st;
+    for (int32_t i = 0; i < batch; ++i) {
+      if ((st = check_f8_dim(rows[i], "rows", i)) != MUON_OK) return st;
+      if ((st = check_f8_dim(cols[i], "cols", i)) != MUON_OK) return st;
+      F8QuantDesc& d = desc[i];
+      d = F8QuantDesc{};
+      d.rows = static_cast<int32_t>(rows[i]);
+      d.cols = static_cast<int32_t>(cols[i]);
+      if (d.rows > 0 && d.cols > 0) {
+        if ((st = check_ptr(x[i], "x", i)) != MUON_OK) return st;
+        d.x = x[i];
+        if (q != nullptr) {
+          if ((st = check_ptr(q[i], "q", i)) != MUON_OK) return st;
+          if ((st = check_ptr(s[i], "s", i)) != MUON_OK) return st;
+          d.q = static_cast<uint8_t*>(q[i]);
+          d.s = static_cast<uint8_t*>(s[i]);
+        }
+        if (qt != nullptr) {
+          if ((st = check_ptr(qt[i], "qt", i)) != MUON_OK) return st;
+          if ((st = check_ptr(st_[i], "st", i)) != MUON_OK) return st;
+          d.qt = static_cast<uint8_t*>(qt[i]);
+          d.st = static_cast<uint8_t*>(st_[i]);
+        }
+      }
+      if ((st = add_blocks(cdiv(rows[i], kF8Block), cdiv(cols[i], kF8Block), total)) != MUON_OK)
+        return st;
+      prefix[i + 1] = static_cast<int32_t>(total);
+    }
+    if ((st = check_workspace(workspace, workspace_bytes, f8_ws_bytes(batch))) != MUON_OK) return st;
+    char* ws = static_cast<char*>(workspace);
+    hipStream_t stm = static_cast<hipStream_t>(stream);
+    if ((st = put_f8_table(desc, prefix, ws, stm)) != MUON_OK) return st;
+    F8QuantCtx c{};
+    c.desc = reinterpret_cast<const F8QuantDesc*>(ws);
+    c.prefix = reinterpret_cast<const int32_t*>(ws + f8_desc_bytes(batch));
+    c.batch = batch;
+    c.stream = stm;
+    TimedLaunch tl(MUON_K_F8_QUANTIZE, stm);
+    const hipError_t e = launch_f8_quantize(c, prefix[batch], dtype == MUON_BF16, block_rows);
+    if (e != hipSuccess) return hip_fail(e, "launch e4m3 quantization");
+    tl.done();
+    return MUON_OK;
+  } catch (...) {
+    return fail(MUON_ERR_HIP, "unexpected host exception");
+  }
+}
+
+extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const int64_t* n,
+                                          const int64_t* k, const void* const* a,
+                                          const void* const* sa, const void* const* b,
+                                          const void* const* sb, void* const* c, int32_t dtype,
+                                          int32_t accumulate, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  try {
+    clear_detail();
+    if (batch < 0) return fail(MUON_ERR_INVALID_ARG, "batch = %d is negative", batch);
+    if (dtype != MUON_BF16 && dtype != MUON_FP32)
+      return fail(MUON_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+    if (accumulate != 0 && accumulate != 1)
+      return fail(MUON_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+    if (batch == 0) return MUON_OK;
+    if (m == nullptr || n == nullptr || k == nullptr || a == nullptr || sa == nullptr ||
+        b == nullptr || sb == nullptr || c == nullptr)
+      return fail(MUON_ERR_INVALID_ARG, "an argument array is null");
+    std::vector<F8ProdDesc> desc(batch);
+    std::vector<int32_t> prefix(static_cast<size_t>(batch) + 1, 0);
+    int64_t total = 0;
+    int32_t st;
+    for (int32_t i = 0; i < batch; ++i) {
+      if ((st = check_f8_dim(m[i], "m", i)) != MUON_OK) return st;
+      if ((st = check_f8_dim(n[i], "n", i)) != MUON_OK) return st;
+      if ((st = check_f8_dim(k[i], "k", i)) != MUON_OK) return st;
+      F8ProdDesc& d = desc[i];
+      d = F8ProdDesc{};
+      d.m = static_cast<int32_t>(m[i]);
+      d.n = static_cast<int32_t>(n[i]);
+      d.kp = static_cast<int32_t>(cdiv(k[i], kF8Block) * kF8Block);
+      // nothing to store, or nothing to add
+      const bool none = d.m == 0 || d.n == 0 || (d.kp == 0 && accumulate);
+      if (!none) {
+        if ((st = check_ptr(c[i], "c", i)) != MUON_OK) return st;
+        d.c = c[i];
+        if (d.kp > 0) {
+          if ((st = check_ptr(a[i], "a", i)) != MUON_OK) return st;
+          if ((st = check_ptr(sa[i], "sa", i)) != MUON_OK) return st;
+          if ((st = check_ptr(b[i], "b", i)) != MUON_OK) return st;
+          if ((st = check_ptr(sb[i], "sb", i)) != MUON_OK) return st;
+          d.a = static_cast<const uint8_t*>(a[i]);
+          d.sa = static_cast<const uint8_t*>(sa[i]);
+          d.b = static_cast<const uint8_t*>(b[i]);
+          d.sb = static_cast<const uint8_t*>(sb[i]);
+        }
+        if ((st = add_blocks(cdiv(m[i], kF8Tile), cdiv(n[i], kF8Tile), total)) != MUON_OK) return st;
+      }
+      prefix[i + 1] = static_cast<int32_t>(total);
+    }
+    if ((st = check_workspace(workspace, workspace_bytes, f8_ws_bytes(batch))) != MUON_OK) return st;
+    char* ws = static_cast<char*>(workspace);
+    hipStream_t stm = static_cast<hipStream_t>(stream);
+    if ((st = put_f8_table(desc, prefix, ws, stm)) != MUON_OK) return st;
+    F8ProdCtx x{};
+    x.desc = reinterpret_cast<const F8ProdDesc*>(ws);
+    x.prefix = reinterpret_cast<const int32_t*>(ws + f8_desc_bytes(batch));
+    x.batch = batch;
+    x.accumulate = accumulate;
+    x.stream = stm;
+    TimedLaunch tl(MUON_K_F8_PROD, stm);
+    const hipError_t e = launch_f8_prod(x, prefix[batch], dtype == MUON_BF16);
+    if (e != hipSuccess) return hip_fail(e, "launch e4m3 product");
+    tl.done();
+    return MUON_OK;
+  } catch (...) {
+    return fail(MUON_ERR_HIP, "unexpected host exception");
+  }
+}
