@@ -159,30 +159,84 @@ __device__ __forceinline__ void set_half(i32x8_t& f, int h, const u32x4_t& v) {
   for (int k = 0; k < 4; ++k) f[4 * h + k] = static_cast<int32_t>(v[k]);
 }
 
-// Sixteen consecutive columns of one row of C.
-template <typename T>
-__device__ __forceinline__ void store16(T* c, float* v, int32_t left, bool vec, bool add) {
-  constexpr int V = Elt<T>::kVec;
-  if (left >= 16 && vec) {
-    if (add) {
-      float o[16];
+// Stores the wave's 128 x 128 part of the tile, whose first element is row m0,
+// column n0 of C.  acc[mi][ni][4 g + e] of lane (lr, lh) is row 4 lr + ni,
+// column 4 (8 g + 4 lh + e) + mi.  The 32 rows of one ni go through 16 KiB of
+// LDS of the wave's own in fp32, four columns (the four mi) a 16-byte chunk,
+// chunk c of row r at c ^ r; they come out as whole rows, so that every store
+// covers full 128-byte lines (written from the accumulators, 16 bytes a row,
+// the store ran at 2.5 TB/s).  ADD: the old C of one ni is requested while the
+// one before it is stored.
+template <typename T, bool ADD>
+__device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][4], char* lds, T* c, int32_t m0,
+                                           int32_t n0, int32_t m, int32_t n, int lane) {
+  constexpr int V = Elt<T>::kVec;            // columns per lane: 16 bytes
+  constexpr int LPR = 128 / V;               // lanes per row
+  constexpr int RPI = 64 / LPR;              // rows per instruction
+  constexpr int NI = 32 / RPI;               // instructions per ni
+  const int lr = lane & 31, lh = lane >> 5;
+  const int rr0 = lane / LPR, ch = lane % LPR * (V / 4);
+  const int32_t col = n0 + lane % LPR * V;
+  const bool vec = n % V == 0;               // then a lane's columns all exist, or none
+  const bool fast = vec && col < n;
+  T* const corner = c + static_cast<int64_t>(m0) * n + col;
+  u32x4_t old[2][ADD ? NI : 1];
+  auto request = [&](int ni, u32x4_t* to) {
 #pragma unroll
-      for (int h = 0; h < 16 / V; ++h) vec_to_f32<T>(ld16(c + h * V), o + h * V);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] += o[e];
+    for (int i = 0; i < NI; ++i) {
+      const int32_t r = 4 * (RPI * i + rr0) + ni;
+      if (fast && m0 + r < m) to[i] = ld16(corner + static_cast<int64_t>(r) * n);
     }
+  };
+  if constexpr (ADD) request(0, old[0]);
 #pragma unroll
-    for (int h = 0; h < 16 / V; ++h) st16(c + h * V, f32_to_vec<T>(v + h * V));
-    return;
+  for (int ni = 0; ni < 4; ++ni) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f32x4_t x;
+#pragma unroll
+        for (int mi = 0; mi < 4; ++mi) x[mi] = acc[mi][ni][4 * g + e];
+        *reinterpret_cast<f32x4_t*>(lds + lr * 512 + (((8 * g + 4 * lh + e) ^ lr) << 4)) = x;
+      }
+    __builtin_amdgcn_wave_barrier();
+    if constexpr (ADD)
+      if (ni < 3) request(ni + 1, old[(ni + 1) & 1]);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int rr = RPI * i + rr0;
+      float v[V];
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(lds + rr * 512 + (((ch + q) ^ rr) << 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
+      }
+      const int32_t r = 4 * rr + ni;
+      if (m0 + r >= m || col >= n) continue;
+      T* const to = corner + static_cast<int64_t>(r) * n;
+      if (fast) {
+        if constexpr (ADD) {
+          float o[V];
+          vec_to_f32<T>(old[ni & 1][i], o);
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[e] += o[e];
+        }
+        st16(to, f32_to_vec<T>(v));
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (col + e < n) to[e] = Elt<T>::from_f32(ADD ? v[e] + Elt<T>::to_f32(to[e]) : v[e]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (e < left) c[e] = Elt<T>::from_f32(add ? v[e] + Elt<T>::to_f32(c[e]) : v[e]);
 }
 
 }  // namespace
 
-template <typename T>
+template <typename T, bool ADD>
 __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(F8ProdCtx c) {
   __shared__ __attribute__((aligned(1024))) char smem[LDS8];
   __shared__ int slot;
@@ -389,38 +443,297 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(F8ProdCtx c) {
         ssq = nsq;
       }
     }
-    wait_vm<0>();  // no load may still target LDS when the block ends
+    wait_vm<0>();  // no load may still target LDS: the ring is reused for the store
+  }
+  __syncthreads();
+  store_part<T, ADD>(acc, smem + wave * 16384, static_cast<T*>(d.c), m0 + 128 * wn, n0 + 128 * wm,
+                     d.m, d.n, lane);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows, or a batch of few tiles: blocks of 16 MT rows of A by 16 NT rows of
+// B, the K blocks of 128 dealt to the four waves (kb = wave, wave + 4, ...) and
+// the four partial tiles joined through LDS in a fixed order.  Each wave streams
+// its own K blocks through LDS of its own, kStages deep, with no barrier until
+// the join: direct-to-LDS loads of whole 128-byte rows.  (Loaded straight into
+// registers, where neighbouring lanes sit in different rows, a load took 64
+// cycles of the address unit instead of 16, and that bounded the kernel.)
+//   v_mfma_f32_16x16x.. with B as its first operand: lane (r, g) holds the
+// 16-byte chunks g and 4 + g of row r's 128 bytes (both operands alike, so the
+// order of K within them does not matter).  Row r of B's fragment t is row
+// NT r + t of the tile, so that a lane's NT scales are neighbours and its
+// results 4 NT consecutive columns of C.  Chunk c of LDS row s sits at
+// c ^ ((s / 2) % 8): the 16 rows of a fragment read fall on distinct banks.
+// ---------------------------------------------------------------------------
+namespace {
+
+__device__ __forceinline__ i32x8_t joined(const u32x4_t& lo, const u32x4_t& hi) {
+  typedef uint32_t u32x8_t __attribute__((ext_vector_type(8)));
+  const u32x8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(i32x8_t, v);
+}
+
+// Waits until at most N of this wave's loads are in flight; the compiler moves
+// no memory access across it.
+template <int N>
+__device__ __forceinline__ void await_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// The rows of one operand, 128 bytes of each per K block: N fragments of 16.
+template <int N>
+struct SmallStream {
+  const uint8_t* base;    // the tile's first row (uniform)
+  const uint8_t* scales;  // scale row 0 at the tile's first row (uniform)
+  uint32_t bytes;         // of the tile's rows that exist
+  int32_t rp;             // bytes of a scale row
+  int32_t voff[2 * N];
+  int32_t soff;
+
+  // STRIDE: tile row of LDS row 16 t + r is N r + t (B) or 16 t + r (A).
+  template <bool STRIDE>
+  __device__ __forceinline__ void init(const uint8_t* q, const uint8_t* s, int32_t row0,
+                                       int32_t rows, int32_t kp, int lane) {
+    const int32_t valid = min(16 * N, rows - row0);
+    base = q + static_cast<int64_t>(row0) * kp;
+    bytes = static_cast<uint32_t>(valid) * static_cast<uint32_t>(kp);
+    scales = s + row0;
+    rp = (rows + 15) & ~15;
+#pragma unroll
+    for (int u = 0; u < 2 * N; ++u) {
+      const int l = 8 * u + (lane >> 3);  // LDS row
+      const int row = STRIDE ? N * (l & 15) + (l >> 4) : l;
+      voff[u] = min(row, valid - 1) * kp + (((lane & 7) ^ ((l >> 1) & 7)) << 4);
+    }
+    soff = min(4 * lane, rp - 4 - row0);
+  }
+  __device__ __forceinline__ void issue(int kb, uint32_t lds, uint32_t lds_scales) const {
+    const i32x4_t r = make_rsrc(base + static_cast<int64_t>(kb) * kF8Block,
+                                bytes - static_cast<uint32_t>(kb) * kF8Block);
+#pragma unroll
+    for (int u = 0; u < 2 * N; ++u) lds_dma16(lds + 1024 * u, voff[u], r);
+    lds_dma4(lds_scales, soff, make_rsrc(scales + static_cast<int64_t>(kb) * rp, 256));
+  }
+};
+
+template <int N>
+__device__ __forceinline__ int32_t lds_scales(const char* p) {
+  if constexpr (N == 4)
+    return *reinterpret_cast<const int32_t*>(p);
+  else if constexpr (N == 2)
+    return *reinterpret_cast<const uint16_t*>(p);
+  else
+    return *reinterpret_cast<const uint8_t*>(p);
+}
+
+template <int MT, int NT>
+struct SmallShape {
+  static constexpr int kA = 2048 * NT, kSB = kA + 2048 * MT, kSA = kSB + 256;  // within a stage
+  static constexpr int kStageBytes = kSA + 256;
+  static constexpr int kStages = 4 * 3 * kStageBytes <= 152 * 1024 ? 3 : 2;
+  static constexpr int kWaveBytes = kStages * kStageBytes;
+  static constexpr int kPitch = 16 * NT + 4;  // floats per row of a partial tile
+  static constexpr int kLoads = 2 * NT + 2 * MT + 2;  // per stage
+  static_assert(16 * MT * kPitch * 4 <= kWaveBytes, "a partial tile fits the wave's ring");
+};
+
+}  // namespace
+
+template <typename T, int MT, int NT>
+__global__ __launch_bounds__(kThreads) void k_f8_small(F8ProdCtx c) {
+  using S = SmallShape<MT, NT>;
+  constexpr int BM = 16 * MT, BN = 16 * NT, PITCH = S::kPitch;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * S::kWaveBytes];
+  __shared__ int slot;
+  const int32_t blk = xcd_remap(blockIdx.x, gridDim.x);
+  const int j = __builtin_amdgcn_readfirstlane(locate_matrix(c.prefix, c.batch, blk, &slot));
+  const F8ProdDesc d = load_const(c.desc + j);
+  const int32_t t = blk - load_const(c.prefix + j);
+  const int32_t tm = (d.m + BM - 1) / BM;
+  const int32_t m0 = t % tm * BM, n0 = t / tm * BN;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  char* const mine = smem + wave * S::kWaveBytes;
+
+  f32x4_t acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int k = 0; k < NT; ++k) acc[i][k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  const int nkb = d.kp / kF8Block;
+  const int steps = (nkb - wave + 3) / 4;  // of this wave; 0 or less: none
+  if (steps > 0) {
+    SmallStream<NT> sb;
+    SmallStream<MT> sa;
+    sb.template init<true>(d.b, d.sb, n0, d.n, d.kp, lane);
+    sa.template init<false>(d.a, d.sa, m0, d.m, d.kp, lane);
+    const uint32_t ring = __builtin_amdgcn_readfirstlane(
+        static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LDS_AS char*)mine)));
+    // Past the end the last block is loaded again: nobody reads it, and the
+    // count in flight stays constant.
+    auto issue = [&](int s, int stage) {
+      const int kb = wave + 4 * min(s, steps - 1);
+      const uint32_t at = ring + stage * S::kStageBytes;
+      sb.issue(kb, at, at + S::kSB);
+      sa.issue(kb, at + S::kA, at + S::kSA);
+    };
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) issue(s, s);
+    const int ch0 = (g ^ ((r >> 1) & 7)) << 4, ch1 = ((4 + g) ^ ((r >> 1) & 7)) << 4;
+    int stage = 0;
+    for (int s = 0; s < steps; ++s) {
+      // refill the stage read in the last step
+      issue(s + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
+      await_loads<(S::kStages - 1) * S::kLoads>();
+      const char* const at = mine + stage * S::kStageBytes;
+      u32x4_t b[NT][2], a[MT][2];
+      int32_t xa[MT];
+      const int32_t xb = lds_scales<NT>(at + S::kSB + NT * r);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) xa[i] = lds_scales<1>(at + S::kSA + 16 * i + r);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        a[i][0] = lds16(at + S::kA + (16 * i + r) * 128 + ch0);
+        a[i][1] = lds16(at + S::kA + (16 * i + r) * 128 + ch1);
+      }
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        b[k][0] = lds16(at + (16 * k + r) * 128 + ch0);
+        b[k][1] = lds16(at + (16 * k + r) * 128 + ch1);
+      }
+      if constexpr (sizeof(T) == 2) {
+        static_for<NT>([&](auto K) {
+          constexpr int k = decltype(K)::value;
+          const i32x8_t fb = joined(b[k][0], b[k][1]);
+          static_for<MT>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            acc[i][k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                fb, joined(a[i][0], a[i][1]), acc[i][k], 0, 0, k, xb, 0, xa[i]);
+          });
+        });
+      } else {
+        Wide wa[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            widen(wa[i], q, static_cast<int32_t>(a[i][q >> 2][q & 3]), scale_value(xa[i], 0));
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+          Wide wb;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            widen(wb, q, static_cast<int32_t>(b[k][q >> 2][q & 3]), scale_value(xb, k));
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+              acc[i][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.v[q], wa[i].v[q], acc[i][k], 0, 0, 0);
+        }
+      }
+      wait_lgkm0();  // the reads are done before the stage is refilled
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    }
+    await_loads<0>();  // no load may still target LDS: the ring is reused for the join
   }
 
-  // acc[mi][ni][4 g + e] of this lane: row 128 wn + 4 lr + ni, column
-  // 128 wm + 4 (8 g + 4 lh + e) + mi of the tile.
+  // acc[i][k][e] of lane (r, g): row 16 i + r, column NT (4 g + e) + k
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float* to = reinterpret_cast<float*>(mine) + (16 * i + r) * PITCH + NT * (4 * g + e);
+#pragma unroll
+      for (int k = 0; k < NT; ++k) to[k] = acc[i][k][e];
+    }
+  __syncthreads();
+  constexpr int LPR = BN / 4;  // threads per row, four columns each
+  const int32_t col = n0 + 4 * static_cast<int>(threadIdx.x % LPR);
+  const bool vec = d.n % 4 == 0;
   T* const cc = static_cast<T*>(d.c);
-  const bool vec = d.n % Elt<T>::kVec == 0;
+  for (int rr = threadIdx.x / LPR; rr < BM; rr += kThreads / LPR) {
+    const int32_t row = m0 + rr;
+    if (row >= d.m || col >= d.n) break;
+    const float* from = reinterpret_cast<const float*>(smem) + rr * PITCH + 4 * (threadIdx.x % LPR);
+    constexpr int W = S::kWaveBytes / 4;
+    float v[4];
 #pragma unroll
-  for (int ni = 0; ni < 4; ++ni) {
-    const int32_t row = m0 + 128 * wn + 4 * lr + ni;
-    if (row >= d.m) continue;
+    for (int e = 0; e < 4; ++e) v[e] = ((from[e] + from[W + e]) + from[2 * W + e]) + from[3 * W + e];
+    T* to = cc + static_cast<int64_t>(row) * d.n + col;
+    if (vec) {
+      if (c.accumulate) {
+        float o[4];
+        load4<T>(to, o);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int32_t col = n0 + 128 * wm + 32 * g + 16 * lh;
-      float v[16];
+        for (int e = 0; e < 4; ++e) v[e] += o[e];
+      }
+      store4<T>(to, v);
+    } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int mi = 0; mi < 4; ++mi) v[4 * e + mi] = acc[mi][ni][4 * g + e];
-      if (col < d.n)
-        store16(cc + static_cast<int64_t>(row) * d.n + col, v, d.n - col, vec, c.accumulate != 0);
+        if (col + e < d.n)
+          to[e] = Elt<T>::from_f32(c.accumulate ? v[e] + Elt<T>::to_f32(to[e]) : v[e]);
     }
   }
 }
 
+namespace {
+
+template <typename T>
+hipError_t run_small(const F8ProdCtx& c, int32_t nblocks, int32_t mt, int32_t nt) {
+  const dim3 grid(nblocks), block(kThreads);
+  if (nt == 4) {
+    if (mt == 1)
+      hipLaunchKernelGGL((k_f8_small<T, 1, 4>), grid, block, 0, c.stream, c);
+    else if (mt == 2)
+      hipLaunchKernelGGL((k_f8_small<T, 2, 4>), grid, block, 0, c.stream, c);
+    else
+      hipLaunchKernelGGL((k_f8_small<T, 4, 4>), grid, block, 0, c.stream, c);
+  } else if (nt == 2) {
+    if (mt == 1)
+      hipLaunchKernelGGL((k_f8_small<T, 1, 2>), grid, block, 0, c.stream, c);
+    else if (mt == 2)
+      hipLaunchKernelGGL((k_f8_small<T, 2, 2>), grid, block, 0, c.stream, c);
+    else
+      hipLaunchKernelGGL((k_f8_small<T, 4, 2>), grid, block, 0, c.stream, c);
+  } else {
+    if (mt == 1)
+      hipLaunchKernelGGL((k_f8_small<T, 1, 1>), grid, block, 0, c.stream, c);
+    else if (mt == 2)
+      hipLaunchKernelGGL((k_f8_small<T, 2, 1>), grid, block, 0, c.stream, c);
+    else
+      hipLaunchKernelGGL((k_f8_small<T, 4, 1>), grid, block, 0, c.stream, c);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_f8_small(const F8ProdCtx& c, int32_t nblocks, bool is_bf16, int32_t mt,
+                           int32_t nt) {
+  if (nblocks <= 0) return hipSuccess;
+  return is_bf16 ? run_small<uint16_t>(c, nblocks, mt, nt) : run_small<float>(c, nblocks, mt, nt);
+}
+
+namespace {
+
+template <typename T>
+hipError_t run_prod(const F8ProdCtx& c, int32_t ntiles) {
+  if (c.accumulate)
+    hipLaunchKernelGGL((k_f8_prod<T, true>), dim3(ntiles), dim3(kThreads), 0, c.stream, c);
+  else
+    hipLaunchKernelGGL((k_f8_prod<T, false>), dim3(ntiles), dim3(kThreads), 0, c.stream, c);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_f8_prod(const F8ProdCtx& c, int32_t ntiles, bool is_bf16) {
   if (ntiles <= 0) return hipSuccess;
-  if (is_bf16)
-    hipLaunchKernelGGL(k_f8_prod<uint16_t>, dim3(ntiles), dim3(kThreads), 0, c.stream, c);
-  else
-    hipLaunchKernelGGL(k_f8_prod<float>, dim3(ntiles), dim3(kThreads), 0, c.stream, c);
-  return hipGetLastError();
+  return is_bf16 ? run_prod<uint16_t>(c, ntiles) : run_prod<float>(c, ntiles);
 }
 
 }  // namespace muon

@@ -245,6 +245,9 @@ struct F8ProdCtx {
 };
 hipError_t launch_f8_prod(const F8ProdCtx& c, int32_t ntiles, bool is_bf16);
 constexpr int kF8Tile = 256;  // output tile (both sides)
+// The kernel of few rows: blocks of 16 mt x 16 nt, mt in {1, 2, 4}, nt in {1, 4}.
+hipError_t launch_f8_small(const F8ProdCtx& c, int32_t nblocks, bool is_bf16, int32_t mt,
+                           int32_t nt);
 
 // Host launchers (one per kernel family).  is_bf16 selects the element type.
 // Momentum (step), U into X ping and the per-block sums of U^2.

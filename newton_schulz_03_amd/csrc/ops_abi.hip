@@ -164,7 +164,7 @@ size_t f8_desc_bytes(int32_t batch) {
                   kAlign);
 }
 size_t f8_ws_bytes(int32_t batch) {
-  return f8_desc_bytes(batch) + align_up(sizeof(int32_t) * (static_cast<size_t>(batch) + 1), kAlign);
+  return f8_desc_bytes(batch) + align_up(2 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1), kAlign);
 }
 
 int32_t check_ptr(const void* p, const char* what, int32_t i) {
@@ -182,13 +182,80 @@ int32_t add_blocks(int64_t a, int64_t b, int64_t& total) {
 
 int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
+// Which kernel takes which product, and the block shape of the small one.
+//
+// Products of up to kFewRows rows go to the kernel of few rows: B's bytes bound
+// them, and its blocks are as many as its 64-row pieces (24 products 4 x 2048 x
+// 6144: 51 us against 91 in 256 x 256 tiles).  The others go where the
+// following estimates, fitted to measurements from 64 to 24576 tiles, say the
+// call ends first; all of them to one kernel.  us per tile on one of the 256
+// CUs: a fixed part and one per K slice, which grows in the large tile as the
+// chip fills up.  (2048^3 in bf16: 32 us large, 31 small; 1024^3: 21 and 9;
+// 4096^3: 67 and 189.)
+constexpr int32_t kFewRows = 64;
+constexpr double kCus = 256;
+
+struct SmallPlan {
+  int32_t mt = 1, nt = 4;
+};
+
+int32_t plan_products(const std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int32_t>& big,
+                      std::vector<int32_t>& small, SmallPlan& sp) {
+  double tiles = 0, slices = 0, blocks = 0, steps = 0;
+  int32_t few_rows = 0;
+  for (const F8ProdDesc& d : desc) {
+    if (d.m <= kFewRows) {
+      few_rows = std::max(few_rows, d.m);
+      continue;
+    }
+    const double t = static_cast<double>(cdiv(d.m, kF8Tile)) * static_cast<double>(cdiv(d.n, kF8Tile));
+    tiles += t;
+    slices += t * (d.kp / 64);
+    const double b = static_cast<double>(cdiv(d.m, 64)) * static_cast<double>(cdiv(d.n, 64));
+    blocks += b;
+    steps += b * static_cast<double>(cdiv(d.kp, 4 * kF8Block));
+  }
+  bool all_small = true;
+  if (tiles > 0) {
+    const double full = std::min(1.0, tiles / kCus);
+    const double fixed = bf16 ? 8 : 15, slice = bf16 ? 0.45 + 0.35 * full : 1.25 + 0.2 * full;
+    const double large_us = std::ceil(tiles / kCus) * (fixed + slice * slices / tiles);
+    const double small_us = std::ceil(blocks / kCus) * (3.0 + 1.25 * steps / blocks);
+    all_small = small_us < large_us;
+  }
+  if (all_small && tiles > 0) few_rows = kFewRows;
+  sp.mt = few_rows <= 16 ? 1 : few_rows <= 32 ? 2 : 4;
+  // narrower blocks while there are too few to occupy the chip (one product 4 x
+  // 2048 x 6144: 9.3 us in 32 blocks, 7.6 in 64, 7.2 in 128)
+  double n64 = 0;
+  for (const F8ProdDesc& d : desc)
+    if (d.m > 0 && (d.m <= kFewRows || all_small))
+      n64 += static_cast<double>(cdiv(d.m, 16 * sp.mt)) * static_cast<double>(cdiv(d.n, 64));
+  sp.nt = n64 >= 96 ? 4 : n64 >= 48 ? 2 : 1;
+  int64_t nb = 0, ns = 0;
+  int32_t st;
+  for (size_t i = 0; i < desc.size(); ++i) {
+    const F8ProdDesc& d = desc[i];
+    if (d.m > 0) {
+      st = d.m <= kFewRows || all_small
+               ? add_blocks(cdiv(d.m, 16 * sp.mt), cdiv(d.n, 16 * sp.nt), ns)
+               : add_blocks(cdiv(d.m, kF8Tile), cdiv(d.n, kF8Tile), nb);
+      if (st != MUON_OK) return st;
+    }
+    big[i + 1] = static_cast<int32_t>(nb);
+    small[i + 1] = static_cast<int32_t>(ns);
+  }
+  return MUON_OK;
+}
+
 template <typename D>
 int32_t put_f8_table(const std::vector<D>& desc, const std::vector<int32_t>& prefix, char* ws,
                      hipStream_t s) {
-  hipError_t e = launch_put_bytes(desc.data(), sizeof(D) * desc.size(), ws, s);
-  if (e == hipSuccess)
-    e = launch_put_bytes(prefix.data(), sizeof(int32_t) * prefix.size(),
-                         ws + f8_desc_bytes(static_cast<int32_t>(desc.size())), s);
+  const size_t off = f8_desc_bytes(static_cast<int32_t>(desc.size()));
+  std::vector<char> t(off + sizeof(int32_t) * prefix.size(), 0);
+  std::memcpy(t.data(), desc.data(), sizeof(D) * desc.size());
+  std::memcpy(t.data() + off, prefix.data(), sizeof(int32_t) * prefix.size());
+  const hipError_t e = launch_put_bytes(t.data(), t.size(), ws, s);
   return e == hipSuccess ? MUON_OK : hip_fail(e, "launch descriptor copy");
 }
 
@@ -380,8 +447,8 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
         b == nullptr || sb == nullptr || c == nullptr)
       return fail(MUON_ERR_INVALID_ARG, "an argument array is null");
     std::vector<F8ProdDesc> desc(batch);
-    std::vector<int32_t> prefix(static_cast<size_t>(batch) + 1, 0);
-    int64_t total = 0;
+    // tiles of the two kernels, each product's in one of them
+    std::vector<int32_t> big(static_cast<size_t>(batch) + 1, 0), small(big);
     int32_t st;
     for (int32_t i = 0; i < batch; ++i) {
       if ((st = check_f8_dim(m[i], "m", i)) != MUON_OK) return st;
@@ -407,13 +474,17 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
           d.b = static_cast<const uint8_t*>(b[i]);
           d.sb = static_cast<const uint8_t*>(sb[i]);
         }
-        if ((st = add_blocks(cdiv(m[i], kF8Tile), cdiv(n[i], kF8Tile), total)) != MUON_OK) return st;
+      } else {
+        d.m = 0;
       }
-      prefix[i + 1] = static_cast<int32_t>(total);
     }
+    SmallPlan sp;
+    if ((st = plan_products(desc, dtype == MUON_BF16, big, small, sp)) != MUON_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, f8_ws_bytes(batch))) != MUON_OK) return st;
     char* ws = static_cast<char*>(workspace);
     hipStream_t stm = static_cast<hipStream_t>(stream);
+    std::vector<int32_t> prefix(big);
+    prefix.insert(prefix.end(), small.begin(), small.end());
     if ((st = put_f8_table(desc, prefix, ws, stm)) != MUON_OK) return st;
     F8ProdCtx x{};
     x.desc = reinterpret_cast<const F8ProdDesc*>(ws);
@@ -422,7 +493,9 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
     x.accumulate = accumulate;
     x.stream = stm;
     TimedLaunch tl(MUON_K_F8_PROD, stm);
-    const hipError_t e = launch_f8_prod(x, prefix[batch], dtype == MUON_BF16);
+    hipError_t e = launch_f8_prod(x, big[batch], dtype == MUON_BF16);
+    x.prefix += batch + 1;
+    if (e == hipSuccess) e = launch_f8_small(x, small[batch], dtype == MUON_BF16, sp.mt, sp.nt);
     if (e != hipSuccess) return hip_fail(e, "launch e4m3 product");
     tl.done();
     return MUON_OK;
