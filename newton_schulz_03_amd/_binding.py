@@ -7,8 +7,10 @@ library is missing the calls raise; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+from array import array
 from typing import List, NamedTuple, Optional, Sequence, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -103,9 +105,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_step_batched.argtypes = [i32, i64p, i64p, vpp, vpp, vpp, i32,
                                       ctypes.POINTER(StepParams), vp, sz, vp]
     lib.muon_step_batched.restype = i32
-    lib.muon_adamw_workspace_bytes.argtypes = [i32, i64p]
+    lib.muon_adamw_workspace_bytes.argtypes = [i32, vp]
     lib.muon_adamw_workspace_bytes.restype = sz
-    lib.muon_adamw_batched.argtypes = [i32, i64p, vpp, vpp, vpp, vpp, i32,
+    lib.muon_adamw_batched.argtypes = [i32, vp, vp, vp, vp, vp, i32,
                                        ctypes.POINTER(AdamWParams), vp, sz, vp]
     lib.muon_adamw_batched.restype = i32
     lib.muon_status_string.argtypes = [i32]
@@ -121,30 +123,29 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_timing_reset.restype = i32
     lib.muon_hbm_stream.argtypes = [i32, vpp, i32, vpp, sz, i32, vp]
     lib.muon_hbm_stream.restype = i32
-    i32p = ctypes.POINTER(i32)
-    lib.muon_grad_workspace_bytes.argtypes = [i32, i64p]
+    # The calls below take their host arrays as addresses (of an array.array's
+    # buffer, or a ctypes array).
+    lib.muon_grad_workspace_bytes.argtypes = [i32, vp]
     lib.muon_grad_workspace_bytes.restype = sz
-    lib.muon_grad_norm_batched.argtypes = [i32, i64p, vpp, i32p, ctypes.POINTER(GradNormParams), vp,
-                                           vp, sz, vp]
+    lib.muon_grad_norm_batched.argtypes = [i32, vp, vp, vp, ctypes.POINTER(GradNormParams), vp, vp,
+                                           sz, vp]
     lib.muon_grad_norm_batched.restype = i32
-    lib.muon_grad_scale_batched.argtypes = [i32, i64p, vpp, i32p, vpp, i32p, vp, vp, sz, vp]
+    lib.muon_grad_scale_batched.argtypes = [i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.muon_grad_scale_batched.restype = i32
-    lib.muon_grad_clip_batched.argtypes = [i32, i64p, vpp, i32p, vpp, i32p,
-                                           ctypes.POINTER(GradNormParams), vp, vp, sz, vp]
+    lib.muon_grad_clip_batched.argtypes = [i32, vp, vp, vp, vp, vp, ctypes.POINTER(GradNormParams),
+                                           vp, vp, sz, vp]
     lib.muon_grad_clip_batched.restype = i32
     lib.muon_step_batched_scaled.argtypes = [i32, i64p, i64p, vpp, vpp, vpp, i32,
                                              ctypes.POINTER(StepParams), vp, vp, sz, vp]
     lib.muon_step_batched_scaled.restype = i32
-    lib.muon_adamw_batched_scaled.argtypes = [i32, i64p, vpp, vpp, vpp, vpp, i32,
+    lib.muon_adamw_batched_scaled.argtypes = [i32, vp, vp, vp, vp, vp, i32,
                                               ctypes.POINTER(AdamWParams), vp, vp, sz, vp]
     lib.muon_adamw_batched_scaled.restype = i32
     lib.muon_f8_workspace_bytes.argtypes = [i32]
     lib.muon_f8_workspace_bytes.restype = sz
-    lib.muon_f8_quantize_batched.argtypes = [i32, i64p, i64p, vpp, i32, i32, vpp, vpp, vpp, vpp, vp,
-                                             sz, vp]
+    lib.muon_f8_quantize_batched.argtypes = [i32, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp]
     lib.muon_f8_quantize_batched.restype = i32
-    lib.muon_f8_matmul_batched.argtypes = [i32, i64p, i64p, i64p, vpp, vpp, vpp, vpp, vpp, i32, i32,
-                                           vp, sz, vp]
+    lib.muon_f8_matmul_batched.argtypes = [i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, sz, vp]
     lib.muon_f8_matmul_batched.restype = i32
     _lib_handle = lib
     return lib
@@ -365,8 +366,9 @@ def _scale_pointer(t, dev):
 
     if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != torch.float32 or \
             t.numel() != 1:
-        raise ValueError("grad_scale: a float32 tensor of one element on the device of the weights")
-    return ctypes.c_void_p(t.data_ptr())
+        raise ValueError("the factor must be a float32 tensor of one element on the device of the "
+                         "other tensors")
+    return t.data_ptr()
 
 
 def adamw_workspace_bytes(numels: Sequence[int]) -> int:
@@ -405,32 +407,60 @@ def adamw_batched(params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg
         raise ValueError(f"params must live on a HIP device, got {dev}")
     for group, want in ((ps, ps[0].dtype), (gs, ps[0].dtype), (ms, torch.float32),
                         (vs, torch.float32)):
-        for t in group:
-            if t.device != dev or t.dtype != want or not t.is_contiguous():
-                raise ValueError("tensors must be contiguous on one device; p and g share a "
-                                 "dtype, the moments are float32")
-    for p, g, m, v in zip(ps, gs, ms, vs):
-        if not (p.shape == g.shape == m.shape == v.shape):
-            raise ValueError("p, g, m and v of one entry must have the same shape")
+        if not _all_same(group, dev, want):
+            raise ValueError("tensors must be contiguous on one device; p and g share a "
+                             "dtype, the moments are float32")
+    shapes = [p.shape for p in ps]
+    if not (shapes == [g.shape for g in gs] == [m.shape for m in ms] == [v.shape for v in vs]):
+        raise ValueError("p, g, m and v of one entry must have the same shape")
     code = _dtype_code(ps[0].dtype)
-    numels = [p.numel() for p in ps]
+    numels = array("q", map(torch.Tensor.numel, ps))
     if workspace is None:
-        n = adamw_workspace_bytes(numels)
-        ws = torch.empty(max(n, 1) + 256, dtype=torch.uint8, device=dev)
-        off = (-ws.data_ptr()) % 256
-        workspace = ws[off:off + max(n, 1)]
+        workspace = _byte_workspace(_adamw_table_bytes(len(ps)), dev)
     b1, b2 = (float(b) for b in betas)
     prm = AdamWParams(float(lr), b1, b2, float(eps), float(weight_decay), int(step))
+    ptrs = [array("Q", map(torch.Tensor.data_ptr, group)) for group in (ps, gs, ms, vs)]
     fn, scale = lib.muon_adamw_batched, ()
     if grad_scale is not None:
         fn, scale = lib.muon_adamw_batched_scaled, (_scale_pointer(grad_scale, dev),)
-    with torch.cuda.device(dev):
-        st = fn(len(ps), _i64_array(numels), _ptr_array([t.data_ptr() for t in ps]),
-                _ptr_array([t.data_ptr() for t in gs]), _ptr_array([t.data_ptr() for t in ms]),
-                _ptr_array([t.data_ptr() for t in vs]), code, ctypes.byref(prm), *scale,
-                ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                ctypes.c_void_p(_stream_handle(dev)))
-    _check(st, fn.__name__)
+    _call(fn, dev, workspace, len(ps), _addr(numels), *map(_addr, ptrs), code, ctypes.byref(prm),
+          *scale)
+
+
+@functools.lru_cache(maxsize=None)
+def _adamw_table_bytes(batch: int) -> int:
+    # the workspace is the descriptor table, whatever the sizes
+    return adamw_workspace_bytes([0] * batch)
+
+
+def _addr(a: array) -> int:
+    """Address of an array's buffer; the array must outlive its use."""
+    return a.buffer_info()[0]
+
+
+def _all_same(ts, dev, dtype) -> bool:
+    """Whether every tensor is contiguous, on `dev` and of `dtype`."""
+    import torch
+
+    n = len(ts)
+    return ([t.dtype for t in ts].count(dtype) == n
+            and list(map(torch.Tensor.get_device, ts)).count(dev.index) == n
+            and all(map(torch.Tensor.is_contiguous, ts)))
+
+
+def _call(fn, dev, workspace, *args) -> None:
+    """Runs an entry point whose last arguments are the workspace, its size and
+    the stream, on `dev` and its current stream."""
+    import torch
+
+    args += (workspace.data_ptr(), workspace.numel(), _stream_handle(dev))
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != MUON_OK:
+        _check(st, fn.__name__)
 
 
 # ---------------------------------------------------------------------------
@@ -443,34 +473,35 @@ _NORM_KINDS = {2: 0, math.inf: 1}  # MUON_NORM_L2, MUON_NORM_MAX
 def _byte_workspace(nbytes: int, dev):
     import torch
 
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if ws.data_ptr() % 256 == 0:  # as torch's allocator gives it
+        return ws
     ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
     off = (-ws.data_ptr()) % 256
-    return ws[off:off + nbytes] if off else ws[:nbytes]
+    return ws[off:off + nbytes]
 
 
 def _flat_tensors(ts, name, dev=None):
-    """(device, dtype codes, element counts, pointers) of contiguous bf16 / fp32 tensors."""
+    """(device, dtype codes, element counts, pointers) of contiguous bf16 / fp32
+    tensors, the last three as arrays."""
     import torch
 
-    codes = {torch.bfloat16: MUON_BF16, torch.float32: MUON_FP32}
     dev = ts[0].device if dev is None else dev
     if dev.type != "cuda":
         raise ValueError(f"{name}: tensors must live on a HIP device, got {dev}")
-    got, numels, ptrs = [], [], []
-    for t in ts:
-        code = codes.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{name}: unsupported dtype {t.dtype}: use torch.bfloat16 or torch.float32")
-        if t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: tensors must be contiguous on one device")
-        got.append(code)
-        numels.append(t.numel())
-        ptrs.append(t.data_ptr())
-    return dev, got, numels, ptrs
-
-
-def _i32_array(vals: Sequence[int]):
-    return (ctypes.c_int32 * max(1, len(vals)))(*vals)
+    n = len(ts)
+    dtypes = [t.dtype for t in ts]
+    if dtypes.count(torch.bfloat16) == n:
+        codes = array("i", [MUON_BF16]) * n
+    elif dtypes.count(torch.float32) == n:
+        codes = array("i", [MUON_FP32]) * n
+    else:
+        codes = array("i", map(_dtype_code, dtypes))
+    if list(map(torch.Tensor.get_device, ts)).count(dev.index) != n or \
+            not all(map(torch.Tensor.is_contiguous, ts)):
+        raise ValueError(f"{name}: tensors must be contiguous on one device")
+    return (dev, codes, array("q", map(torch.Tensor.numel, ts)),
+            array("Q", map(torch.Tensor.data_ptr, ts)))
 
 
 def grad_workspace_bytes(numels: Sequence[int]) -> int:
@@ -480,6 +511,12 @@ def grad_workspace_bytes(numels: Sequence[int]) -> int:
     if n == SIZE_MAX:
         raise MuonError(MUON_ERR_INVALID_ARG, "muon_grad_workspace_bytes", last_error_detail())
     return int(n)
+
+
+@functools.lru_cache(maxsize=None)
+def _grad_table_bytes(batch: int) -> int:
+    # the workspace depends on the number of tensors only
+    return grad_workspace_bytes([0] * batch)
 
 
 def _norm_params(max_norm, norm_type, eps) -> GradNormParams:
@@ -520,15 +557,9 @@ def grad_norm_batched(grads: Sequence, max_norm: Optional[float] = None, norm_ty
     dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
     result = _norm_result(result, dev)
     if workspace is None:
-        workspace = _byte_workspace(grad_workspace_bytes(numels), dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.muon_grad_norm_batched(len(ptrs), _i64_array(numels), _ptr_array(ptrs),
-                                        _i32_array(codes), ctypes.byref(p),
-                                        ctypes.c_void_p(result.data_ptr()),
-                                        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                        ctypes.c_void_p(_stream_handle(dev)))
-    _check(st, "muon_grad_norm_batched")
+        workspace = _byte_workspace(_grad_table_bytes(len(grads)), dev)
+    _call(load_library().muon_grad_norm_batched, dev, workspace, len(grads), _addr(numels),
+          _addr(ptrs), _addr(codes), ctypes.byref(p), result.data_ptr())
     return result
 
 
@@ -559,14 +590,9 @@ def grad_scale_batched(grads: Sequence, scale, out: Optional[Sequence] = None,
     out, ocodes, optrs = _grad_outputs(grads, out, dev, codes, numels, ptrs)
     factor = _scale_pointer(scale, dev)
     if workspace is None:
-        workspace = _byte_workspace(grad_workspace_bytes(numels), dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.muon_grad_scale_batched(len(ptrs), _i64_array(numels), _ptr_array(ptrs),
-                                         _i32_array(codes), _ptr_array(optrs), _i32_array(ocodes),
-                                         factor, ctypes.c_void_p(workspace.data_ptr()),
-                                         workspace.numel(), ctypes.c_void_p(_stream_handle(dev)))
-    _check(st, "muon_grad_scale_batched")
+        workspace = _byte_workspace(_grad_table_bytes(len(grads)), dev)
+    _call(load_library().muon_grad_scale_batched, dev, workspace, len(grads), _addr(numels),
+          _addr(ptrs), _addr(codes), _addr(optrs), _addr(ocodes), factor)
     return out
 
 
@@ -588,15 +614,10 @@ def grad_clip_batched(grads: Sequence, max_norm: float, norm_type: float = 2.0, 
     _, ocodes, optrs = _grad_outputs(grads, out, dev, codes, numels, ptrs)
     result = _norm_result(result, dev)
     if workspace is None:
-        workspace = _byte_workspace(grad_workspace_bytes(numels), dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.muon_grad_clip_batched(len(ptrs), _i64_array(numels), _ptr_array(ptrs),
-                                        _i32_array(codes), _ptr_array(optrs), _i32_array(ocodes),
-                                        ctypes.byref(p), ctypes.c_void_p(result.data_ptr()),
-                                        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                        ctypes.c_void_p(_stream_handle(dev)))
-    _check(st, "muon_grad_clip_batched")
+        workspace = _byte_workspace(_grad_table_bytes(len(grads)), dev)
+    _call(load_library().muon_grad_clip_batched, dev, workspace, len(grads), _addr(numels),
+          _addr(ptrs), _addr(codes), _addr(optrs), _addr(ocodes), ctypes.byref(p),
+          result.data_ptr())
     return result
 
 
@@ -632,24 +653,25 @@ def _f8_pointers(ops, name, dev, shapes=None):
     """(shapes, value pointers, scale pointers) of operands; shapes: what they must be."""
     import torch
 
-    got, qs, ss = [], [], []
-    for i, (q, s) in enumerate(ops):
-        if q.dtype != torch.float8_e4m3fn or s.dtype != torch.uint8:
-            raise TypeError(f"{name}: an operand is a float8_e4m3fn tensor and a uint8 tensor")
-        if q.device != dev or s.device != dev or not q.is_contiguous() or not s.is_contiguous() \
-                or q.dim() != 2 or s.dim() != 2:
-            raise ValueError(f"{name}: operands must be contiguous 2-D tensors on one HIP device")
-        r, kp = q.shape
-        if kp % F8_BLOCK or tuple(s.shape) != (kp // F8_BLOCK, -(-r // 16) * 16):
-            raise ValueError(f"{name}: operand {i} has values {tuple(q.shape)} and scales "
+    qs, ss = [o[0] for o in ops], [o[1] for o in ops]
+    n = len(qs)
+    if [q.dtype for q in qs].count(torch.float8_e4m3fn) != n or \
+            [s.dtype for s in ss].count(torch.uint8) != n:
+        raise TypeError(f"{name}: an operand is a float8_e4m3fn tensor and a uint8 tensor")
+    if list(map(torch.Tensor.get_device, qs + ss)).count(dev.index) != 2 * n or \
+            not all(map(torch.Tensor.is_contiguous, qs + ss)):
+        raise ValueError(f"{name}: operands must be contiguous 2-D tensors on one HIP device")
+    got = [tuple(q.shape) for q in qs]
+    for i, (x, s) in enumerate(zip(got, ss)):
+        if len(x) != 2 or x[1] % F8_BLOCK or s.shape != (x[1] // F8_BLOCK, -(-x[0] // 16) * 16):
+            raise ValueError(f"{name}: operand {i} has values {x} and scales "
                              f"{tuple(s.shape)}: want (R, Kp) with Kp a multiple of {F8_BLOCK}, and "
                              "(Kp / 128, R up to a multiple of 16)")
-        if shapes is not None and (r, kp) != shapes[i]:
-            raise ValueError(f"{name}: operand {i} has values {(r, kp)}, want {shapes[i]}")
-        got.append((r, kp))
-        qs.append(q.data_ptr())
-        ss.append(s.data_ptr())
-    return got, qs, ss
+    if shapes is not None and got != shapes:
+        i = next(i for i, (x, y) in enumerate(zip(got, shapes)) if x != y)
+        raise ValueError(f"{name}: operand {i} has values {got[i]}, want {shapes[i]}")
+    return (got, array("Q", map(torch.Tensor.data_ptr, qs)),
+            array("Q", map(torch.Tensor.data_ptr, ss)))
 
 
 def f8_workspace_bytes(batch: int) -> int:
@@ -682,7 +704,7 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
         raise ValueError("out goes with normal, out_t with transpose")
     if not xs:
         return ([], []) if normal and transpose else []
-    dev = _check_tensors(xs, "xs")
+    dev = _check_matrices(xs, "xs")
     code = _dtype_code(xs[0].dtype)
     shapes = [tuple(x.shape) for x in xs]
 
@@ -693,21 +715,17 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
         if len(ops) != len(xs):
             raise ValueError(f"{name} must have one operand per matrix")
         _, q, s = _f8_pointers(ops, name, dev, [(r, -(-k // F8_BLOCK) * F8_BLOCK) for r, k in dims])
-        return ops, _ptr_array(q), _ptr_array(s)
+        return ops, q, s
 
     ops, q, s = side(normal, out, "out", shapes)
     ops_t, qt, st_ = side(transpose, out_t, "out_t", [(c, r) for r, c in shapes])
     if workspace is None:
         workspace = _byte_workspace(f8_workspace_bytes(len(xs)), dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.muon_f8_quantize_batched(len(xs), _i64_array([r for r, _ in shapes]),
-                                          _i64_array([c for _, c in shapes]),
-                                          _ptr_array([x.data_ptr() for x in xs]), code,
-                                          int(block_rows), q, s, qt, st_,
-                                          ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                          ctypes.c_void_p(_stream_handle(dev)))
-    _check(st, "muon_f8_quantize_batched")
+    rows, cols = array("q", [r for r, _ in shapes]), array("q", [c for _, c in shapes])
+    ptrs = array("Q", map(torch.Tensor.data_ptr, xs))
+    _call(load_library().muon_f8_quantize_batched, dev, workspace, len(xs), _addr(rows), _addr(cols),
+          _addr(ptrs), code, int(block_rows),
+          *(None if a is None else _addr(a) for a in (q, s, qt, st_)))
     return (ops, ops_t) if normal and transpose else ops if normal else ops_t
 
 
@@ -736,9 +754,9 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
         raise ValueError(f"a: operands must live on a HIP device, got {dev}")
     ash, aq, asc = _f8_pointers(a, "a", dev)
     bsh, bq, bsc = _f8_pointers(b, "b", dev)
-    for i, (x, y) in enumerate(zip(ash, bsh)):
-        if x[1] != y[1]:
-            raise ValueError(f"product {i}: contracted sides {x[1]} and {y[1]} differ")
+    if [x[1] for x in ash] != [y[1] for y in bsh]:
+        i = next(i for i, (x, y) in enumerate(zip(ash, bsh)) if x[1] != y[1])
+        raise ValueError(f"product {i}: contracted sides {ash[i][1]} and {bsh[i][1]} differ")
     shapes = [(x[0], y[0]) for x, y in zip(ash, bsh)]
     if out is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
@@ -750,25 +768,28 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
             raise ValueError("out must have one tensor per product")
         if out_dtype is not None and any(o.dtype != out_dtype for o in out):
             raise ValueError("out has another dtype than out_dtype")
-    if _check_tensors(out, "out") != dev:
+    if _check_matrices(out, "out") != dev:
         raise ValueError("out must live on the operands' device")
-    if any(tuple(o.shape) != s for o, s in zip(out, shapes)):
+    if [tuple(o.shape) for o in out] != shapes:
         raise ValueError("out must have the shape (rows of a, rows of b)")
     code = _dtype_code(out[0].dtype)
     if workspace is None:
         workspace = _byte_workspace(f8_workspace_bytes(len(a)), dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.muon_f8_matmul_batched(len(a), _i64_array([s[0] for s in shapes]),
-                                        _i64_array([s[1] for s in shapes]),
-                                        _i64_array([s[1] for s in ash]), _ptr_array(aq),
-                                        _ptr_array(asc), _ptr_array(bq), _ptr_array(bsc),
-                                        _ptr_array([o.data_ptr() for o in out]), code,
-                                        1 if accumulate else 0,
-                                        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                        ctypes.c_void_p(_stream_handle(dev)))
-    _check(st, "muon_f8_matmul_batched")
+    m, n = array("q", [s[0] for s in shapes]), array("q", [s[1] for s in shapes])
+    k = array("q", [s[1] for s in ash])
+    ptrs = array("Q", map(torch.Tensor.data_ptr, out))
+    _call(load_library().muon_f8_matmul_batched, dev, workspace, len(a), _addr(m), _addr(n),
+          _addr(k), _addr(aq), _addr(asc), _addr(bq), _addr(bsc), _addr(ptrs), code,
+          1 if accumulate else 0)
     return out
+
+
+def _check_matrices(ts, name):
+    """_check_tensors over whole lists at a time."""
+    dev = ts[0].device
+    if dev.type != "cuda" or not _all_same(ts, dev, ts[0].dtype) or any(t.dim() != 2 for t in ts):
+        return _check_tensors(ts, name)  # says what is wrong
+    return dev
 
 
 def hbm_stream(ins: Sequence, outs: Sequence, nontemporal: bool = False) -> None:

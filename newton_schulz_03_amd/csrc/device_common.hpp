@@ -148,6 +148,13 @@ __device__ __forceinline__ T load_const(const T* p) {
   return v;
 }
 
+// The first byte of a call's descriptor table: in the workspace, or, without
+// one, among the arguments of the kernel, whose first parameter it must be.
+__device__ __forceinline__ const char* table_base(const void* mem) {
+  return mem != nullptr ? static_cast<const char*>(mem)
+                        : (const char*)(__builtin_amdgcn_kernarg_segment_ptr());
+}
+
 // Index j with prefix[j] <= b < prefix[j+1] (b < prefix[batch]); exactly one
 // interval holds b, and empty intervals never match.  Up to kLocateScan
 // matrices the whole block finds it at once: every thread tests a few

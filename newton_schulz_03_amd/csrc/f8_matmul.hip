@@ -237,13 +237,15 @@ __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][4], char* ld
 }  // namespace
 
 template <typename T, bool ADD>
-__global__ __launch_bounds__(kThreads, 1) void k_f8_prod(F8ProdCtx c) {
+__global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) {
   __shared__ __attribute__((aligned(1024))) char smem[LDS8];
   __shared__ int slot;
   const int32_t b = xcd_remap(blockIdx.x, gridDim.x);
-  const int j = __builtin_amdgcn_readfirstlane(locate_matrix(c.prefix, c.batch, b, &slot));
-  const F8ProdDesc d = load_const(c.desc + j);
-  const int32_t t = b - load_const(c.prefix + j);
+  const char* const table = table_base(c.table);
+  const int32_t* const prefix = reinterpret_cast<const int32_t*>(table + c.prefix_off);
+  const int j = __builtin_amdgcn_readfirstlane(locate_matrix(prefix, c.batch, b, &slot));
+  const F8ProdDesc d = load_const(reinterpret_cast<const F8ProdDesc*>(table) + j);
+  const int32_t t = b - load_const(prefix + j);
   const int32_t tm = (d.m + kTile - 1) / kTile;
   const int32_t m0 = t % tm * kTile, n0 = t / tm * kTile;  // down a column of tiles: B stays
 
@@ -541,15 +543,17 @@ struct SmallShape {
 }  // namespace
 
 template <typename T, int MT, int NT>
-__global__ __launch_bounds__(kThreads) void k_f8_small(F8ProdCtx c) {
+__global__ __launch_bounds__(kThreads) void k_f8_small(ArgTable, F8ProdCtx c) {
   using S = SmallShape<MT, NT>;
   constexpr int BM = 16 * MT, BN = 16 * NT, PITCH = S::kPitch;
   __shared__ __attribute__((aligned(1024))) char smem[4 * S::kWaveBytes];
   __shared__ int slot;
   const int32_t blk = xcd_remap(blockIdx.x, gridDim.x);
-  const int j = __builtin_amdgcn_readfirstlane(locate_matrix(c.prefix, c.batch, blk, &slot));
-  const F8ProdDesc d = load_const(c.desc + j);
-  const int32_t t = blk - load_const(c.prefix + j);
+  const char* const table = table_base(c.table);
+  const int32_t* const prefix = reinterpret_cast<const int32_t*>(table + c.prefix_off);
+  const int j = __builtin_amdgcn_readfirstlane(locate_matrix(prefix, c.batch, blk, &slot));
+  const F8ProdDesc d = load_const(reinterpret_cast<const F8ProdDesc*>(table) + j);
+  const int32_t t = blk - load_const(prefix + j);
   const int32_t tm = (d.m + BM - 1) / BM;
   const int32_t m0 = t % tm * BM, n0 = t / tm * BN;
   const int lane = threadIdx.x & 63;
@@ -683,57 +687,59 @@ __global__ __launch_bounds__(kThreads) void k_f8_small(F8ProdCtx c) {
 namespace {
 
 template <typename T>
-hipError_t run_small(const F8ProdCtx& c, int32_t nblocks, int32_t mt, int32_t nt) {
+hipError_t run_small(const ArgTable& t, const F8ProdCtx& c, int32_t nblocks, int32_t mt,
+                     int32_t nt) {
   const dim3 grid(nblocks), block(kThreads);
   if (nt == 4) {
     if (mt == 1)
-      hipLaunchKernelGGL((k_f8_small<T, 1, 4>), grid, block, 0, c.stream, c);
+      hipLaunchKernelGGL((k_f8_small<T, 1, 4>), grid, block, 0, c.stream, t, c);
     else if (mt == 2)
-      hipLaunchKernelGGL((k_f8_small<T, 2, 4>), grid, block, 0, c.stream, c);
+      hipLaunchKernelGGL((k_f8_small<T, 2, 4>), grid, block, 0, c.stream, t, c);
     else
-      hipLaunchKernelGGL((k_f8_small<T, 4, 4>), grid, block, 0, c.stream, c);
+      hipLaunchKernelGGL((k_f8_small<T, 4, 4>), grid, block, 0, c.stream, t, c);
   } else if (nt == 2) {
     if (mt == 1)
-      hipLaunchKernelGGL((k_f8_small<T, 1, 2>), grid, block, 0, c.stream, c);
+      hipLaunchKernelGGL((k_f8_small<T, 1, 2>), grid, block, 0, c.stream, t, c);
     else if (mt == 2)
-      hipLaunchKernelGGL((k_f8_small<T, 2, 2>), grid, block, 0, c.stream, c);
+      hipLaunchKernelGGL((k_f8_small<T, 2, 2>), grid, block, 0, c.stream, t, c);
     else
-      hipLaunchKernelGGL((k_f8_small<T, 4, 2>), grid, block, 0, c.stream, c);
+      hipLaunchKernelGGL((k_f8_small<T, 4, 2>), grid, block, 0, c.stream, t, c);
   } else {
     if (mt == 1)
-      hipLaunchKernelGGL((k_f8_small<T, 1, 1>), grid, block, 0, c.stream, c);
+      hipLaunchKernelGGL((k_f8_small<T, 1, 1>), grid, block, 0, c.stream, t, c);
     else if (mt == 2)
-      hipLaunchKernelGGL((k_f8_small<T, 2, 1>), grid, block, 0, c.stream, c);
+      hipLaunchKernelGGL((k_f8_small<T, 2, 1>), grid, block, 0, c.stream, t, c);
     else
-      hipLaunchKernelGGL((k_f8_small<T, 4, 1>), grid, block, 0, c.stream, c);
+      hipLaunchKernelGGL((k_f8_small<T, 4, 1>), grid, block, 0, c.stream, t, c);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_f8_small(const F8ProdCtx& c, int32_t nblocks, bool is_bf16, int32_t mt,
-                           int32_t nt) {
+hipError_t launch_f8_small(const ArgTable& t, const F8ProdCtx& c, int32_t nblocks, bool is_bf16,
+                           int32_t mt, int32_t nt) {
   if (nblocks <= 0) return hipSuccess;
-  return is_bf16 ? run_small<uint16_t>(c, nblocks, mt, nt) : run_small<float>(c, nblocks, mt, nt);
+  return is_bf16 ? run_small<uint16_t>(t, c, nblocks, mt, nt)
+                 : run_small<float>(t, c, nblocks, mt, nt);
 }
 
 namespace {
 
 template <typename T>
-hipError_t run_prod(const F8ProdCtx& c, int32_t ntiles) {
+hipError_t run_prod(const ArgTable& t, const F8ProdCtx& c, int32_t ntiles) {
   if (c.accumulate)
-    hipLaunchKernelGGL((k_f8_prod<T, true>), dim3(ntiles), dim3(kThreads), 0, c.stream, c);
+    hipLaunchKernelGGL((k_f8_prod<T, true>), dim3(ntiles), dim3(kThreads), 0, c.stream, t, c);
   else
-    hipLaunchKernelGGL((k_f8_prod<T, false>), dim3(ntiles), dim3(kThreads), 0, c.stream, c);
+    hipLaunchKernelGGL((k_f8_prod<T, false>), dim3(ntiles), dim3(kThreads), 0, c.stream, t, c);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_f8_prod(const F8ProdCtx& c, int32_t ntiles, bool is_bf16) {
+hipError_t launch_f8_prod(const ArgTable& t, const F8ProdCtx& c, int32_t ntiles, bool is_bf16) {
   if (ntiles <= 0) return hipSuccess;
-  return is_bf16 ? run_prod<uint16_t>(c, ntiles) : run_prod<float>(c, ntiles);
+  return is_bf16 ? run_prod<uint16_t>(t, c, ntiles) : run_prod<float>(t, c, ntiles);
 }
 
 }  // namespace muon

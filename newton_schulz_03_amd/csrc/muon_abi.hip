@@ -49,6 +49,23 @@ int32_t check_workspace(const void* ws, size_t ws_bytes, size_t need) {
   return MUON_OK;
 }
 
+int32_t place_table(const void* desc, size_t desc_bytes, const void* prefix, size_t prefix_bytes,
+                    char* ws, hipStream_t stream, ArgTable& args, const void** mem) {
+  const size_t off = align_up(desc_bytes, kAlign), total = off + prefix_bytes;
+  if (total <= kArgTableBytes) {
+    if (desc_bytes > 0) std::memcpy(args.bytes, desc, desc_bytes);
+    std::memcpy(args.bytes + off, prefix, prefix_bytes);
+    *mem = nullptr;
+    return MUON_OK;
+  }
+  std::vector<unsigned char> t(total, 0);
+  std::memcpy(t.data(), desc, desc_bytes);
+  std::memcpy(t.data() + off, prefix, prefix_bytes);
+  *mem = ws;
+  const hipError_t e = launch_put_bytes(t.data(), total, ws, stream);
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "launch descriptor copy");
+}
+
 namespace {
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -1115,13 +1132,10 @@ int32_t adamw_batched(int32_t batch, const int64_t* numel, void* const* p, const
       return fail(MUON_ERR_INVALID_ARG, "workspace not %d-byte aligned", kAlign);
     char* ws = static_cast<char*>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    st = stage_upload(
-        pl.total_bytes,
-        [&](char* h) {
-          std::memcpy(h, pl.desc.data(), sizeof(AdamDesc) * pl.batch);
-          std::memcpy(h + pl.prefix_off, pl.prefix.data(), sizeof(int32_t) * pl.prefix.size());
-        },
-        ws, s);
+    ArgTable table;
+    AdamCtx c{};
+    st = place_table(pl.desc.data(), sizeof(AdamDesc) * pl.batch, pl.prefix.data(),
+                     sizeof(int32_t) * pl.prefix.size(), ws, s, table, &c.table);
     if (st != MUON_OK) return st;
     const double t = static_cast<double>(prm->step);
     const double bc1 = 1.0 - std::pow(static_cast<double>(prm->beta1), t);
@@ -1136,13 +1150,11 @@ int32_t adamw_batched(int32_t batch, const int64_t* numel, void* const* p, const
     a.inv_bc2_sqrt = static_cast<float>(1.0 / std::sqrt(bc2));
     a.eps = prm->eps;
     a.g_scale = g_scale;
-    AdamCtx c{};
-    c.desc = reinterpret_cast<const AdamDesc*>(ws);
-    c.prefix = reinterpret_cast<const int32_t*>(ws + pl.prefix_off);
+    c.prefix_off = static_cast<int32_t>(pl.prefix_off);
     c.batch = pl.batch;
     c.stream = s;
     TimedLaunch tl(MUON_K_ADAMW, s);
-    hipError_t e = launch_adamw(c, pl.prefix[pl.batch], pl.bf16, a);
+    hipError_t e = launch_adamw(table, c, pl.prefix[pl.batch], pl.bf16, a);
     if (e != hipSuccess) return hip_fail(e, "launch adamw");
     tl.done();
     return MUON_OK;

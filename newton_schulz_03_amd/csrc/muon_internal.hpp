@@ -139,6 +139,13 @@ __host__ __device__ __forceinline__ char* f8_buffer(const MatDesc& d, int k) {
   return static_cast<char*>(d.poly) + sb + k * f8_buffer_bytes(d.s_pad, d.l_pad);
 }
 
+// A descriptor table that travels as a kernel's first argument: a call whose
+// table fits needs no launch to write it to the workspace first.
+constexpr size_t kArgTableBytes = 3840;  // of the 4096 a kernel's arguments may have
+struct alignas(16) ArgTable {
+  unsigned char bytes[kArgTableBytes];
+};
+
 // AdamW over a ragged batch of flat tensors.
 struct AdamDesc {
   void* p;          // parameters (T), updated in place
@@ -148,9 +155,10 @@ struct AdamDesc {
   int64_t numel;
 };
 
+// The table is the descriptors, then (at prefix_off) batch+1 block prefixes.
 struct AdamCtx {
-  const AdamDesc* desc;    // device copy of the descriptors
-  const int32_t* prefix;   // device: batch+1 block prefixes
+  const void* table;       // device copy of the table; null: it is the argument table
+  int32_t prefix_off;
   int32_t batch;
   hipStream_t stream;
 };
@@ -166,7 +174,8 @@ struct AdamParams {
 };
 
 int64_t adamw_blocks(int64_t numel);
-hipError_t launch_adamw(const AdamCtx& c, int32_t nblocks, bool is_bf16, const AdamParams& a);
+hipError_t launch_adamw(const ArgTable& t, const AdamCtx& c, int32_t nblocks, bool is_bf16,
+                        const AdamParams& a);
 
 // Global gradient norm, clip factor and scaled gradients over a ragged batch.
 // Every tensor is cut into chunks of kGradSpan elements, numbered through the
@@ -179,22 +188,12 @@ struct GradDesc {
   int64_t numel;
   int32_t in_bf16, out_bf16;  // element types: bf16 or fp32
 };
+// The table is the descriptors, then (at prefix_off) batch+1 chunk prefixes.
 struct GradCtx {
-  const GradDesc* desc;    // device copy of the descriptors
-  const int32_t* prefix;   // device: batch+1 chunk prefixes
+  const void* table;       // device copy of the table; null: it is the argument table
+  int32_t prefix_off;
   int32_t batch;
-};
-// Up to kGradInline tensors travel as kernel arguments: no table to write first.
-constexpr int kGradInline = 32;
-struct GradInline {
-  GradDesc desc[kGradInline];
-  int32_t prefix[kGradInline + 1];
-  int32_t batch;
-};
-struct GradTable {
-  bool in_args;
-  GradCtx mem;
-  GradInline args;
+  hipStream_t stream;
 };
 struct GradNormArgs {
   float* result;     // device: norm, clip factor
@@ -202,10 +201,18 @@ struct GradNormArgs {
   int32_t chunks;
   int32_t clip;      // 0: the factor is 1
   float max_norm, eps;
+  int32_t keep_partials;  // 1: the scale pass joins the partials
 };
-// kind 0: L2, 1: largest magnitude.
-hipError_t launch_grad_norm(const GradTable& t, const GradNormArgs& p, int32_t kind, hipStream_t s);
-hipError_t launch_grad_scale(const GradTable& t, int32_t chunks, const float* scale, hipStream_t s);
+// kind 0: L2, 1: largest magnitude.  bytes: of the gradients (norm), of the
+// gradients and the outputs (scale).
+hipError_t launch_grad_norm(const ArgTable& t, const GradCtx& c, const GradNormArgs& p,
+                            int32_t kind, int64_t bytes);
+// joined: the factor comes from the partials of that norm (keep_partials set,
+// grad_few_blocks), not from `scale`.
+hipError_t launch_grad_scale(const ArgTable& t, const GradCtx& c, int32_t chunks,
+                             const float* scale, const GradNormArgs* joined, int32_t kind,
+                             int64_t bytes);
+bool grad_few_blocks(int32_t chunks);
 
 // Block-scaled e4m3 operands for products outside the step.  An operand of
 // R rows contracted over K columns: values R x Kp bytes (Kp = K up to a
@@ -220,13 +227,14 @@ struct F8QuantDesc {
   int32_t rows, cols;
 };
 struct F8QuantCtx {
-  const F8QuantDesc* desc;
-  const int32_t* prefix;   // device: batch+1 block prefixes
+  const void* table;       // as GradCtx: descriptors, batch+1 block prefixes
+  int32_t prefix_off;
   int32_t batch;
   hipStream_t stream;
 };
-hipError_t launch_f8_quantize(const F8QuantCtx& c, int32_t nblocks, bool is_bf16,
-                              int32_t block_rows);
+// bytes: of the matrices.
+hipError_t launch_f8_quantize(const ArgTable& t, const F8QuantCtx& c, int32_t nblocks, bool is_bf16,
+                              int32_t block_rows, int64_t bytes);
 
 // C = A B^T (+ C) over such operands.
 struct F8ProdDesc {
@@ -237,17 +245,17 @@ struct F8ProdDesc {
   int32_t reserved;
 };
 struct F8ProdCtx {
-  const F8ProdDesc* desc;
-  const int32_t* prefix;   // device: batch+1 tile prefixes
+  const void* table;       // as GradCtx: descriptors, batch+1 tile prefixes of each kernel
+  int32_t prefix_off;      // of the prefixes of the kernel launched
   int32_t batch;
   int32_t accumulate;
   hipStream_t stream;
 };
-hipError_t launch_f8_prod(const F8ProdCtx& c, int32_t ntiles, bool is_bf16);
+hipError_t launch_f8_prod(const ArgTable& t, const F8ProdCtx& c, int32_t ntiles, bool is_bf16);
 constexpr int kF8Tile = 256;  // output tile (both sides)
 // The kernel of few rows: blocks of 16 mt x 16 nt, mt in {1, 2, 4}, nt in {1, 4}.
-hipError_t launch_f8_small(const F8ProdCtx& c, int32_t nblocks, bool is_bf16, int32_t mt,
-                           int32_t nt);
+hipError_t launch_f8_small(const ArgTable& t, const F8ProdCtx& c, int32_t nblocks, bool is_bf16,
+                           int32_t mt, int32_t nt);
 
 // Host launchers (one per kernel family).  is_bf16 selects the element type.
 // Momentum (step), U into X ping and the per-block sums of U^2.

@@ -21,14 +21,18 @@ std::mutex g_scratch_mu;
 std::map<int, char*> g_scratch_base;
 
 // Bytes carried by one launch of the copy kernel, as its arguments.
-constexpr uint32_t kPutChunk = 2048;
-struct PutChunk {
+constexpr uint32_t kPutChunk = 3840;
+struct alignas(16) PutChunk {
   unsigned char bytes[kPutChunk];
 };
 
 __global__ __launch_bounds__(kThreads) void k_put_bytes(PutChunk c, unsigned char* dst,
                                                         uint32_t n) {
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads) dst[i] = c.bytes[i];
+  // whole dwords (dst is at least 256-byte aligned), then what is left
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(c.bytes);
+  uint32_t* to = reinterpret_cast<uint32_t*>(dst);
+  for (uint32_t i = threadIdx.x; i < n / 4; i += kThreads) to[i] = from[i];
+  for (uint32_t i = n / 4 * 4 + threadIdx.x; i < n; i += kThreads) dst[i] = c.bytes[i];
 }
 
 }  // namespace

@@ -1,7 +1,6 @@
 // C ABI of the operators around the step: the gradient norm and clip, the
-// block-scaled e4m3 operands and their product.  Descriptor tables travel as
-// kernel arguments, so a call enqueues kernel launches only and can be captured
-// into a graph.
+// block-scaled e4m3 operands and their product.  A call enqueues kernel launches
+// only (place_table), so that it can be captured into a graph.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -17,11 +16,15 @@ namespace {
 // ---------------------------------------------------------------------------
 // Gradient norm and clip
 // ---------------------------------------------------------------------------
+// The scale pass numbers four blocks per chunk.
+constexpr int64_t kMaxChunks = INT32_MAX / 4;
+
 struct GradPlan {
   std::vector<GradDesc> desc;
   std::vector<int32_t> prefix;
   size_t prefix_off = 0, partials_off = 0, total_bytes = 0;
   int32_t chunks = 0;
+  int64_t in_bytes = 0, out_bytes = 0;
 };
 
 int32_t make_grad_plan(int32_t batch, const int64_t* numel, GradPlan& pl) {
@@ -35,7 +38,7 @@ int32_t make_grad_plan(int32_t batch, const int64_t* numel, GradPlan& pl) {
       return fail(MUON_ERR_INVALID_ARG, "tensor %d: numel %lld is negative", i,
                   static_cast<long long>(numel[i]));
     pl.desc[i].numel = numel[i];
-    if (numel[i] / kGradSpan > INT32_MAX - total - 1)
+    if (numel[i] / kGradSpan > kMaxChunks - total - 1)
       return fail(MUON_ERR_UNSUPPORTED, "batch needs more than 2^31 blocks");
     total += (numel[i] + kGradSpan - 1) / kGradSpan;
     pl.prefix[i + 1] = static_cast<int32_t>(total);
@@ -74,6 +77,8 @@ int32_t bind_grads(int32_t batch, const void* const* g, const int32_t* dtype, vo
       d.out_bf16 = out_dtype[i] == MUON_BF16;
     }
     if (d.numel == 0) continue;
+    pl.in_bytes += d.numel * (d.in_bf16 ? 2 : 4);
+    pl.out_bytes += d.numel * (d.out_bf16 ? 2 : 4);
     if (d.g == nullptr || d.out == nullptr)
       return fail(MUON_ERR_INVALID_ARG, "tensor %d: null device pointer", i);
     if (!aligned16(d.g) || !aligned16(d.out))
@@ -103,27 +108,16 @@ int32_t check_float_ptr(const void* p, const char* what) {
   return MUON_OK;
 }
 
-// The table: among the kernel arguments, or written to the workspace.
-int32_t grad_table(const GradPlan& pl, char* ws, hipStream_t s, GradTable& t) {
-  const int32_t batch = static_cast<int32_t>(pl.desc.size());
-  t.in_args = batch <= kGradInline;
-  if (t.in_args) {
-    std::copy(pl.desc.begin(), pl.desc.end(), t.args.desc);
-    std::copy(pl.prefix.begin(), pl.prefix.end(), t.args.prefix);
-    t.args.batch = batch;
-    return MUON_OK;
-  }
-  t.mem.desc = reinterpret_cast<const GradDesc*>(ws);
-  t.mem.prefix = reinterpret_cast<const int32_t*>(ws + pl.prefix_off);
-  t.mem.batch = batch;
-  hipError_t e = launch_put_bytes(pl.desc.data(), sizeof(GradDesc) * batch, ws, s);
-  if (e == hipSuccess)
-    e = launch_put_bytes(pl.prefix.data(), sizeof(int32_t) * pl.prefix.size(), ws + pl.prefix_off, s);
-  return e == hipSuccess ? MUON_OK : hip_fail(e, "launch descriptor copy");
+int32_t grad_table(const GradPlan& pl, char* ws, hipStream_t s, ArgTable& t, GradCtx& c) {
+  c.batch = static_cast<int32_t>(pl.desc.size());
+  c.prefix_off = static_cast<int32_t>(pl.prefix_off);
+  c.stream = s;
+  return place_table(pl.desc.data(), sizeof(GradDesc) * pl.desc.size(), pl.prefix.data(),
+                     sizeof(int32_t) * pl.prefix.size(), ws, s, t, &c.table);
 }
 
-int32_t run_norm(const GradPlan& pl, const GradTable& t, const muon_grad_norm_params& p,
-                 float* result, char* ws, hipStream_t s) {
+GradNormArgs norm_args(const GradPlan& pl, const muon_grad_norm_params& p, float* result,
+                       char* ws) {
   GradNormArgs a{};
   a.result = result;
   a.partials = ws + pl.partials_off;
@@ -131,16 +125,23 @@ int32_t run_norm(const GradPlan& pl, const GradTable& t, const muon_grad_norm_pa
   a.clip = p.clip;
   a.max_norm = p.max_norm;
   a.eps = p.eps;
-  TimedLaunch tl(MUON_K_GRAD_NORM, s);
-  const hipError_t e = launch_grad_norm(t, a, p.kind, s);
+  return a;
+}
+
+int32_t run_norm(const GradPlan& pl, const ArgTable& t, const GradCtx& c, const GradNormArgs& a,
+                 int32_t kind) {
+  TimedLaunch tl(MUON_K_GRAD_NORM, c.stream);
+  const hipError_t e = launch_grad_norm(t, c, a, kind, pl.in_bytes);
   if (e != hipSuccess) return hip_fail(e, "launch gradient norm");
   tl.done();
   return MUON_OK;
 }
 
-int32_t run_scale(const GradPlan& pl, const GradTable& t, const float* scale, hipStream_t s) {
-  TimedLaunch tl(MUON_K_GRAD_SCALE, s);
-  const hipError_t e = launch_grad_scale(t, pl.chunks, scale, s);
+int32_t run_scale(const GradPlan& pl, const ArgTable& t, const GradCtx& c, const float* scale,
+                  const GradNormArgs* joined = nullptr, int32_t kind = 0) {
+  TimedLaunch tl(MUON_K_GRAD_SCALE, c.stream);
+  const hipError_t e =
+      launch_grad_scale(t, c, pl.chunks, scale, joined, kind, pl.in_bytes + pl.out_bytes);
   if (e != hipSuccess) return hip_fail(e, "launch gradient scale");
   tl.done();
   return MUON_OK;
@@ -248,17 +249,6 @@ int32_t plan_products(const std::vector<F8ProdDesc>& desc, bool bf16, std::vecto
   return MUON_OK;
 }
 
-template <typename D>
-int32_t put_f8_table(const std::vector<D>& desc, const std::vector<int32_t>& prefix, char* ws,
-                     hipStream_t s) {
-  const size_t off = f8_desc_bytes(static_cast<int32_t>(desc.size()));
-  std::vector<char> t(off + sizeof(int32_t) * prefix.size(), 0);
-  std::memcpy(t.data(), desc.data(), sizeof(D) * desc.size());
-  std::memcpy(t.data() + off, prefix.data(), sizeof(int32_t) * prefix.size());
-  const hipError_t e = launch_put_bytes(t.data(), t.size(), ws, s);
-  return e == hipSuccess ? MUON_OK : hip_fail(e, "launch descriptor copy");
-}
-
 }  // namespace
 }  // namespace muon
 
@@ -291,9 +281,10 @@ extern "C" int32_t muon_grad_norm_batched(int32_t batch, const int64_t* numel,
     if ((st = check_workspace(workspace, workspace_bytes, pl.total_bytes)) != MUON_OK) return st;
     char* ws = static_cast<char*>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    GradTable t;
-    if ((st = grad_table(pl, ws, s, t)) != MUON_OK) return st;
-    return run_norm(pl, t, *p, result, ws, s);
+    ArgTable t;
+    GradCtx c{};
+    if ((st = grad_table(pl, ws, s, t, c)) != MUON_OK) return st;
+    return run_norm(pl, t, c, norm_args(pl, *p, result, ws), p->kind);
   } catch (...) {
     return fail(MUON_ERR_HIP, "unexpected host exception");
   }
@@ -315,9 +306,10 @@ extern "C" int32_t muon_grad_scale_batched(int32_t batch, const int64_t* numel,
     if ((st = bind_grads(batch, g, dtype, out, out_dtype, pl)) != MUON_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, pl.total_bytes)) != MUON_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    GradTable t;
-    if ((st = grad_table(pl, static_cast<char*>(workspace), s, t)) != MUON_OK) return st;
-    return run_scale(pl, t, scale, s);
+    ArgTable t;
+    GradCtx c{};
+    if ((st = grad_table(pl, static_cast<char*>(workspace), s, t, c)) != MUON_OK) return st;
+    return run_scale(pl, t, c, scale);
   } catch (...) {
     return fail(MUON_ERR_HIP, "unexpected host exception");
   }
@@ -341,10 +333,13 @@ extern "C" int32_t muon_grad_clip_batched(int32_t batch, const int64_t* numel,
     if ((st = check_workspace(workspace, workspace_bytes, pl.total_bytes)) != MUON_OK) return st;
     char* ws = static_cast<char*>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    GradTable t;
-    if ((st = grad_table(pl, ws, s, t)) != MUON_OK) return st;
-    if ((st = run_norm(pl, t, *p, result, ws, s)) != MUON_OK) return st;
-    return run_scale(pl, t, result + 1, s);
+    ArgTable t;
+    GradCtx c{};
+    if ((st = grad_table(pl, ws, s, t, c)) != MUON_OK) return st;
+    GradNormArgs a = norm_args(pl, *p, result, ws);
+    a.keep_partials = grad_few_blocks(pl.chunks) ? 1 : 0;
+    if ((st = run_norm(pl, t, c, a, p->kind)) != MUON_OK) return st;
+    return run_scale(pl, t, c, result + 1, a.keep_partials ? &a : nullptr, p->kind);
   } catch (...) {
     return fail(MUON_ERR_HIP, "unexpected host exception");
   }
@@ -381,7 +376,7 @@ extern "C" int32_t muon_f8_quantize_batched(int32_t batch, const int64_t* rows,
       return fail(MUON_ERR_INVALID_ARG, "rows/cols/x array is null");
     std::vector<F8QuantDesc> desc(batch);
     std::vector<int32_t> prefix(static_cast<size_t>(batch) + 1, 0);
-    int64_t total = 0;
+    int64_t total = 0, bytes = 0;
     int32_t st;
     for (int32_t i = 0; i < batch; ++i) {
       if ((st = check_f8_dim(rows[i], "rows", i)) != MUON_OK) return st;
@@ -409,18 +404,21 @@ extern "C" int32_t muon_f8_quantize_batched(int32_t batch, const int64_t* rows,
       if ((st = add_blocks(cdiv(rows[i], kF8Block), cdiv(cols[i], kF8Block), total)) != MUON_OK)
         return st;
       prefix[i + 1] = static_cast<int32_t>(total);
+      bytes += rows[i] * cols[i] * (dtype == MUON_BF16 ? 2 : 4);
     }
     if ((st = check_workspace(workspace, workspace_bytes, f8_ws_bytes(batch))) != MUON_OK) return st;
     char* ws = static_cast<char*>(workspace);
     hipStream_t stm = static_cast<hipStream_t>(stream);
-    if ((st = put_f8_table(desc, prefix, ws, stm)) != MUON_OK) return st;
+    ArgTable t;
     F8QuantCtx c{};
-    c.desc = reinterpret_cast<const F8QuantDesc*>(ws);
-    c.prefix = reinterpret_cast<const int32_t*>(ws + f8_desc_bytes(batch));
+    if ((st = place_table(desc.data(), sizeof(F8QuantDesc) * batch, prefix.data(),
+                          sizeof(int32_t) * prefix.size(), ws, stm, t, &c.table)) != MUON_OK)
+      return st;
+    c.prefix_off = static_cast<int32_t>(align_up(sizeof(F8QuantDesc) * batch, kAlign));
     c.batch = batch;
     c.stream = stm;
     TimedLaunch tl(MUON_K_F8_QUANTIZE, stm);
-    const hipError_t e = launch_f8_quantize(c, prefix[batch], dtype == MUON_BF16, block_rows);
+    const hipError_t e = launch_f8_quantize(t, c, prefix[batch], dtype == MUON_BF16, block_rows, bytes);
     if (e != hipSuccess) return hip_fail(e, "launch e4m3 quantization");
     tl.done();
     return MUON_OK;
@@ -485,17 +483,19 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
     hipStream_t stm = static_cast<hipStream_t>(stream);
     std::vector<int32_t> prefix(big);
     prefix.insert(prefix.end(), small.begin(), small.end());
-    if ((st = put_f8_table(desc, prefix, ws, stm)) != MUON_OK) return st;
+    ArgTable t;
     F8ProdCtx x{};
-    x.desc = reinterpret_cast<const F8ProdDesc*>(ws);
-    x.prefix = reinterpret_cast<const int32_t*>(ws + f8_desc_bytes(batch));
+    if ((st = place_table(desc.data(), sizeof(F8ProdDesc) * batch, prefix.data(),
+                          sizeof(int32_t) * prefix.size(), ws, stm, t, &x.table)) != MUON_OK)
+      return st;
+    x.prefix_off = static_cast<int32_t>(align_up(sizeof(F8ProdDesc) * batch, kAlign));
     x.batch = batch;
     x.accumulate = accumulate;
     x.stream = stm;
     TimedLaunch tl(MUON_K_F8_PROD, stm);
-    hipError_t e = launch_f8_prod(x, big[batch], dtype == MUON_BF16);
-    x.prefix += batch + 1;
-    if (e == hipSuccess) e = launch_f8_small(x, small[batch], dtype == MUON_BF16, sp.mt, sp.nt);
+    hipError_t e = launch_f8_prod(t, x, big[batch], dtype == MUON_BF16);
+    x.prefix_off += static_cast<int32_t>(sizeof(int32_t)) * (batch + 1);
+    if (e == hipSuccess) e = launch_f8_small(t, x, small[batch], dtype == MUON_BF16, sp.mt, sp.nt);
     if (e != hipSuccess) return hip_fail(e, "launch e4m3 product");
     tl.done();
     return MUON_OK;

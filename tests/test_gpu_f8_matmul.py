@@ -126,8 +126,9 @@ def test_quantize_ragged(dtype, block_rows):
             assert torch.equal(a.scales, b.scales)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("block_rows", [1, 128])
-def test_quantize_edges_of_the_range(block_rows):
+def test_quantize_edges_of_the_range(block_rows, dtype):
     # block maxima at the steps of the scale, ties between e4m3 values, the
     # largest and smallest fp32 values, zeros, infinities and NaNs
     x = torch.zeros((150, 400))
@@ -147,6 +148,7 @@ def test_quantize_edges_of_the_range(block_rows):
     x[23, 300:310] = math.nan
     x[24, 256:384] = -math.inf
     x[140, 390] = math.nan
+    x = x.to(dtype)
     h = x.double().numpy()
     ops, ops_t = nsa.f8_quantize_batched([x.cuda()], block_rows=block_rows, transpose=True)
     check_operand(ops[0], h, block_rows, "range")

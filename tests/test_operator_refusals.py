@@ -10,7 +10,7 @@ import torch
 
 import newton_schulz_03_amd as nsa
 from newton_schulz_03_amd._binding import (AdamWParams, GradNormParams, NsParams, StepParams,
-                                           _i32_array, _i64_array, _ptr_array)
+                                           _i64_array, _ptr_array)
 
 FAKE = 0x7f0000000000
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
@@ -19,6 +19,10 @@ OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
 @pytest.fixture(scope="module")
 def lib():
     return nsa.load_library()
+
+
+def _i32_array(vals):
+    return (ctypes.c_int32 * max(1, len(vals)))(*vals)
 
 
 def up(x, a):
@@ -140,7 +144,7 @@ def test_scaled_steps_refuse_a_missing_factor(lib):
 
 def test_f8_workspace():
     for n in (0, 1, 7, 384):
-        assert nsa.f8_workspace_bytes(n) == up(56 * n, 256) + up(4 * (n + 1), 256)
+        assert nsa.f8_workspace_bytes(n) == up(56 * n, 256) + up(2 * 4 * (n + 1), 256)
     with pytest.raises(nsa.MuonError):
         nsa.f8_workspace_bytes(-1)
 
