@@ -24,7 +24,7 @@
 // one: what they give is not stored.
 //   The first matrix operand (P) is B, the second (Q) A: a lane's registers
 // then run along a row of C.  LDS row 128 h + 32 i + r holds the tile's row
-// 128 h + 4 r + i, so that lane r of fragment i works on row 4 r + i: the
+// 128 h + 4 r + i (RowStream), so that lane r of fragment i works on row 4 r + i: the
 // scales of a lane's four fragments are one aligned dword of the scale row
 // (op_sel picks the byte), and a lane's registers hold 16 consecutive columns
 // of C for each of its rows.
@@ -40,7 +40,6 @@ static_assert(kF8Tile == kTile, "the pipeline's tile");
 constexpr int SCB = 256;                   // scale bytes per operand and stage
 constexpr int STAGE8 = 2 * OPB + 2 * SCB;  // P data, Q data, P scales, Q scales
 constexpr int LDS8 = NST * STAGE8;
-constexpr int LOADS8 = 2 * LPO + 1;        // loads per wave and stage: P, then scales, then Q
 static_assert(LDS8 + 1024 <= 160 * 1024, "LDS of a CU");
 
 typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
@@ -64,16 +63,14 @@ __device__ __forceinline__ i32x4_t make_rsrc(const uint8_t* base, uint32_t bytes
   return r;
 }
 
-// Tile row held by LDS row s (0 .. 255).
-__device__ __forceinline__ int tile_row(int s) {
-  return (s & 128) + 4 * (s & 31) + ((s >> 5) & 3);
-}
-
-// One operand's rows of the tile, 64 bytes of each per slice.
+// One operand's 64 N rows of the tile (N = 4, or 2 for A in a half tile), 64
+// bytes of each per slice.  LDS row 32 (N h + i) + r holds tile row
+// 32 N h + N r + i.
+template <int N>
 struct RowStream {
   const uint8_t* base;  // the tile's first row (uniform)
   uint32_t bytes;       // of the tile's rows that exist
-  int32_t voff[LPO];    // per-lane offsets, one per load instruction
+  int32_t voff[N];      // per-lane offsets, one per load instruction
   int32_t lds;          // LDS offset of this wave's first 1 KiB block, within the operand
 
   __device__ __forceinline__ void init(const uint8_t* rows0, int32_t valid, int32_t kp, int wave,
@@ -81,12 +78,12 @@ struct RowStream {
     base = rows0;
     bytes = static_cast<uint32_t>(valid) * static_cast<uint32_t>(kp);
 #pragma unroll
-    for (int u = 0; u < LPO; ++u) {
-      const int s = 16 * (LPO * wave + u) + (lane >> 2);
-      const int row = tile_row(s);
+    for (int u = 0; u < N; ++u) {
+      const int s = 16 * (N * wave + u) + (lane >> 2);
+      const int row = s / (32 * N) * (32 * N) + N * (s & 31) + (s >> 5) % N;
       voff[u] = (row < valid ? row : valid - 1) * kp + (((lane & 3) ^ kkey(s)) << 4);
     }
-    lds = LPO * wave * 1024;
+    lds = N * wave * 1024;
   }
   __device__ __forceinline__ i32x4_t rsrc(int ks) const {
     return make_rsrc(base + 64 * ks, bytes - 64u * ks);
@@ -97,7 +94,7 @@ struct RowStream {
   __device__ __forceinline__ void issue(int ks, uint32_t stage_op) const {
     const i32x4_t r = rsrc(ks);
 #pragma unroll
-    for (int u = 0; u < LPO; ++u) issue_one(r, stage_op, u);
+    for (int u = 0; u < N; ++u) issue_one(r, stage_op, u);
   }
 };
 
@@ -124,9 +121,10 @@ struct ScaleRows {
   }
 };
 
+template <int NQ>
 struct Frags8 {
   i32x8_t p[4];    // dwords 0-3: chunk h of the 64-byte row, 4-7: chunk 2 + h
-  i32x8_t q[4];
+  i32x8_t q[NQ];
   int32_t sp, sq;  // byte i: the scale of fragment i's row
 };
 
@@ -159,16 +157,16 @@ __device__ __forceinline__ void set_half(i32x8_t& f, int h, const u32x4_t& v) {
   for (int k = 0; k < 4; ++k) f[4 * h + k] = static_cast<int32_t>(v[k]);
 }
 
-// Stores the wave's 128 x 128 part of the tile, whose first element is row m0,
-// column n0 of C.  acc[mi][ni][4 g + e] of lane (lr, lh) is row 4 lr + ni,
+// Stores the wave's 32 NQ x 128 part of the tile, whose first element is row
+// m0, column n0 of C.  acc[mi][ni][4 g + e] of lane (lr, lh) is row NQ lr + ni,
 // column 4 (8 g + 4 lh + e) + mi.  The 32 rows of one ni go through 16 KiB of
 // LDS of the wave's own in fp32, four columns (the four mi) a 16-byte chunk,
 // chunk c of row r at c ^ r; they come out as whole rows, so that every store
 // covers full 128-byte lines (written from the accumulators, 16 bytes a row,
 // the store ran at 2.5 TB/s).  ADD: the old C of one ni is requested while the
 // one before it is stored.
-template <typename T, bool ADD>
-__device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][4], char* lds, T* c, int32_t m0,
+template <typename T, bool ADD, int NQ>
+__device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][NQ], char* lds, T* c, int32_t m0,
                                            int32_t n0, int32_t m, int32_t n, int lane) {
   constexpr int V = Elt<T>::kVec;            // columns per lane: 16 bytes
   constexpr int LPR = 128 / V;               // lanes per row
@@ -184,13 +182,13 @@ __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][4], char* ld
   auto request = [&](int ni, u32x4_t* to) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int32_t r = 4 * (RPI * i + rr0) + ni;
+      const int32_t r = NQ * (RPI * i + rr0) + ni;
       if (fast && m0 + r < m) to[i] = ld16(corner + static_cast<int64_t>(r) * n);
     }
   };
   if constexpr (ADD) request(0, old[0]);
 #pragma unroll
-  for (int ni = 0; ni < 4; ++ni) {
+  for (int ni = 0; ni < NQ; ++ni) {
 #pragma unroll
     for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -202,7 +200,7 @@ __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][4], char* ld
       }
     __builtin_amdgcn_wave_barrier();
     if constexpr (ADD)
-      if (ni < 3) request(ni + 1, old[(ni + 1) & 1]);
+      if (ni + 1 < NQ) request(ni + 1, old[(ni + 1) & 1]);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int rr = RPI * i + rr0;
@@ -213,7 +211,7 @@ __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][4], char* ld
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
       }
-      const int32_t r = 4 * rr + ni;
+      const int32_t r = NQ * rr + ni;
       if (m0 + r >= m || col >= n) continue;
       T* const to = corner + static_cast<int64_t>(r) * n;
       if (fast) {
@@ -234,39 +232,30 @@ __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][4], char* ld
   }
 }
 
-}  // namespace
-
-template <typename T, bool ADD>
-__global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) {
-  __shared__ __attribute__((aligned(1024))) char smem[LDS8];
-  __shared__ int slot;
-  const int32_t b = xcd_remap(blockIdx.x, gridDim.x);
-  const char* const table = table_base(c.table);
-  const int32_t* const prefix = reinterpret_cast<const int32_t*>(table + c.prefix_off);
-  const int j = __builtin_amdgcn_readfirstlane(locate_matrix(prefix, c.batch, b, &slot));
-  const F8ProdDesc d = load_const(reinterpret_cast<const F8ProdDesc*>(table) + j);
-  const int32_t t = b - load_const(prefix + j);
-  const int32_t tm = (d.m + kTile - 1) / kTile;
-  const int32_t m0 = t % tm * kTile, n0 = t / tm * kTile;  // down a column of tiles: B stays
-
+// One tile: 256 columns of C from n0, 64 NQ rows from m0.
+template <typename T, bool ADD, int NQ>
+__device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32_t n0, char* smem) {
+  constexpr int kRows = 64 * NQ;
+  constexpr int kLoads = 4 + NQ + 1;  // per wave and stage: P, then scales, then Q
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int lr = lane & 31, lh = lane >> 5;
 
-  f32x16_t acc[4][4];
+  f32x16_t acc[4][NQ];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < NQ; ++k)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][k][e] = 0.f;
 
   const int nk = d.kp / 64;
   if (nk > 0) {
-    RowStream sp, sq;
+    RowStream<4> sp;
+    RowStream<NQ> sq;
     sp.init(d.b + static_cast<int64_t>(n0) * d.kp, min(kTile, d.n - n0), d.kp, wave, lane);
-    sq.init(d.a + static_cast<int64_t>(m0) * d.kp, min(kTile, d.m - m0), d.kp, wave, lane);
+    sq.init(d.a + static_cast<int64_t>(m0) * d.kp, min(kRows, d.m - m0), d.kp, wave, lane);
     ScaleRows ss;
     if (wave & 1)
       ss.init(d.sa, m0, d.m, wave, lane);
@@ -277,29 +266,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) 
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       const int sw = ((2 * sub + lh) ^ kkey(lr)) << 4;
-      qoff[sub] = OPB + (wn * 128 + lr) * KROW + sw;
+      qoff[sub] = OPB + (wn * 32 * NQ + lr) * KROW + sw;
       poff[sub] = (wm * 128 + lr) * KROW + sw;
     }
     const int32_t psc = 2 * OPB + 4 * (32 * wm + lr);
-    const int32_t qsc = 2 * OPB + SCB + 4 * (32 * wn + lr);
-
-    // Fragment reads in the order the MFMAs consume them: the scales, P[0],
-    // Q[0..3], then P[1..3]; two 16-byte reads per fragment.
-    constexpr int NREAD8 = 18;
-    auto read_op = [&](Frags8& f, const char* stage, int i) {
-      if (i == 0) {
-        f.sp = *reinterpret_cast<const int32_t*>(stage + psc);
-      } else if (i == 1) {
-        f.sq = *reinterpret_cast<const int32_t*>(stage + qsc);
-      } else if (i < 4) {
-        set_half(f.p[0], i - 2, lds16(stage + poff[i - 2]));
-      } else if (i < 12) {
-        const int ni = (i - 4) >> 1, h = (i - 4) & 1;
-        set_half(f.q[ni], h, lds16(stage + qoff[h] + ni * 32 * KROW));
-      } else {
-        const int mi = 1 + ((i - 12) >> 1), h = (i - 12) & 1;
-        set_half(f.p[mi], h, lds16(stage + poff[h] + mi * 32 * KROW));
-      }
+    const int32_t qsc = 2 * OPB + SCB + NQ * (32 * wn + lr);
+    auto q_scales = [&](const char* stage) -> int32_t {
+      if constexpr (NQ == 4)
+        return *reinterpret_cast<const int32_t*>(stage + qsc);
+      else
+        return *reinterpret_cast<const uint16_t*>(stage + qsc);
     };
 
     const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LDS_AS char*)smem));
@@ -313,52 +289,64 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) 
       ss.issue(ks, ring + s * STAGE8);
       sq.issue(ks, ring + s * STAGE8 + OPB);
     }
-    wait_vm<(NST - 2) * LOADS8>();
+    wait_vm<(NST - 2) * kLoads>();
     __syncthreads();
 
     if constexpr (sizeof(T) == 2) {
-      Frags8 f0, f1;
-  #pragma unroll
-      for (int i = 0; i < NREAD8; ++i) read_op(f0, smem, i);
+      // Fragment reads in the order the MFMAs consume them: the scales, P[0],
+      // the Qs, then P[1..3]; two 16-byte reads per fragment.
+      constexpr int kReads = 2 + 2 * (4 + NQ), kHalf = 2 * NQ;  // MFMAs: 2 kHalf a slice
+      auto read_op = [&](Frags8<NQ>& f, const char* stage, int i) {
+        if (i == 0) {
+          f.sp = *reinterpret_cast<const int32_t*>(stage + psc);
+        } else if (i == 1) {
+          f.sq = q_scales(stage);
+        } else if (i < 4) {
+          set_half(f.p[0], i - 2, lds16(stage + poff[i - 2]));
+        } else if (i < 4 + 2 * NQ) {
+          const int ni = (i - 4) >> 1, h = (i - 4) & 1;
+          set_half(f.q[ni], h, lds16(stage + qoff[h] + ni * 32 * KROW));
+        } else {
+          const int mi = 1 + ((i - 4 - 2 * NQ) >> 1), h = (i - 4) & 1;
+          set_half(f.p[mi], h, lds16(stage + poff[h] + mi * 32 * KROW));
+        }
+      };
+      Frags8<NQ> f0, f1;
+#pragma unroll
+      for (int i = 0; i < kReads; ++i) read_op(f0, smem, i);
 
       // Slice kt on fragments fa (stage kt), reading stage kt+1 into fb.
-      auto slice = [&](int kt, Frags8& fa, Frags8& fb) {
+      auto slice = [&](int kt, Frags8<NQ>& fa, Frags8<NQ>& fb) {
         const int ks = kt + NST - 1 < nk ? kt + NST - 1 : nk - 1;
         const uint32_t fill = ring + ((kt + NST - 1) & (NST - 1)) * STAGE8;
         const i32x4_t rp = sp.rsrc(ks);
-        static_for(
-            [&](auto I) {
-              constexpr int i = decltype(I)::value;
-              if constexpr ((i & 1) == 0) sp.issue_one(rp, fill, i >> 1);
-              if constexpr (i == 7) ss.issue(ks, fill);
-              acc[i >> 2][i & 3] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                  fa.p[i >> 2], fa.q[i & 3], acc[i >> 2][i & 3], 0, 0, i >> 2, fa.sp, i & 3, fa.sq);
-              __builtin_amdgcn_sched_barrier(0);
-            },
-            std::make_integer_sequence<int, 8>{});
+        static_for<kHalf>([&](auto I) {
+          constexpr int i = decltype(I)::value, mi = i / NQ, ni = i % NQ;
+          if constexpr (i % (kHalf / 4) == 0) sp.issue_one(rp, fill, i / (kHalf / 4));
+          if constexpr (i == kHalf - 1) ss.issue(ks, fill);
+          acc[mi][ni] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              fa.p[mi], fa.q[ni], acc[mi][ni], 0, 0, mi, fa.sp, ni, fa.sq);
+          __builtin_amdgcn_sched_barrier(0);
+        });
         // slice kt+1 has landed once only slice kt+2 and the P and scale loads of
         // kt+NST-1 remain
-        wait_vm<(NST - 3) * LOADS8 + LPO + 1>();
+        wait_vm<(NST - 3) * kLoads + 4 + 1>();
         wait_lgkm0();  // this wave's reads of stage kt+NST-1's previous slice are done
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
         const i32x4_t rq = sq.rsrc(ks);
         const char* next = smem + ((kt + 1) & (NST - 1)) * STAGE8;
-        static_for(
-            [&](auto I) {
-              constexpr int i = 8 + decltype(I)::value;
-              constexpr int j = decltype(I)::value;
-              if constexpr ((j & 1) == 0) sq.issue_one(rq, fill + OPB, j >> 1);
-              // 18 reads over 8 MFMAs: three in the first two, two in the rest
-              constexpr int r0 = j < 2 ? 3 * j : 6 + 2 * (j - 2);
-              constexpr int r1 = j < 2 ? 3 * j + 3 : 6 + 2 * (j - 1);
-  #pragma unroll
-              for (int r = r0; r < r1; ++r) read_op(fb, next, r);
-              acc[i >> 2][i & 3] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                  fa.p[i >> 2], fa.q[i & 3], acc[i >> 2][i & 3], 0, 0, i >> 2, fa.sp, i & 3, fa.sq);
-              __builtin_amdgcn_sched_barrier(0);
-            },
-            std::make_integer_sequence<int, 8>{});
+        static_for<kHalf>([&](auto I) {
+          constexpr int j = decltype(I)::value, i = kHalf + j, mi = i / NQ, ni = i % NQ;
+          if constexpr ((j & 1) == 0) sq.issue_one(rq, fill + OPB, j >> 1);
+          constexpr int r0 = (j * kReads + kHalf - 1) / kHalf;
+          constexpr int r1 = ((j + 1) * kReads + kHalf - 1) / kHalf;
+#pragma unroll
+          for (int r = r0; r < r1; ++r) read_op(fb, next, r);
+          acc[mi][ni] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              fa.p[mi], fa.q[ni], acc[mi][ni], 0, 0, mi, fa.sp, ni, fa.sq);
+          __builtin_amdgcn_sched_barrier(0);
+        });
       };
       // nk is even: the operands' K is padded to whole blocks of 128
       for (int kt = 0; kt < nk; kt += 2) {
@@ -367,10 +355,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) 
       }
     } else {
       // Fragments of slice kt are converted one step ahead of the MFMAs that take
-      // them, between MFMAs.  On entry to a slice: Q[0..2] and P[0] converted,
-      // Q[3] raw.
-      Wide qb[4], pb[2];
-      i32x8_t rq[4], rp;
+      // them, between MFMAs.  On entry to a slice: P[0] and the Qs but the last
+      // converted, the last Q raw.  A quarter of a slice is one P fragment.
+      constexpr int kQuarter = 4 * NQ, kPer = 4 / NQ;  // dwords converted per MFMA
+      constexpr int kLast = NQ - 1;
+      Wide qb[NQ], pb[2];
+      i32x8_t rq[NQ], rp;
       int32_t ssp, ssq, nsp = 0, nsq = 0;
       auto load_q = [&](const char* stage, int ni, int h) {
         set_half(rq[ni], h, lds16(stage + qoff[h] + ni * 32 * KROW));
@@ -381,9 +371,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) 
       auto widen_q = [&](int ni, int d, int32_t sc) { widen(qb[ni], d, rq[ni][d], scale_value(sc, ni)); };
       auto widen_p = [&](int mi, int d, int32_t sc) { widen(pb[mi & 1], d, rp[d], scale_value(sc, mi)); };
       ssp = *reinterpret_cast<const int32_t*>(smem + psc);
-      ssq = *reinterpret_cast<const int32_t*>(smem + qsc);
+      ssq = q_scales(smem);
 #pragma unroll
-      for (int ni = 0; ni < 4; ++ni)
+      for (int ni = 0; ni < NQ; ++ni)
 #pragma unroll
         for (int h = 0; h < 2; ++h) load_q(smem, ni, h);
 #pragma unroll
@@ -391,7 +381,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) 
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
 #pragma unroll
-        for (int ni = 0; ni < 3; ++ni) widen_q(ni, d, ssq);
+        for (int ni = 0; ni < kLast; ++ni) widen_q(ni, d, ssq);
         widen_p(0, d, ssp);
       }
       for (int kt = 0; kt < nk; ++kt) {
@@ -400,13 +390,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) 
         const char* cur = smem + (kt & (NST - 1)) * STAGE8;
         const char* next = smem + ((kt + 1) & (NST - 1)) * STAGE8;
         const i32x4_t rsp = sp.rsrc(ks), rsq = sq.rsrc(ks);
-        static_for<64>([&](auto I) {
+        static_for<4 * kQuarter>([&](auto I) {
           constexpr int i = decltype(I)::value;
-          constexpr int mi = i >> 4, ni = (i >> 2) & 3, s = i & 3, j = i & 15;
-          if constexpr (i == 48) {
+          constexpr int mi = i / kQuarter, ni = (i >> 2) % NQ, s = i & 3, j = i % kQuarter;
+          if constexpr (i == 3 * kQuarter) {
             // slice kt+1 has landed once only slice kt+2 and kt+NST-1 remain; this
             // wave has read all it needs of stage kt
-            wait_vm<(NST - 2) * LOADS8>();
+            wait_vm<(NST - 2) * kLoads>();
             wait_lgkm0();
             __syncthreads();
             __builtin_amdgcn_sched_barrier(0);
@@ -414,28 +404,34 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) 
           if constexpr (mi < 3) {
             // the next P fragment: read, then converted half a quarter later
             if constexpr (j < 2) load_p(cur, mi + 1, j);
-            if constexpr (j >= 8) widen_p(mi + 1, j - 8, ssp);
-            // Q[3], before its first use
-            if constexpr (mi == 0 && j < 8) widen_q(3, j, ssq);
+            if constexpr (j >= kQuarter / 2)
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) widen_p(mi + 1, (j - kQuarter / 2) * kPer + k, ssp);
+            // the last Q, before its first use
+            if constexpr (mi == 0 && j < kQuarter / 2)
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) widen_q(kLast, j * kPer + k, ssq);
           } else {
-            // slice kt+1: scales, Q[0..3], P[0]
+            // slice kt+1: scales, the Qs, P[0]
             if constexpr (j == 0) {
               nsp = *reinterpret_cast<const int32_t*>(next + psc);
-              nsq = *reinterpret_cast<const int32_t*>(next + qsc);
+              nsq = q_scales(next);
             }
-            if constexpr (j < 4) {
+            if constexpr (j < NQ) {
               load_q(next, j, 0);
               load_q(next, j, 1);
             }
-            if constexpr (j >= 4 && j < 6) load_p(next, 0, j - 4);
-            if constexpr (j >= 4) {  // Q[ni - 1] has had its last MFMA
+            if constexpr (j >= NQ && j < NQ + 2) load_p(next, 0, j - NQ);
+            if constexpr (ni > 0) {  // Q[ni - 1] has had its last MFMA
               widen_q(ni - 1, 2 * s, nsq);
               widen_q(ni - 1, 2 * s + 1, nsq);
             }
-            if constexpr (j >= 8) widen_p(0, j - 8, nsp);
+            if constexpr (j >= kQuarter / 2)
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) widen_p(0, (j - kQuarter / 2) * kPer + k, nsp);
           }
-          if constexpr (mi == 1 && (j & 3) == 0) sp.issue_one(rsp, fill, j >> 2);
-          if constexpr (mi == 1 && j == 14) ss.issue(ks, fill);
+          if constexpr (mi == 1 && j % NQ == 0) sp.issue_one(rsp, fill, j / NQ);
+          if constexpr (mi == 1 && j == kQuarter - 2) ss.issue(ks, fill);
           if constexpr (mi == 2 && (j & 3) == 0) sq.issue_one(rsq, fill + OPB, j >> 2);
           acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pb[mi & 1].v[s], qb[ni].v[s],
                                                                 acc[mi][ni], 0, 0, 0);
@@ -448,8 +444,35 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c) 
     wait_vm<0>();  // no load may still target LDS: the ring is reused for the store
   }
   __syncthreads();
-  store_part<T, ADD>(acc, smem + wave * 16384, static_cast<T*>(d.c), m0 + 128 * wn, n0 + 128 * wm,
-                     d.m, d.n, lane);
+  store_part<T, ADD, NQ>(acc, smem + wave * 16384, static_cast<T*>(d.c), m0 + 32 * NQ * wn,
+                         n0 + 128 * wm, d.m, d.n, lane);
+}
+
+}  // namespace
+
+// The launch's tiles: full ones of 256 x 256 first, then half ones of 128 x 256
+// (F8ProdDesc::full: the product's rows of full tiles; the half ones follow
+// them), which end ragged products and fill the launch's last round.  Both add
+// every element up the same way.
+template <typename T, bool ADD>
+__global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c, int32_t nfull) {
+  __shared__ __attribute__((aligned(1024))) char smem[LDS8];
+  __shared__ int slot;
+  const char* const table = table_base(c.table);
+  const bool half = static_cast<int32_t>(blockIdx.x) >= nfull;
+  const int32_t* const prefix =
+      reinterpret_cast<const int32_t*>(table + c.prefix_off) + (half ? c.batch + 1 : 0);
+  const int32_t b = half ? xcd_remap(blockIdx.x - nfull, gridDim.x - nfull) : xcd_remap(blockIdx.x, nfull);
+  const int j = __builtin_amdgcn_readfirstlane(locate_matrix(prefix, c.batch, b, &slot));
+  const F8ProdDesc d = load_const(reinterpret_cast<const F8ProdDesc*>(table) + j);
+  const int32_t t = b - load_const(prefix + j);
+  // down a column of tiles: B stays
+  if (!half) {
+    prod_tile<T, ADD, 4>(d, t % d.full * kTile, t / d.full * kTile, smem);
+  } else {
+    const int32_t halves = (d.m - d.full * kTile + kTile / 2 - 1) / (kTile / 2);
+    prod_tile<T, ADD, 2>(d, d.full * kTile + t % halves * (kTile / 2), t / halves * kTile, smem);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -727,19 +750,21 @@ hipError_t launch_f8_small(const ArgTable& t, const F8ProdCtx& c, int32_t nblock
 namespace {
 
 template <typename T>
-hipError_t run_prod(const ArgTable& t, const F8ProdCtx& c, int32_t ntiles) {
+hipError_t run_prod(const ArgTable& t, const F8ProdCtx& c, int32_t nfull, int32_t nhalf) {
+  const dim3 grid(nfull + nhalf);
   if (c.accumulate)
-    hipLaunchKernelGGL((k_f8_prod<T, true>), dim3(ntiles), dim3(kThreads), 0, c.stream, t, c);
+    hipLaunchKernelGGL((k_f8_prod<T, true>), grid, dim3(kThreads), 0, c.stream, t, c, nfull);
   else
-    hipLaunchKernelGGL((k_f8_prod<T, false>), dim3(ntiles), dim3(kThreads), 0, c.stream, t, c);
+    hipLaunchKernelGGL((k_f8_prod<T, false>), grid, dim3(kThreads), 0, c.stream, t, c, nfull);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_f8_prod(const ArgTable& t, const F8ProdCtx& c, int32_t ntiles, bool is_bf16) {
-  if (ntiles <= 0) return hipSuccess;
-  return is_bf16 ? run_prod<uint16_t>(t, c, ntiles) : run_prod<float>(t, c, ntiles);
+hipError_t launch_f8_prod(const ArgTable& t, const F8ProdCtx& c, int32_t nfull, int32_t nhalf,
+                          bool is_bf16) {
+  if (nfull + nhalf <= 0) return hipSuccess;
+  return is_bf16 ? run_prod<uint16_t>(t, c, nfull, nhalf) : run_prod<float>(t, c, nfull, nhalf);
 }
 
 }  // namespace muon

@@ -94,9 +94,8 @@ template <> struct Sub<uint16_t> {
     r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, hi), scale, true);
     return __builtin_bit_cast(uint32_t, r);
   }
-  template <bool NT>
   __device__ __forceinline__ void load_row(int p, const uint16_t* g) {
-    const u32x4_t v = NT ? ld16_nt(g) : ld16(g);
+    const u32x4_t v = ld16(g);
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[p][k] = v[k];
   }
@@ -135,9 +134,8 @@ template <> struct Sub<float> {
     r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(c), __uint_as_float(d), scale, true);
     return __builtin_bit_cast(uint32_t, r);
   }
-  template <bool NT>
   __device__ __forceinline__ void load_row(int p, const float* g) {
-    const u32x4_t v = NT ? ld16_nt(g) : ld16(g), w = NT ? ld16_nt(g + 4) : ld16(g + 4);
+    const u32x4_t v = ld16(g), w = ld16(g + 4);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       x[p][k] = v[k];
@@ -192,11 +190,10 @@ __device__ __forceinline__ void maxima(const Sub<T>& s, uint32_t* row, uint32_t*
 // 8 (t % 16) .. + 7 of the tile: 16 lanes cover a row's 128 columns, and the
 // 8 rows of a column are 8 bytes of the transpose.  Tiles without infinities
 // and NaNs, which the block votes on, skip the selects that set them apart.
-// NT: x is read with the nontemporal hint, and of two outputs one written with
-// it.  16 bf16 matrices of 2048 x 6144 (403 MB in, 406 out): 121 us, 6.6 TB/s;
-// with the hint on the loads alone 152, on everything 146, on nothing 151.  32
-// batches of 256 rows (101 MB in) just written by another kernel: 34 us without
-// the hint, 38 with it.
+// NT: the values are stored with the nontemporal hint, for outputs that outgrow
+// the caches.  16 matrices of 2048 x 6144 from memory, both outputs: bf16 144 us
+// (5.6 TB/s) with the hint on the stores, 149 without, 150 on the loads alone;
+// fp32 214, 221 and 244 us.
 template <typename T, bool SQUARE, bool NT>
 __global__ __launch_bounds__(kThreads) void k_f8_quantize(ArgTable, F8QuantCtx c) {
   using S = Sub<T>;
@@ -220,13 +217,13 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(ArgTable, F8QuantCtx c
   const T* const x = static_cast<const T*>(d.x) + static_cast<int64_t>(r0 + 8 * rg) * d.cols + col;
   if (vec && r0 + kQ <= d.rows) {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) s.template load_row<NT>(p, x + static_cast<int64_t>(p) * d.cols);
+    for (int p = 0; p < 8; ++p) s.load_row(p, x + static_cast<int64_t>(p) * d.cols);
   } else {
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const int n = r0 + 8 * rg + p < d.rows ? min(8, d.cols - col) : 0;
       if (vec && n > 0)
-        s.template load_row<NT>(p, x + static_cast<int64_t>(p) * d.cols);
+        s.load_row(p, x + static_cast<int64_t>(p) * d.cols);
       else
         s.load_some(p, x + static_cast<int64_t>(p) * d.cols, n);
     }
@@ -279,7 +276,12 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(ArgTable, F8QuantCtx c
         u32x2_t w;
         w[0] = s.along_row(p, 0, scale);
         w[1] = s.along_row(p, 1, scale);
-        *(GLOBAL_AS u32x2_t*)(d.q + static_cast<int64_t>(row) * kp + col) = w;
+        GLOBAL_AS u32x2_t* const to =
+            (GLOBAL_AS u32x2_t*)(d.q + static_cast<int64_t>(row) * kp + col);
+        if constexpr (NT)
+          __builtin_nontemporal_store(w, to);
+        else
+          *to = w;
       }
     }
   }
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(ArgTable, F8QuantCtx c
       if (c0 + cc >= d.cols) continue;
       uint8_t* const to = d.qt + static_cast<int64_t>(c0 + cc) * kp + r0 + 16 * i;
       const u32x4_t v = *reinterpret_cast<const u32x4_t*>(tr + cc * 144 + ((i ^ (cc >> 4)) << 4));
-      if (NT && d.q != nullptr)
+      if constexpr (NT)
         st16_nt(to, v);
       else
         st16(to, v);

@@ -242,16 +242,19 @@ struct F8ProdDesc {
   const uint8_t *b, *sb;   // n rows
   void* c;                 // m x n, bf16 or fp32
   int32_t m, n, kp;        // kp: the operands' padded K
-  int32_t reserved;
+  int32_t full;            // rows of full tiles in the large-tile kernel; half tiles follow
 };
 struct F8ProdCtx {
-  const void* table;       // as GradCtx: descriptors, batch+1 tile prefixes of each kernel
+  const void* table;       // as GradCtx: descriptors, then batch+1 prefixes of full tiles,
+                           // of half tiles and of the few-rows kernel's blocks
   int32_t prefix_off;      // of the prefixes of the kernel launched
   int32_t batch;
   int32_t accumulate;
   hipStream_t stream;
 };
-hipError_t launch_f8_prod(const ArgTable& t, const F8ProdCtx& c, int32_t ntiles, bool is_bf16);
+// Two prefix arrays: full tiles (nfull of them), half tiles.
+hipError_t launch_f8_prod(const ArgTable& t, const F8ProdCtx& c, int32_t nfull, int32_t nhalf,
+                          bool is_bf16);
 constexpr int kF8Tile = 256;  // output tile (both sides)
 // The kernel of few rows: blocks of 16 mt x 16 nt, mt in {1, 2, 4}, nt in {1, 4}.
 hipError_t launch_f8_small(const ArgTable& t, const F8ProdCtx& c, int32_t nblocks, bool is_bf16,

@@ -165,7 +165,7 @@ size_t f8_desc_bytes(int32_t batch) {
                   kAlign);
 }
 size_t f8_ws_bytes(int32_t batch) {
-  return f8_desc_bytes(batch) + align_up(2 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1), kAlign);
+  return f8_desc_bytes(batch) + align_up(3 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1), kAlign);
 }
 
 int32_t check_ptr(const void* p, const char* what, int32_t i) {
@@ -200,8 +200,65 @@ struct SmallPlan {
   int32_t mt = 1, nt = 4;
 };
 
-int32_t plan_products(const std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int32_t>& big,
-                      std::vector<int32_t>& small, SmallPlan& sp) {
+// Rounds that F full tiles and then H half ones take on the chip, in full tiles.
+constexpr double kHalfCost = 0.58;
+double rounds(int64_t f, int64_t h) {
+  const int64_t cus = static_cast<int64_t>(kCus), q = f / cus, r = f % cus;
+  const double t = static_cast<double>(q);
+  if (h == 0) return t + (r > 0 ? 1.0 : 0.0);
+  const double alone = kHalfCost * static_cast<double>(cdiv(h, cus - r));
+  if (r == 0) return t + alone;
+  if (alone <= 1.0) return t + 1.0;
+  return t + std::max(1.0, (static_cast<double>(r) + kHalfCost * static_cast<double>(h)) / kCus + 0.5 * kHalfCost);
+}
+
+// Rows of full and half tiles of the products that the large-tile kernel takes:
+// a rest of up to 128 rows is one half tile, and where it shortens the launch's
+// last round, the last full tiles become two half ones each.
+void cut_rows(std::vector<F8ProdDesc>& desc, const std::vector<char>& large) {
+  int64_t f = 0, h = 0;
+  for (size_t i = 0; i < desc.size(); ++i) {
+    F8ProdDesc& d = desc[i];
+    if (!large[i]) continue;
+    const int32_t rest = d.m % kF8Tile;
+    d.full = d.m / kF8Tile + (rest > kF8Tile / 2 ? 1 : 0);
+    const int64_t tn = cdiv(d.n, kF8Tile);
+    f += d.full * tn;
+    h += rest > 0 && rest <= kF8Tile / 2 ? tn : 0;
+  }
+  // one row of tiles at a time, from the end, as long as a whole last round's
+  // worth has not been split
+  const int64_t most = f % static_cast<int64_t>(kCus);
+  double best = rounds(f, h);
+  int64_t take = 0, bf = f, bh = h, taken = 0;
+  for (size_t i = desc.size(); i-- > 0 && taken < most;) {
+    if (!large[i]) continue;
+    const F8ProdDesc& d = desc[i];
+    const int64_t tn = cdiv(d.n, kF8Tile);
+    for (int32_t k = 0; k < d.full && taken < most; ++k) {
+      // the last full row may hold fewer than 256 rows, but more than 128
+      taken += tn;
+      bf -= tn;
+      bh += 2 * tn;
+      if (const double r = rounds(bf, bh); r < best) {
+        best = r;
+        take = taken;
+      }
+    }
+  }
+  for (size_t i = desc.size(); i-- > 0 && take > 0;) {
+    if (!large[i]) continue;
+    F8ProdDesc& d = desc[i];
+    const int64_t tn = cdiv(d.n, kF8Tile);
+    while (d.full > 0 && take > 0) {
+      --d.full;
+      take -= tn;
+    }
+  }
+}
+
+int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int32_t>& full,
+                      std::vector<int32_t>& half, std::vector<int32_t>& small, SmallPlan& sp) {
   double tiles = 0, slices = 0, blocks = 0, steps = 0;
   int32_t few_rows = 0;
   for (const F8ProdDesc& d : desc) {
@@ -233,17 +290,24 @@ int32_t plan_products(const std::vector<F8ProdDesc>& desc, bool bf16, std::vecto
     if (d.m > 0 && (d.m <= kFewRows || all_small))
       n64 += static_cast<double>(cdiv(d.m, 16 * sp.mt)) * static_cast<double>(cdiv(d.n, 64));
   sp.nt = n64 >= 96 ? 4 : n64 >= 48 ? 2 : 1;
-  int64_t nb = 0, ns = 0;
+  std::vector<char> large(desc.size(), 0);
+  for (size_t i = 0; i < desc.size(); ++i) large[i] = desc[i].m > kFewRows && !all_small;
+  cut_rows(desc, large);
+  int64_t nf = 0, nh = 0, ns = 0;
   int32_t st;
   for (size_t i = 0; i < desc.size(); ++i) {
     const F8ProdDesc& d = desc[i];
-    if (d.m > 0) {
-      st = d.m <= kFewRows || all_small
-               ? add_blocks(cdiv(d.m, 16 * sp.mt), cdiv(d.n, 16 * sp.nt), ns)
-               : add_blocks(cdiv(d.m, kF8Tile), cdiv(d.n, kF8Tile), nb);
-      if (st != MUON_OK) return st;
+    if (large[i]) {
+      const int64_t tn = cdiv(d.n, kF8Tile);
+      const int64_t left = std::max<int64_t>(0, d.m - static_cast<int64_t>(d.full) * kF8Tile);
+      if ((st = add_blocks(d.full, tn, nf)) != MUON_OK) return st;
+      if ((st = add_blocks(cdiv(left, kF8Tile / 2), tn, nh)) != MUON_OK) return st;
+      if (nf + nh > INT32_MAX) return fail(MUON_ERR_UNSUPPORTED, "batch needs more than 2^31 blocks");
+    } else if (d.m > 0) {
+      if ((st = add_blocks(cdiv(d.m, 16 * sp.mt), cdiv(d.n, 16 * sp.nt), ns)) != MUON_OK) return st;
     }
-    big[i + 1] = static_cast<int32_t>(nb);
+    full[i + 1] = static_cast<int32_t>(nf);
+    half[i + 1] = static_cast<int32_t>(nh);
     small[i + 1] = static_cast<int32_t>(ns);
   }
   return MUON_OK;
@@ -446,7 +510,7 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
       return fail(MUON_ERR_INVALID_ARG, "an argument array is null");
     std::vector<F8ProdDesc> desc(batch);
     // tiles of the two kernels, each product's in one of them
-    std::vector<int32_t> big(static_cast<size_t>(batch) + 1, 0), small(big);
+    std::vector<int32_t> full(static_cast<size_t>(batch) + 1, 0), half(full), small(full);
     int32_t st;
     for (int32_t i = 0; i < batch; ++i) {
       if ((st = check_f8_dim(m[i], "m", i)) != MUON_OK) return st;
@@ -477,11 +541,12 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
       }
     }
     SmallPlan sp;
-    if ((st = plan_products(desc, dtype == MUON_BF16, big, small, sp)) != MUON_OK) return st;
+    if ((st = plan_products(desc, dtype == MUON_BF16, full, half, small, sp)) != MUON_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, f8_ws_bytes(batch))) != MUON_OK) return st;
     char* ws = static_cast<char*>(workspace);
     hipStream_t stm = static_cast<hipStream_t>(stream);
-    std::vector<int32_t> prefix(big);
+    std::vector<int32_t> prefix(full);
+    prefix.insert(prefix.end(), half.begin(), half.end());
     prefix.insert(prefix.end(), small.begin(), small.end());
     ArgTable t;
     F8ProdCtx x{};
@@ -493,8 +558,8 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
     x.accumulate = accumulate;
     x.stream = stm;
     TimedLaunch tl(MUON_K_F8_PROD, stm);
-    hipError_t e = launch_f8_prod(t, x, big[batch], dtype == MUON_BF16);
-    x.prefix_off += static_cast<int32_t>(sizeof(int32_t)) * (batch + 1);
+    hipError_t e = launch_f8_prod(t, x, full[batch], half[batch], dtype == MUON_BF16);
+    x.prefix_off += 2 * static_cast<int32_t>(sizeof(int32_t)) * (batch + 1);
     if (e == hipSuccess) e = launch_f8_small(t, x, small[batch], dtype == MUON_BF16, sp.mt, sp.nt);
     if (e != hipSuccess) return hip_fail(e, "launch e4m3 product");
     tl.done();

@@ -181,8 +181,11 @@ def operands(shapes, seed, b_rows=1):
 
 def check_product(c, a, b, old=None, what=""):
     x, y = values(a), values(b)
-    want = x @ y.T
-    mag = np.abs(x) @ np.abs(y).T
+    if x.shape[0] * y.shape[0] * x.shape[1] > 1 << 28:  # the same in float64 on the device
+        dx, dy = torch.from_numpy(x).cuda(), torch.from_numpy(y).cuda().t().contiguous()
+        want, mag = (dx @ dy).cpu().numpy(), (dx.abs() @ dy.abs()).cpu().numpy()
+    else:
+        want, mag = x @ y.T, np.abs(x) @ np.abs(y).T
     acc = x.shape[1] * 2.0 ** -23 * mag
     if c.dtype == BF16:
         acc = acc + 2.0 ** -10 * mag
@@ -217,6 +220,42 @@ def test_matmul_ragged(out, accumulate):
         assert got[i] is c[i]
         check_product(c[i], a[i], b[i], old[i] if accumulate else None, s)
         assert (room[i][:16] == 3).all() and (room[i][16 + s[0] * s[1]:] == 3).all(), s
+
+
+# enough work for the 256 x 256 tiles: rests of rows below and above 128, of
+# columns, odd numbers of K blocks, a single one and none
+LARGE = [(700, 2100, 1500), (1290, 1030, 2048), (257, 2050, 128), (129, 1000, 900), (128, 2304, 1300),
+         (384, 1024, 1100), (513, 777, 0), (70, 2000, 2000), (1024, 1025, 640), (33, 600, 700)]
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_matmul_large_tiles(out, accumulate):
+    a, b = operands(LARGE, 2000, b_rows=128)
+    room = [torch.full((16 + m * n + 16,), 3.0, dtype=out, device="cuda") for m, n, _ in LARGE]
+    c = [r[16:16 + m * n].view(m, n) for r, (m, n, _) in zip(room, LARGE)]
+    g = torch.Generator().manual_seed(5)
+    for x in c:
+        x.copy_(torch.randn(tuple(x.shape), generator=g))
+    old = [host_f64(x) for x in c]
+    nsa.f8_matmul_batched(a, b, out=c, accumulate=accumulate)
+    torch.cuda.synchronize()
+    for i, s in enumerate(LARGE):
+        check_product(c[i], a[i], b[i], old[i] if accumulate else None, s)
+        assert (room[i][:16] == 3).all() and (room[i][16 + s[0] * s[1]:] == 3).all(), s
+
+
+@pytest.mark.parametrize("tiles", [255, 257, 300, 513])
+def test_matmul_last_round_in_half_tiles(tiles):
+    # one row of tiles more or less than whole rounds of the chip: the bits of a
+    # row of C do not depend on where its tile ends
+    (a,), (b,) = operands([(256 * tiles - 100, 200, 256)], 3000 + tiles)
+    for out in (BF16, FP32):
+        (c,) = nsa.f8_matmul_batched([a], [b], out_dtype=out)
+        rows = torch.randperm(256 * tiles - 100, generator=torch.Generator().manual_seed(1))[:600]
+        rows = torch.cat([rows, torch.arange(256 * tiles - 400, 256 * tiles - 100)])
+        part = (a.q[rows.cuda()], a.scales[:, rows.cuda()].contiguous())
+        check_product(c[rows.cuda()], (part[0], part[1]), b, what=tiles)
 
 
 @pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 31, 33, 48, 64, 65, 100, 129, 200])
