@@ -17,11 +17,13 @@
 //    2^-133), and v_mfma_f32_32x32x16_bf16 sums them with fp32 precision, at
 //    half the matrix rate.
 //
-// 256 x 256 tiles, four waves of 128 x 128, K in slices of 64 through an LDS
-// ring of 4 stages filled by direct-to-LDS loads (gemm_pipeline.hpp's slice
-// loop and swizzle).  The operands are row-major; a slice takes 64 bytes of
-// each of the tile's 256 rows.  Rows past the operand's end repeat its last
-// one: what they give is not stored.
+// 256 x 256 tiles, four waves of 128 x 128, K in blocks of 128 through two LDS
+// buffers filled by direct-to-LDS loads, each block in two slices of 64.  The
+// operands are row-major, and a load instruction takes the whole 128-byte lines
+// of 8 rows: with 64-byte pieces of 16 rows and four buffers of 64 the L2 served
+// twice the requests and the loop ran 15% slower (16 products 1024 x 2048 x
+// 6144: 217 us against 184 with whole lines).  Rows past the operand's end
+// repeat its last one: what they give is not stored.
 //   The first matrix operand (P) is B, the second (Q) A: a lane's registers
 // then run along a row of C.  LDS row 128 h + 32 i + r holds the tile's row
 // 128 h + 4 r + i (RowStream), so that lane r of fragment i works on row 4 r + i: the
@@ -37,9 +39,11 @@ namespace muon {
 namespace {
 
 static_assert(kF8Tile == kTile, "the pipeline's tile");
-constexpr int SCB = 256;                   // scale bytes per operand and stage
-constexpr int STAGE8 = 2 * OPB + 2 * SCB;  // P data, Q data, P scales, Q scales
-constexpr int LDS8 = NST * STAGE8;
+constexpr int LROW = kF8Block;             // bytes of an LDS row: one K block of one row
+constexpr int OPB8 = kTile * LROW;         // 32 KiB per operand and buffer
+constexpr int SCB = 256;                   // scale bytes per operand and buffer
+constexpr int BUF8 = 2 * OPB8 + 2 * SCB;   // P data, Q data, P scales, Q scales
+constexpr int LDS8 = 2 * BUF8;
 static_assert(LDS8 + 1024 <= 160 * 1024, "LDS of a CU");
 
 typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
@@ -63,14 +67,16 @@ __device__ __forceinline__ i32x4_t make_rsrc(const uint8_t* base, uint32_t bytes
   return r;
 }
 
-// One operand's 64 N rows of the tile (N = 4, or 2 for A in a half tile), 64
-// bytes of each per slice.  LDS row 32 (N h + i) + r holds tile row
-// 32 N h + N r + i.
+// One operand's 64 N rows of the tile (N = 4, or 2 for A in a half tile), 128
+// bytes of each per block.  LDS row 32 (N h + i) + r holds tile row
+// 32 N h + N r + i, its 16-byte chunk c at c ^ ((r / 2) % 8): the rows of a
+// fragment read then fall on distinct banks.
 template <int N>
 struct RowStream {
+  static constexpr int kLoads = 2 * N;  // per wave and block
   const uint8_t* base;  // the tile's first row (uniform)
   uint32_t bytes;       // of the tile's rows that exist
-  int32_t voff[N];      // per-lane offsets, one per load instruction
+  int32_t voff[kLoads];  // per-lane offsets, one per load instruction
   int32_t lds;          // LDS offset of this wave's first 1 KiB block, within the operand
 
   __device__ __forceinline__ void init(const uint8_t* rows0, int32_t valid, int32_t kp, int wave,
@@ -78,23 +84,23 @@ struct RowStream {
     base = rows0;
     bytes = static_cast<uint32_t>(valid) * static_cast<uint32_t>(kp);
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const int s = 16 * (N * wave + u) + (lane >> 2);
+    for (int u = 0; u < kLoads; ++u) {
+      const int s = 8 * (kLoads * wave + u) + (lane >> 3);
       const int row = s / (32 * N) * (32 * N) + N * (s & 31) + (s >> 5) % N;
-      voff[u] = (row < valid ? row : valid - 1) * kp + (((lane & 3) ^ kkey(s)) << 4);
+      voff[u] = (row < valid ? row : valid - 1) * kp + (((lane & 7) ^ ((s >> 1) & 7)) << 4);
     }
-    lds = N * wave * 1024;
+    lds = kLoads * wave * 1024;
   }
-  __device__ __forceinline__ i32x4_t rsrc(int ks) const {
-    return make_rsrc(base + 64 * ks, bytes - 64u * ks);
+  __device__ __forceinline__ i32x4_t rsrc(int kb) const {
+    return make_rsrc(base + static_cast<int64_t>(kb) * kF8Block, bytes - static_cast<uint32_t>(kF8Block) * kb);
   }
-  __device__ __forceinline__ void issue_one(const i32x4_t& r, uint32_t stage_op, int u) const {
-    lds_dma16(__builtin_amdgcn_readfirstlane(stage_op + lds + u * 1024), voff[u], r);
+  __device__ __forceinline__ void issue_one(const i32x4_t& r, uint32_t at, int u) const {
+    lds_dma16(__builtin_amdgcn_readfirstlane(at + lds + u * 1024), voff[u], r);
   }
-  __device__ __forceinline__ void issue(int ks, uint32_t stage_op) const {
-    const i32x4_t r = rsrc(ks);
+  __device__ __forceinline__ void issue(int kb, uint32_t at) const {
+    const i32x4_t r = rsrc(kb);
 #pragma unroll
-    for (int u = 0; u < N; ++u) issue_one(r, stage_op, u);
+    for (int u = 0; u < kLoads; ++u) issue_one(r, at, u);
   }
 };
 
@@ -113,17 +119,17 @@ struct ScaleRows {
     rp = (rows + 15) & ~15;
     const int32_t last = rp - 4 - row0;
     voff = 4 * lane < last ? 4 * lane : last;
-    lds = 2 * OPB + (wave & 1) * SCB;
+    lds = 2 * OPB8 + (wave & 1) * SCB;
   }
-  __device__ __forceinline__ void issue(int ks, uint32_t stage) const {
-    const i32x4_t r = make_rsrc(base + static_cast<int64_t>(ks >> 1) * rp, 256);
-    lds_dma4(__builtin_amdgcn_readfirstlane(stage + lds), voff, r);
+  __device__ __forceinline__ void issue(int kb, uint32_t at) const {
+    const i32x4_t r = make_rsrc(base + static_cast<int64_t>(kb) * rp, 256);
+    lds_dma4(__builtin_amdgcn_readfirstlane(at + lds), voff, r);
   }
 };
 
 template <int NQ>
 struct Frags8 {
-  i32x8_t p[4];    // dwords 0-3: chunk h of the 64-byte row, 4-7: chunk 2 + h
+  i32x8_t p[4];    // dwords 0-3: chunk h of the slice's 64 bytes, 4-7: chunk 2 + h
   i32x8_t q[NQ];
   int32_t sp, sq;  // byte i: the scale of fragment i's row
 };
@@ -236,7 +242,8 @@ __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][NQ], char* l
 template <typename T, bool ADD, int NQ>
 __device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32_t n0, char* smem) {
   constexpr int kRows = 64 * NQ;
-  constexpr int kLoads = 4 + NQ + 1;  // per wave and stage: P, then scales, then Q
+  constexpr int kPLoads = RowStream<4>::kLoads, kQLoads = RowStream<NQ>::kLoads;
+  constexpr int kLoads = kPLoads + kQLoads + 1;  // per wave and block
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -250,8 +257,8 @@ __device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][k][e] = 0.f;
 
-  const int nk = d.kp / 64;
-  if (nk > 0) {
+  const int nb = d.kp / kF8Block;
+  if (nb > 0) {
     RowStream<4> sp;
     RowStream<NQ> sq;
     sp.init(d.b + static_cast<int64_t>(n0) * d.kp, min(kTile, d.n - n0), d.kp, wave, lane);
@@ -262,148 +269,176 @@ __device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32
     else
       ss.init(d.sb, n0, d.n, wave, lane);
 
-    int32_t qoff[2], poff[2];
+    // Offsets of this lane's two chunks of a fragment row in slice 0 and 1 of a
+    // block: chunks h and 2 + h, and 4 more.
+    int32_t poff[2][2], qoff[2][2];
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      const int sw = ((2 * sub + lh) ^ kkey(lr)) << 4;
-      qoff[sub] = OPB + (wn * 32 * NQ + lr) * KROW + sw;
-      poff[sub] = (wm * 128 + lr) * KROW + sw;
+    for (int h = 0; h < 2; ++h) {
+      const int x = ((2 * h + lh) ^ ((lr >> 1) & 7)) << 4;
+      poff[0][h] = (wm * 128 + lr) * LROW + x;
+      poff[1][h] = poff[0][h] ^ 64;
+      qoff[0][h] = OPB8 + (wn * 32 * NQ + lr) * LROW + x;
+      qoff[1][h] = qoff[0][h] ^ 64;
     }
-    const int32_t psc = 2 * OPB + 4 * (32 * wm + lr);
-    const int32_t qsc = 2 * OPB + SCB + NQ * (32 * wn + lr);
-    auto q_scales = [&](const char* stage) -> int32_t {
+    const int32_t psc = 2 * OPB8 + 4 * (32 * wm + lr);
+    const int32_t qsc = 2 * OPB8 + SCB + NQ * (32 * wn + lr);
+    auto p_scales = [&](const char* buf) { return *reinterpret_cast<const int32_t*>(buf + psc); };
+    auto q_scales = [&](const char* buf) -> int32_t {
       if constexpr (NQ == 4)
-        return *reinterpret_cast<const int32_t*>(stage + qsc);
+        return *reinterpret_cast<const int32_t*>(buf + qsc);
       else
-        return *reinterpret_cast<const uint16_t*>(stage + qsc);
+        return *reinterpret_cast<const uint16_t*>(buf + qsc);
     };
 
-    const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LDS_AS char*)smem));
-    // Prologue: slices 0..NST-2 requested (P, scales, Q each), slice 0 awaited.
-    // Slice indices past the end are clamped to the last slice: those loads
-    // refill a stage nobody reads again and keep the count in flight constant.
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LDS_AS char*)smem));
+    // Requests number 0 .. kLoads - 1 of a block: P's, the scales, Q's.  Block
+    // indices past the end are clamped to the last block: those loads refill a
+    // buffer nobody reads again and keep the count in flight constant.
+    auto request = [&](int kb, uint32_t at, const i32x4_t& rp, const i32x4_t& rq, auto U) {
+      constexpr int u = decltype(U)::value;
+      if constexpr (u < kPLoads)
+        sp.issue_one(rp, at, u);
+      else if constexpr (u == kPLoads)
+        ss.issue(kb, at);
+      else
+        sq.issue_one(rq, at + OPB8, u - kPLoads - 1);
+    };
 #pragma unroll
-    for (int s = 0; s < NST - 1; ++s) {
-      const int ks = s < nk ? s : nk - 1;
-      sp.issue(ks, ring + s * STAGE8);
-      ss.issue(ks, ring + s * STAGE8);
-      sq.issue(ks, ring + s * STAGE8 + OPB);
+    for (int b = 0; b < 2; ++b) {
+      const int kb = b < nb ? b : nb - 1;
+      sp.issue(kb, lds0 + b * BUF8);
+      ss.issue(kb, lds0 + b * BUF8);
+      sq.issue(kb, lds0 + b * BUF8 + OPB8);
     }
-    wait_vm<(NST - 2) * kLoads>();
+    wait_vm<kLoads>();  // block 0
     __syncthreads();
 
     if constexpr (sizeof(T) == 2) {
       // Fragment reads in the order the MFMAs consume them: the scales, P[0],
       // the Qs, then P[1..3]; two 16-byte reads per fragment.
-      constexpr int kReads = 2 + 2 * (4 + NQ), kHalf = 2 * NQ;  // MFMAs: 2 kHalf a slice
-      auto read_op = [&](Frags8<NQ>& f, const char* stage, int i) {
+      constexpr int kReads = 2 + 2 * (4 + NQ), kMfma = 4 * NQ, kHalf = kMfma / 2;
+      auto read_op = [&](Frags8<NQ>& f, const char* buf, int sub, int i) {
         if (i == 0) {
-          f.sp = *reinterpret_cast<const int32_t*>(stage + psc);
+          f.sp = p_scales(buf);
         } else if (i == 1) {
-          f.sq = q_scales(stage);
+          f.sq = q_scales(buf);
         } else if (i < 4) {
-          set_half(f.p[0], i - 2, lds16(stage + poff[i - 2]));
+          set_half(f.p[0], i - 2, lds16(buf + poff[sub][i - 2]));
         } else if (i < 4 + 2 * NQ) {
           const int ni = (i - 4) >> 1, h = (i - 4) & 1;
-          set_half(f.q[ni], h, lds16(stage + qoff[h] + ni * 32 * KROW));
+          set_half(f.q[ni], h, lds16(buf + qoff[sub][h] + ni * 32 * LROW));
         } else {
           const int mi = 1 + ((i - 4 - 2 * NQ) >> 1), h = (i - 4) & 1;
-          set_half(f.p[mi], h, lds16(stage + poff[h] + mi * 32 * KROW));
+          set_half(f.p[mi], h, lds16(buf + poff[sub][h] + mi * 32 * LROW));
         }
       };
       Frags8<NQ> f0, f1;
 #pragma unroll
-      for (int i = 0; i < kReads; ++i) read_op(f0, smem, i);
+      for (int i = 0; i < kReads; ++i) read_op(f0, smem, 0, i);
 
-      // Slice kt on fragments fa (stage kt), reading stage kt+1 into fb.
-      auto slice = [&](int kt, Frags8<NQ>& fa, Frags8<NQ>& fb) {
-        const int ks = kt + NST - 1 < nk ? kt + NST - 1 : nk - 1;
-        const uint32_t fill = ring + ((kt + NST - 1) & (NST - 1)) * STAGE8;
-        const i32x4_t rp = sp.rsrc(ks);
-        static_for<kHalf>([&](auto I) {
+      // Block b: slice 0 on f0, slice 1 on f1.  Slice 1's fragments are read in
+      // the first half of slice 0; every wave has then left the buffer, and block
+      // b + 2 is requested into it from the second half of slice 0 (P) to the
+      // first half of slice 1 (scales, Q).  Slice 1 reads block b + 1's first
+      // fragments.
+      constexpr int kEarly = kPLoads;  // requests issued in slice 0
+      for (int b = 0; b < nb; ++b) {
+        const char* const cur = smem + (b & 1) * BUF8;
+        const char* const next = smem + ((b + 1) & 1) * BUF8;
+        const uint32_t fill = lds0 + (b & 1) * BUF8;
+        const int kb = b + 2 < nb ? b + 2 : nb - 1;
+        const i32x4_t rp = sp.rsrc(kb), rq = sq.rsrc(kb);
+        static_for<kMfma>([&](auto I) {
           constexpr int i = decltype(I)::value, mi = i / NQ, ni = i % NQ;
-          if constexpr (i % (kHalf / 4) == 0) sp.issue_one(rp, fill, i / (kHalf / 4));
-          if constexpr (i == kHalf - 1) ss.issue(ks, fill);
+          if constexpr (i < kHalf) {
+#pragma unroll
+            for (int r = i * kReads / kHalf; r < (i + 1) * kReads / kHalf; ++r) read_op(f1, cur, 1, r);
+          }
+          if constexpr (i == kHalf) {
+            wait_lgkm0();  // this wave's reads of the buffer are done
+            __syncthreads();
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if constexpr (i >= kHalf) {
+            static_for<kEarly / kHalf>([&](auto U) {
+              request(kb, fill, rp, rq,
+                      std::integral_constant<int, (i - kHalf) * (kEarly / kHalf) + decltype(U)::value>{});
+            });
+          }
           acc[mi][ni] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              fa.p[mi], fa.q[ni], acc[mi][ni], 0, 0, mi, fa.sp, ni, fa.sq);
+              f0.p[mi], f0.q[ni], acc[mi][ni], 0, 0, mi, f0.sp, ni, f0.sq);
           __builtin_amdgcn_sched_barrier(0);
         });
-        // slice kt+1 has landed once only slice kt+2 and the P and scale loads of
-        // kt+NST-1 remain
-        wait_vm<(NST - 3) * kLoads + 4 + 1>();
-        wait_lgkm0();  // this wave's reads of stage kt+NST-1's previous slice are done
+        wait_vm<kEarly>();  // block b + 1 has landed
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
-        const i32x4_t rq = sq.rsrc(ks);
-        const char* next = smem + ((kt + 1) & (NST - 1)) * STAGE8;
-        static_for<kHalf>([&](auto I) {
-          constexpr int j = decltype(I)::value, i = kHalf + j, mi = i / NQ, ni = i % NQ;
-          if constexpr ((j & 1) == 0) sq.issue_one(rq, fill + OPB, j >> 1);
-          constexpr int r0 = (j * kReads + kHalf - 1) / kHalf;
-          constexpr int r1 = ((j + 1) * kReads + kHalf - 1) / kHalf;
+        static_for<kMfma>([&](auto I) {
+          constexpr int i = decltype(I)::value, mi = i / NQ, ni = i % NQ;
 #pragma unroll
-          for (int r = r0; r < r1; ++r) read_op(fb, next, r);
+          for (int r = i * kReads / kMfma; r < (i + 1) * kReads / kMfma; ++r) read_op(f0, next, 0, r);
+          if constexpr (i == 0) request(kb, fill, rp, rq, std::integral_constant<int, kPLoads>{});
+          if constexpr (i < kHalf) {
+            static_for<kQLoads / kHalf>([&](auto U) {
+              request(kb, fill, rp, rq,
+                      std::integral_constant<int, kPLoads + 1 + i * (kQLoads / kHalf) + decltype(U)::value>{});
+            });
+          }
           acc[mi][ni] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              fa.p[mi], fa.q[ni], acc[mi][ni], 0, 0, mi, fa.sp, ni, fa.sq);
+              f1.p[mi], f1.q[ni], acc[mi][ni], 0, 0, mi, f1.sp, ni, f1.sq);
           __builtin_amdgcn_sched_barrier(0);
         });
-      };
-      // nk is even: the operands' K is padded to whole blocks of 128
-      for (int kt = 0; kt < nk; kt += 2) {
-        slice(kt, f0, f1);
-        slice(kt + 1, f1, f0);
       }
     } else {
-      // Fragments of slice kt are converted one step ahead of the MFMAs that take
+      // Fragments of a slice are converted one step ahead of the MFMAs that take
       // them, between MFMAs.  On entry to a slice: P[0] and the Qs but the last
-      // converted, the last Q raw.  A quarter of a slice is one P fragment.
+      // converted, the last Q raw.  A quarter of a slice is one P fragment; the
+      // last quarter turns to the next slice.  The last quarter of a block's slice
+      // 1 leaves its buffer; block b + 2 is requested into it from there to the
+      // third quarter of the next slice.
       constexpr int kQuarter = 4 * NQ, kPer = 4 / NQ;  // dwords converted per MFMA
       constexpr int kLast = NQ - 1;
       Wide qb[NQ], pb[2];
       i32x8_t rq[NQ], rp;
       int32_t ssp, ssq, nsp = 0, nsq = 0;
-      auto load_q = [&](const char* stage, int ni, int h) {
-        set_half(rq[ni], h, lds16(stage + qoff[h] + ni * 32 * KROW));
+      auto load_q = [&](const char* buf, int sub, int ni, int h) {
+        set_half(rq[ni], h, lds16(buf + qoff[sub][h] + ni * 32 * LROW));
       };
-      auto load_p = [&](const char* stage, int mi, int h) {
-        set_half(rp, h, lds16(stage + poff[h] + mi * 32 * KROW));
+      auto load_p = [&](const char* buf, int sub, int mi, int h) {
+        set_half(rp, h, lds16(buf + poff[sub][h] + mi * 32 * LROW));
       };
       auto widen_q = [&](int ni, int d, int32_t sc) { widen(qb[ni], d, rq[ni][d], scale_value(sc, ni)); };
       auto widen_p = [&](int mi, int d, int32_t sc) { widen(pb[mi & 1], d, rp[d], scale_value(sc, mi)); };
-      ssp = *reinterpret_cast<const int32_t*>(smem + psc);
+      ssp = p_scales(smem);
       ssq = q_scales(smem);
 #pragma unroll
       for (int ni = 0; ni < NQ; ++ni)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) load_q(smem, ni, h);
+        for (int h = 0; h < 2; ++h) load_q(smem, 0, ni, h);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) load_p(smem, 0, h);
+      for (int h = 0; h < 2; ++h) load_p(smem, 0, 0, h);
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
 #pragma unroll
         for (int ni = 0; ni < kLast; ++ni) widen_q(ni, d, ssq);
         widen_p(0, d, ssp);
       }
-      for (int kt = 0; kt < nk; ++kt) {
-        const int ks = kt + NST - 1 < nk ? kt + NST - 1 : nk - 1;
-        const uint32_t fill = ring + ((kt + NST - 1) & (NST - 1)) * STAGE8;
-        const char* cur = smem + (kt & (NST - 1)) * STAGE8;
-        const char* next = smem + ((kt + 1) & (NST - 1)) * STAGE8;
-        const i32x4_t rsp = sp.rsrc(ks), rsq = sq.rsrc(ks);
+      // One slice: `sub` of the block in `cur`; the last quarter reads the other
+      // slice of the block in `next`.  Requests are for block kb, into `fill`.
+      auto slice = [&](auto SUB, const char* cur, const char* next, int kb, uint32_t fill,
+                       const i32x4_t& drp, const i32x4_t& drq) {
+        constexpr int sub = decltype(SUB)::value, nsub = sub ^ 1;
         static_for<4 * kQuarter>([&](auto I) {
           constexpr int i = decltype(I)::value;
           constexpr int mi = i / kQuarter, ni = (i >> 2) % NQ, s = i & 3, j = i % kQuarter;
-          if constexpr (i == 3 * kQuarter) {
-            // slice kt+1 has landed once only slice kt+2 and kt+NST-1 remain; this
-            // wave has read all it needs of stage kt
-            wait_vm<(NST - 2) * kLoads>();
-            wait_lgkm0();
+          if constexpr (sub == 1 && i == 3 * kQuarter) {
+            wait_vm<0>();  // block b + 1 has landed: nothing else is in flight
+            wait_lgkm0();  // this wave has left the buffer
             __syncthreads();
             __builtin_amdgcn_sched_barrier(0);
           }
           if constexpr (mi < 3) {
             // the next P fragment: read, then converted half a quarter later
-            if constexpr (j < 2) load_p(cur, mi + 1, j);
+            if constexpr (j < 2) load_p(cur, sub, mi + 1, j);
             if constexpr (j >= kQuarter / 2)
 #pragma unroll
               for (int k = 0; k < kPer; ++k) widen_p(mi + 1, (j - kQuarter / 2) * kPer + k, ssp);
@@ -412,16 +447,16 @@ __device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32
 #pragma unroll
               for (int k = 0; k < kPer; ++k) widen_q(kLast, j * kPer + k, ssq);
           } else {
-            // slice kt+1: scales, the Qs, P[0]
+            // the next slice: scales, the Qs, P[0]
             if constexpr (j == 0) {
-              nsp = *reinterpret_cast<const int32_t*>(next + psc);
+              nsp = p_scales(next);
               nsq = q_scales(next);
             }
             if constexpr (j < NQ) {
-              load_q(next, j, 0);
-              load_q(next, j, 1);
+              load_q(next, nsub, j, 0);
+              load_q(next, nsub, j, 1);
             }
-            if constexpr (j >= NQ && j < NQ + 2) load_p(next, 0, j - NQ);
+            if constexpr (j >= NQ && j < NQ + 2) load_p(next, nsub, 0, j - NQ);
             if constexpr (ni > 0) {  // Q[ni - 1] has had its last MFMA
               widen_q(ni - 1, 2 * s, nsq);
               widen_q(ni - 1, 2 * s + 1, nsq);
@@ -430,18 +465,35 @@ __device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32
 #pragma unroll
               for (int k = 0; k < kPer; ++k) widen_p(0, (j - kQuarter / 2) * kPer + k, nsp);
           }
-          if constexpr (mi == 1 && j % NQ == 0) sp.issue_one(rsp, fill, j / NQ);
-          if constexpr (mi == 1 && j == kQuarter - 2) ss.issue(ks, fill);
-          if constexpr (mi == 2 && (j & 3) == 0) sq.issue_one(rsq, fill + OPB, j >> 2);
+          // four requests of a block in slice 1, the others in slice 0
+          if constexpr (sub == 1 && mi == 3 && j % NQ == NQ - 1)
+            request(kb, fill, drp, drq, std::integral_constant<int, j / NQ>{});
+          if constexpr (sub == 0 && mi < 3) {
+            constexpr int kRest = kLoads - 4, kSpan = 3 * kQuarter;
+            constexpr int a = i * kRest / kSpan, z = (i + 1) * kRest / kSpan;
+            if constexpr (z > a) request(kb, fill, drp, drq, std::integral_constant<int, 4 + a>{});
+          }
           acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pb[mi & 1].v[s], qb[ni].v[s],
                                                                 acc[mi][ni], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         });
         ssp = nsp;
         ssq = nsq;
+      };
+      // Slice 0 of block b goes on with the requests for block b + 1 that slice 1
+      // of block b - 1 began.  (Block 0's repeats part of those for block 1, the
+      // same bytes to the same place.)
+      for (int b = 0; b < nb; ++b) {
+        const char* const cur = smem + (b & 1) * BUF8;
+        const char* const next = smem + ((b + 1) & 1) * BUF8;
+        const int kb1 = b + 1 < nb ? b + 1 : nb - 1, kb2 = b + 2 < nb ? b + 2 : nb - 1;
+        const i32x4_t p1 = sp.rsrc(kb1), q1 = sq.rsrc(kb1);
+        slice(std::integral_constant<int, 0>{}, cur, cur, kb1, lds0 + ((b + 1) & 1) * BUF8, p1, q1);
+        const i32x4_t p2 = sp.rsrc(kb2), q2 = sq.rsrc(kb2);
+        slice(std::integral_constant<int, 1>{}, cur, next, kb2, lds0 + (b & 1) * BUF8, p2, q2);
       }
     }
-    wait_vm<0>();  // no load may still target LDS: the ring is reused for the store
+    wait_vm<0>();  // no load may still target LDS: the buffers are reused for the store
   }
   __syncthreads();
   store_part<T, ADD, NQ>(acc, smem + wave * 16384, static_cast<T*>(d.c), m0 + 32 * NQ * wn,
