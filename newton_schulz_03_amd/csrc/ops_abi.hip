@@ -183,16 +183,6 @@ int32_t add_blocks(int64_t a, int64_t b, int64_t& total) {
 
 int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
-// Which kernel takes which product, and the block shape of the small one.
-//
-// Products of up to kFewRows rows go to the kernel of few rows: B's bytes bound
-// them, and its blocks are as many as its 64-row pieces (24 products 4 x 2048 x
-// 6144: 51 us against 91 in 256 x 256 tiles).  The others go where the
-// following estimates, fitted to measurements from 64 to 24576 tiles, say the
-// call ends first; all of them to one kernel.  us per tile on one of the 256
-// CUs: a fixed part and one per K slice, which grows in the large tile as the
-// chip fills up.  (2048^3 in bf16: 32 us large, 31 small; 1024^3: 21 and 9;
-// 4096^3: 67 and 189.)
 constexpr int32_t kFewRows = 64;
 constexpr double kCus = 256;
 
@@ -200,8 +190,9 @@ struct SmallPlan {
   int32_t mt = 1, nt = 4;
 };
 
-// Rounds that F full tiles and then H half ones take on the chip, in full tiles.
-constexpr double kHalfCost = 0.58;
+// Rounds that F full tiles and then H half ones take on the chip, in full tiles
+// (a half tile took 0.65 of a full one's time).
+constexpr double kHalfCost = 0.65;
 double rounds(int64_t f, int64_t h) {
   const int64_t cus = static_cast<int64_t>(kCus), q = f / cus, r = f % cus;
   const double t = static_cast<double>(q);
@@ -215,7 +206,7 @@ double rounds(int64_t f, int64_t h) {
 // Rows of full and half tiles of the products that the large-tile kernel takes:
 // a rest of up to 128 rows is one half tile, and where it shortens the launch's
 // last round, the last full tiles become two half ones each.
-void cut_rows(std::vector<F8ProdDesc>& desc, const std::vector<char>& large) {
+double cut_rows(std::vector<F8ProdDesc>& desc, const std::vector<char>& large) {
   int64_t f = 0, h = 0;
   for (size_t i = 0; i < desc.size(); ++i) {
     F8ProdDesc& d = desc[i];
@@ -255,17 +246,32 @@ void cut_rows(std::vector<F8ProdDesc>& desc, const std::vector<char>& large) {
       take -= tn;
     }
   }
+  return best;
 }
 
+// Which kernel takes which product, the rows of its tiles, and the block shape
+// of the kernel of few rows.
+//
+// Products of up to kFewRows rows go to that kernel: B's bytes bound them, and
+// its blocks are as many as B's 64-row pieces (24 products 4 x 2048 x 6144: 50 us
+// against 91 in 256 x 256 tiles).  The others go, all of them to one kernel, where
+// these estimates say that the call ends first: us per tile or block on one of
+// the 256 CUs, a fixed part and one per K slice (64 deep in the tiles; 512 in the
+// blocks, whose four waves share K), which grows in the tiles as the chip fills
+// up.  (bf16, 1024^3: 21 us in tiles, 6.5 in blocks; 2048^3: 18.5 and 28;
+// 4096^3: 67 and 189.)
 int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int32_t>& full,
                       std::vector<int32_t>& half, std::vector<int32_t>& small, SmallPlan& sp) {
   double tiles = 0, slices = 0, blocks = 0, steps = 0;
   int32_t few_rows = 0;
-  for (const F8ProdDesc& d : desc) {
+  std::vector<char> large(desc.size(), 0);
+  for (size_t i = 0; i < desc.size(); ++i) {
+    const F8ProdDesc& d = desc[i];
     if (d.m <= kFewRows) {
       few_rows = std::max(few_rows, d.m);
       continue;
     }
+    large[i] = 1;
     const double t = static_cast<double>(cdiv(d.m, kF8Tile)) * static_cast<double>(cdiv(d.n, kF8Tile));
     tiles += t;
     slices += t * (d.kp / 64);
@@ -275,24 +281,22 @@ int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int3
   }
   bool all_small = true;
   if (tiles > 0) {
-    const double full = std::min(1.0, tiles / kCus);
-    const double fixed = bf16 ? 8 : 15, slice = bf16 ? 0.45 + 0.35 * full : 1.25 + 0.2 * full;
-    const double large_us = std::ceil(tiles / kCus) * (fixed + slice * slices / tiles);
+    const double filled = std::min(1.0, tiles / kCus);
+    const double fixed = bf16 ? 8 : 13, slice = bf16 ? 0.45 + 0.33 * filled : 1.25 + 0.1 * filled;
+    const double large_us = cut_rows(desc, large) * (fixed + slice * slices / tiles);
     const double small_us = std::ceil(blocks / kCus) * (3.0 + 1.25 * steps / blocks);
     all_small = small_us < large_us;
   }
   if (all_small && tiles > 0) few_rows = kFewRows;
+  if (all_small) std::fill(large.begin(), large.end(), 0);
   sp.mt = few_rows <= 16 ? 1 : few_rows <= 32 ? 2 : 4;
   // narrower blocks while there are too few to occupy the chip (one product 4 x
   // 2048 x 6144: 9.3 us in 32 blocks, 7.6 in 64, 7.2 in 128)
   double n64 = 0;
-  for (const F8ProdDesc& d : desc)
-    if (d.m > 0 && (d.m <= kFewRows || all_small))
+  for (size_t i = 0; i < desc.size(); ++i)
+    if (const F8ProdDesc& d = desc[i]; d.m > 0 && !large[i])
       n64 += static_cast<double>(cdiv(d.m, 16 * sp.mt)) * static_cast<double>(cdiv(d.n, 64));
   sp.nt = n64 >= 96 ? 4 : n64 >= 48 ? 2 : 1;
-  std::vector<char> large(desc.size(), 0);
-  for (size_t i = 0; i < desc.size(); ++i) large[i] = desc[i].m > kFewRows && !all_small;
-  cut_rows(desc, large);
   int64_t nf = 0, nh = 0, ns = 0;
   int32_t st;
   for (size_t i = 0; i < desc.size(); ++i) {
