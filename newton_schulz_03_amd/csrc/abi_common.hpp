@@ -21,12 +21,12 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // Null, too small or misaligned workspaces, as every entry point reports them.
 int32_t check_workspace(const void* ws, size_t ws_bytes, size_t need);
 
-// A call's descriptor table: n descriptors of `desc_bytes` together, then the
-// prefixes (align_up(desc_bytes, kAlign) on).  Where it fits it becomes the
+// A call's descriptor table: n descriptors of `desc_bytes` together, then a
+// second array (prefixes, or pointers; align_up(desc_bytes, kAlign) on).  Where it fits it becomes the
 // kernels' argument table; otherwise kernels that carry its pieces write it to
 // `ws`.  *mem: where it lies (null: the argument table).  Kernel launches only,
 // so that calls can be captured into a graph.
-int32_t place_table(const void* desc, size_t desc_bytes, const void* prefix, size_t prefix_bytes,
+int32_t place_table(const void* desc, size_t desc_bytes, const void* second, size_t second_bytes,
                     char* ws, hipStream_t stream, ArgTable& args, const void** mem);
 
 // Brackets one launch with timing events when timing is enabled (and allowed:

@@ -119,9 +119,9 @@ hipError_t run_adamw(const ArgTable& t, const AdamCtx& c, int32_t nblocks, const
 
 }  // namespace
 
-hipError_t launch_adamw(const ArgTable& t, const AdamCtx& c, int32_t nblocks, bool is_bf16,
-                        const AdamParams& a) {
+hipError_t launch_adamw(const AdamCtx& c, int32_t nblocks, bool is_bf16, const AdamParams& a) {
   if (nblocks <= 0) return hipSuccess;
+  const ArgTable& t = *c.args;
   if (a.g_scale != nullptr)
     return is_bf16 ? run_adamw<uint16_t, true>(t, c, nblocks, a) : run_adamw<float, true>(t, c, nblocks, a);
   return is_bf16 ? run_adamw<uint16_t, false>(t, c, nblocks, a) : run_adamw<float, false>(t, c, nblocks, a);

@@ -56,39 +56,40 @@ constexpr int kNormBatch = 4;  // 16-byte loads per thread in flight
 
 // One chunk (kGradSpan elements) of a tensor, or what is left of it.
 struct Chunk {
+  const void* g;
+  void* out;
   int64_t base;  // first element
   int64_t n;     // elements, 1 .. kGradSpan
+  bool in_bf16, out_bf16;
 };
 
-// The call's table, and the chunk's tensor in it by binary search:
-// prefix[j] <= c < prefix[j + 1].
-struct Table {
-  const GradDesc* desc;
-  const int32_t* prefix;
-  int batch;
-  __device__ __forceinline__ explicit Table(const GradCtx& c) {
-    const char* const t = table_base(c.table);
-    desc = reinterpret_cast<const GradDesc*>(t);
-    prefix = reinterpret_cast<const int32_t*>(t + c.prefix_off);
-    batch = c.batch;
+// Chunk c's tensor by binary search in the call's table.
+__device__ __forceinline__ Chunk find_chunk(const GradCtx& ctx, int32_t c) {
+  const char* const table = table_base(ctx.table);
+  const GradDesc* const desc = reinterpret_cast<const GradDesc*>(table);
+  int lo = 0, hi = ctx.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (load_const(&desc[mid].chunk) <= c)
+      lo = mid;
+    else
+      hi = mid;
   }
-  __device__ __forceinline__ Chunk find(int32_t c, GradDesc& d) const {
-    int lo = 0, hi = batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (load_const(prefix + mid) <= c)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    d = load_const(desc + lo);
-    Chunk k;
-    k.base = static_cast<int64_t>(c - load_const(prefix + lo)) * kGradSpan;
-    const int64_t left = d.numel - k.base;
-    k.n = left < kGradSpan ? left : kGradSpan;
-    return k;
+  const GradDesc d = load_const(desc + lo);
+  Chunk k;
+  k.g = d.g;
+  k.out = const_cast<void*>(d.g);
+  if (ctx.out_off > 0) {
+    typedef void* ptr_t;
+    k.out = load_const(reinterpret_cast<const ptr_t*>(table + ctx.out_off) + lo);
   }
-};
+  k.base = static_cast<int64_t>(c - d.chunk) * kGradSpan;
+  const bool last = c + 1 == load_const(&desc[lo + 1].chunk);
+  k.n = last ? kGradSpan - (d.tail & (kGradSpan - 1)) : kGradSpan;
+  k.in_bf16 = (d.tail & kGradInBf16) != 0;
+  k.out_bf16 = (d.tail & kGradOutBf16) != 0;
+  return k;
+}
 
 struct SumSq {
   typedef double acc_t;
@@ -196,15 +197,13 @@ __device__ __forceinline__ float factor_of_few(const GradNormArgs& p, int32_t n)
 template <typename K, bool NT>
 __global__ __launch_bounds__(kThreads) void k_grad_norm(ArgTable, GradCtx ctx, GradNormArgs p) {
   __shared__ typename K::acc_t scratch[kThreads / 64];
-  const Table tab(ctx);
   typename K::acc_t acc = 0;
   for (int32_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-    GradDesc d;
-    const Chunk k = tab.find(c, d);
-    if (d.in_bf16)
-      add_chunk<K, NT>(static_cast<const uint16_t*>(d.g) + k.base, k.n, acc);
+    const Chunk k = find_chunk(ctx, c);
+    if (k.in_bf16)
+      add_chunk<K, NT>(static_cast<const uint16_t*>(k.g) + k.base, k.n, acc);
     else
-      add_chunk<K, NT>(static_cast<const float*>(d.g) + k.base, k.n, acc);
+      add_chunk<K, NT>(static_cast<const float*>(k.g) + k.base, k.n, acc);
   }
   acc = block_join<K>(acc, scratch);
   if (threadIdx.x != 0) return;
@@ -274,22 +273,21 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(ArgTable, GradCtx ctx, 
     s = *scale;
   else
     s = kind == 0 ? factor_of_few<SumSq>(p, nparts) : factor_of_few<MaxAbs>(p, nparts);
-  GradDesc d;
-  const Chunk k = Table(ctx).find(blockIdx.x / kPer, d);
+  const Chunk k = find_chunk(ctx, blockIdx.x / kPer);
   const int64_t off = static_cast<int64_t>(blockIdx.x % kPer) * kScaleSpan;
   const int64_t left = k.n - off, n = left < kScaleSpan ? left : kScaleSpan;
-  if (n <= 0 || (s == 1.f && d.out == d.g)) return;
-  const uint16_t* gh = static_cast<const uint16_t*>(d.g) + k.base + off;
-  const float* gf = static_cast<const float*>(d.g) + k.base + off;
-  uint16_t* oh = static_cast<uint16_t*>(d.out) + k.base + off;
-  float* of = static_cast<float*>(d.out) + k.base + off;
-  if (d.in_bf16) {
-    if (d.out_bf16)
+  if (n <= 0 || (s == 1.f && k.out == k.g)) return;
+  const uint16_t* gh = static_cast<const uint16_t*>(k.g) + k.base + off;
+  const float* gf = static_cast<const float*>(k.g) + k.base + off;
+  uint16_t* oh = static_cast<uint16_t*>(k.out) + k.base + off;
+  float* of = static_cast<float*>(k.out) + k.base + off;
+  if (k.in_bf16) {
+    if (k.out_bf16)
       scale_span<uint16_t, uint16_t, NT>(gh, oh, n, s);
     else
       scale_span<uint16_t, float, NT>(gh, of, n, s);
   } else {
-    if (d.out_bf16)
+    if (k.out_bf16)
       scale_span<float, uint16_t, NT>(gf, oh, n, s);
     else
       scale_span<float, float, NT>(gf, of, n, s);

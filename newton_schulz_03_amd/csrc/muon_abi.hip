@@ -49,18 +49,19 @@ int32_t check_workspace(const void* ws, size_t ws_bytes, size_t need) {
   return MUON_OK;
 }
 
-int32_t place_table(const void* desc, size_t desc_bytes, const void* prefix, size_t prefix_bytes,
+int32_t place_table(const void* desc, size_t desc_bytes, const void* second, size_t second_bytes,
                     char* ws, hipStream_t stream, ArgTable& args, const void** mem) {
-  const size_t off = align_up(desc_bytes, kAlign), total = off + prefix_bytes;
+  const size_t off = align_up(desc_bytes, kAlign);
+  const size_t total = second_bytes > 0 ? off + second_bytes : desc_bytes;
   if (total <= kArgTableBytes) {
-    if (desc_bytes > 0) std::memcpy(args.bytes, desc, desc_bytes);
-    std::memcpy(args.bytes + off, prefix, prefix_bytes);
+    std::memcpy(args.bytes, desc, desc_bytes);
+    if (second_bytes > 0) std::memcpy(args.bytes + off, second, second_bytes);
     *mem = nullptr;
     return MUON_OK;
   }
   std::vector<unsigned char> t(total, 0);
   std::memcpy(t.data(), desc, desc_bytes);
-  std::memcpy(t.data() + off, prefix, prefix_bytes);
+  if (second_bytes > 0) std::memcpy(t.data() + off, second, second_bytes);
   *mem = ws;
   const hipError_t e = launch_put_bytes(t.data(), total, ws, stream);
   return e == hipSuccess ? MUON_OK : hip_fail(e, "launch descriptor copy");
@@ -1150,11 +1151,12 @@ int32_t adamw_batched(int32_t batch, const int64_t* numel, void* const* p, const
     a.inv_bc2_sqrt = static_cast<float>(1.0 / std::sqrt(bc2));
     a.eps = prm->eps;
     a.g_scale = g_scale;
+    c.args = &table;
     c.prefix_off = static_cast<int32_t>(pl.prefix_off);
     c.batch = pl.batch;
     c.stream = s;
     TimedLaunch tl(MUON_K_ADAMW, s);
-    hipError_t e = launch_adamw(table, c, pl.prefix[pl.batch], pl.bf16, a);
+    hipError_t e = launch_adamw(c, pl.prefix[pl.batch], pl.bf16, a);
     if (e != hipSuccess) return hip_fail(e, "launch adamw");
     tl.done();
     return MUON_OK;

@@ -157,6 +157,7 @@ struct AdamDesc {
 
 // The table is the descriptors, then (at prefix_off) batch+1 block prefixes.
 struct AdamCtx {
+  const ArgTable* args;    // host: the argument table
   const void* table;       // device copy of the table; null: it is the argument table
   int32_t prefix_off;
   int32_t batch;
@@ -174,24 +175,26 @@ struct AdamParams {
 };
 
 int64_t adamw_blocks(int64_t numel);
-hipError_t launch_adamw(const ArgTable& t, const AdamCtx& c, int32_t nblocks, bool is_bf16,
-                        const AdamParams& a);
+hipError_t launch_adamw(const AdamCtx& c, int32_t nblocks, bool is_bf16, const AdamParams& a);
 
 // Global gradient norm, clip factor and scaled gradients over a ragged batch.
 // Every tensor is cut into chunks of kGradSpan elements, numbered through the
 // batch by the prefix table.
 constexpr int64_t kGradSpan = 16384;
 constexpr int32_t kNormBlocks = 2048;  // most blocks (and partials) of the norm pass
+// 16 bytes a tensor, so that the gradients of a whole model (239 tensors) travel
+// as arguments.  The table holds batch + 1 of these, the last one only for its
+// `chunk`, then (out_off > 0) batch output pointers.
 struct GradDesc {
   const void* g;
-  void* out;
-  int64_t numel;
-  int32_t in_bf16, out_bf16;  // element types: bf16 or fp32
+  int32_t chunk;    // number of the tensor's first chunk
+  uint32_t tail;    // bits 0..13: elements its last chunk lacks of kGradSpan; flags below
 };
-// The table is the descriptors, then (at prefix_off) batch+1 chunk prefixes.
+static_assert(kGradSpan <= (1 << 14));
+constexpr uint32_t kGradInBf16 = 1u << 30, kGradOutBf16 = 1u << 31;
 struct GradCtx {
   const void* table;       // device copy of the table; null: it is the argument table
-  int32_t prefix_off;
+  int32_t out_off;         // 0: the outputs are the gradients
   int32_t batch;
   hipStream_t stream;
 };

@@ -20,9 +20,9 @@ namespace {
 constexpr int64_t kMaxChunks = INT32_MAX / 4;
 
 struct GradPlan {
-  std::vector<GradDesc> desc;
-  std::vector<int32_t> prefix;
-  size_t prefix_off = 0, partials_off = 0, total_bytes = 0;
+  std::vector<GradDesc> desc;  // batch + 1
+  std::vector<void*> outs;     // of a call that does not work in place
+  size_t partials_off = 0, total_bytes = 0;
   int32_t chunks = 0;
   int64_t in_bytes = 0, out_bytes = 0;
 };
@@ -30,22 +30,23 @@ struct GradPlan {
 int32_t make_grad_plan(int32_t batch, const int64_t* numel, GradPlan& pl) {
   if (batch < 0) return fail(MUON_ERR_INVALID_ARG, "batch = %d is negative", batch);
   if (batch > 0 && numel == nullptr) return fail(MUON_ERR_INVALID_ARG, "numel array is null");
-  pl.desc.assign(batch, GradDesc{});
-  pl.prefix.assign(static_cast<size_t>(batch) + 1, 0);
+  pl.desc.assign(static_cast<size_t>(batch) + 1, GradDesc{});
   int64_t total = 0;
   for (int32_t i = 0; i < batch; ++i) {
     if (numel[i] < 0)
       return fail(MUON_ERR_INVALID_ARG, "tensor %d: numel %lld is negative", i,
                   static_cast<long long>(numel[i]));
-    pl.desc[i].numel = numel[i];
     if (numel[i] / kGradSpan > kMaxChunks - total - 1)
       return fail(MUON_ERR_UNSUPPORTED, "batch needs more than 2^31 blocks");
-    total += (numel[i] + kGradSpan - 1) / kGradSpan;
-    pl.prefix[i + 1] = static_cast<int32_t>(total);
+    const int64_t n = (numel[i] + kGradSpan - 1) / kGradSpan;
+    pl.desc[i].chunk = static_cast<int32_t>(total);
+    pl.desc[i].tail = static_cast<uint32_t>(n * kGradSpan - numel[i]);
+    total += n;
   }
+  pl.desc[batch].chunk = static_cast<int32_t>(total);
   pl.chunks = static_cast<int32_t>(total);
-  pl.prefix_off = align_up(sizeof(GradDesc) * batch, kAlign);
-  pl.partials_off = pl.prefix_off + align_up(sizeof(int32_t) * (static_cast<size_t>(batch) + 1), kAlign);
+  pl.partials_off = align_up(sizeof(GradDesc) * (static_cast<size_t>(batch) + 1), kAlign) +
+                    align_up(sizeof(void*) * static_cast<size_t>(batch), kAlign);
   pl.total_bytes = pl.partials_off + align_up(8 * static_cast<size_t>(kNormBlocks), kAlign);
   return MUON_OK;
 }
@@ -56,36 +57,40 @@ int32_t known_dtype(int32_t dtype, int32_t i) {
   return MUON_OK;
 }
 
-// out == nullptr: nothing is written (the norm), or, with in_place, g itself.
-int32_t bind_grads(int32_t batch, const void* const* g, const int32_t* dtype, void* const* out,
-                   const int32_t* out_dtype, GradPlan& pl) {
+// out == nullptr: the norm, which writes nothing.
+int32_t bind_grads(int32_t batch, const int64_t* numel, const void* const* g, const int32_t* dtype,
+                   void* const* out, const int32_t* out_dtype, GradPlan& pl) {
   if (batch == 0) return MUON_OK;
   if (g == nullptr || dtype == nullptr) return fail(MUON_ERR_INVALID_ARG, "g/dtype array is null");
   if (out != nullptr && out_dtype == nullptr)
     return fail(MUON_ERR_INVALID_ARG, "out_dtype array is null");
+  bool in_place = true;
   for (int32_t i = 0; i < batch; ++i) {
     GradDesc& d = pl.desc[i];
     int32_t st = known_dtype(dtype[i], i);
     if (st != MUON_OK) return st;
-    d.g = g[i];
-    d.in_bf16 = dtype[i] == MUON_BF16;
-    d.out = const_cast<void*>(g[i]);
-    d.out_bf16 = d.in_bf16;
+    const bool in_bf16 = dtype[i] == MUON_BF16;
+    bool out_bf16 = in_bf16;
+    const void* to = g[i];
     if (out != nullptr) {
       if ((st = known_dtype(out_dtype[i], i)) != MUON_OK) return st;
-      d.out = out[i];
-      d.out_bf16 = out_dtype[i] == MUON_BF16;
+      out_bf16 = out_dtype[i] == MUON_BF16;
+      to = out[i];
     }
-    if (d.numel == 0) continue;
-    pl.in_bytes += d.numel * (d.in_bf16 ? 2 : 4);
-    pl.out_bytes += d.numel * (d.out_bf16 ? 2 : 4);
-    if (d.g == nullptr || d.out == nullptr)
+    d.g = g[i];
+    d.tail |= (in_bf16 ? kGradInBf16 : 0u) | (out_bf16 ? kGradOutBf16 : 0u);
+    if (numel[i] == 0) continue;
+    pl.in_bytes += numel[i] * (in_bf16 ? 2 : 4);
+    pl.out_bytes += numel[i] * (out_bf16 ? 2 : 4);
+    if (g[i] == nullptr || to == nullptr)
       return fail(MUON_ERR_INVALID_ARG, "tensor %d: null device pointer", i);
-    if (!aligned16(d.g) || !aligned16(d.out))
+    if (!aligned16(g[i]) || !aligned16(to))
       return fail(MUON_ERR_INVALID_ARG, "tensor %d: device pointer not 16-byte aligned", i);
-    if (d.out == d.g && d.out_bf16 != d.in_bf16)
+    if (to == g[i] && out_bf16 != in_bf16)
       return fail(MUON_ERR_INVALID_ARG, "tensor %d: in place needs one dtype", i);
+    in_place = in_place && to == g[i];
   }
+  if (!in_place) pl.outs.assign(out, out + batch);
   return MUON_OK;
 }
 
@@ -109,11 +114,12 @@ int32_t check_float_ptr(const void* p, const char* what) {
 }
 
 int32_t grad_table(const GradPlan& pl, char* ws, hipStream_t s, ArgTable& t, GradCtx& c) {
-  c.batch = static_cast<int32_t>(pl.desc.size());
-  c.prefix_off = static_cast<int32_t>(pl.prefix_off);
+  const size_t desc_bytes = sizeof(GradDesc) * pl.desc.size();
+  c.batch = static_cast<int32_t>(pl.desc.size()) - 1;
+  c.out_off = pl.outs.empty() ? 0 : static_cast<int32_t>(align_up(desc_bytes, kAlign));
   c.stream = s;
-  return place_table(pl.desc.data(), sizeof(GradDesc) * pl.desc.size(), pl.prefix.data(),
-                     sizeof(int32_t) * pl.prefix.size(), ws, s, t, &c.table);
+  return place_table(pl.desc.data(), desc_bytes, pl.outs.data(), sizeof(void*) * pl.outs.size(), ws,
+                     s, t, &c.table);
 }
 
 GradNormArgs norm_args(const GradPlan& pl, const muon_grad_norm_params& p, float* result,
@@ -345,7 +351,7 @@ extern "C" int32_t muon_grad_norm_batched(int32_t batch, const int64_t* numel,
     if (st != MUON_OK) return st;
     if ((st = check_norm_params(p)) != MUON_OK) return st;
     if ((st = check_float_ptr(result, "result")) != MUON_OK) return st;
-    if ((st = bind_grads(batch, g, dtype, nullptr, nullptr, pl)) != MUON_OK) return st;
+    if ((st = bind_grads(batch, numel, g, dtype, nullptr, nullptr, pl)) != MUON_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, pl.total_bytes)) != MUON_OK) return st;
     char* ws = static_cast<char*>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -371,7 +377,7 @@ extern "C" int32_t muon_grad_scale_batched(int32_t batch, const int64_t* numel,
     if ((st = check_float_ptr(scale, "scale")) != MUON_OK) return st;
     if (batch == 0) return MUON_OK;
     if (out == nullptr) return fail(MUON_ERR_INVALID_ARG, "out array is null");
-    if ((st = bind_grads(batch, g, dtype, out, out_dtype, pl)) != MUON_OK) return st;
+    if ((st = bind_grads(batch, numel, g, dtype, out, out_dtype, pl)) != MUON_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, pl.total_bytes)) != MUON_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     ArgTable t;
@@ -397,7 +403,7 @@ extern "C" int32_t muon_grad_clip_batched(int32_t batch, const int64_t* numel,
     if (!p->clip) return fail(MUON_ERR_INVALID_ARG, "clip must be 1");
     if ((st = check_float_ptr(result, "result")) != MUON_OK) return st;
     if (batch > 0 && out == nullptr) return fail(MUON_ERR_INVALID_ARG, "out array is null");
-    if ((st = bind_grads(batch, g, dtype, out, out_dtype, pl)) != MUON_OK) return st;
+    if ((st = bind_grads(batch, numel, g, dtype, out, out_dtype, pl)) != MUON_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, pl.total_bytes)) != MUON_OK) return st;
     char* ws = static_cast<char*>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -86,14 +86,21 @@ def test_norm_of_one_tensor(numel):
             check_result(nsa.grad_norm_batched(ts, max_norm=0.5, norm_type=kind), ts, kind, 0.5)
 
 
-@pytest.mark.parametrize("batch", [32, 33, 700, 2500])
+@pytest.mark.parametrize("batch", [32, 33, 159, 160, 239, 240, 700, 2500])
 def test_norm_and_clip_of_many_tensors(batch):
-    # up to 32 tensors travel as kernel arguments, more in a table in the workspace
+    # up to 239 tensors (159 into other buffers) travel as kernel arguments, more in
+    # a table in the workspace
     rng = np.random.default_rng(batch)
     numels = [int(n) for n in rng.integers(0, 400, batch)]
     ts = make(numels, mixed(batch), batch)
     check_result(nsa.grad_norm_batched(ts, max_norm=1e-2), ts, 2, 1e-2)
     before = [t.clone() for t in ts]
+    to = [torch.full_like(t, 7, dtype=FP32) for t in ts]
+    r = nsa.grad_clip_batched(ts, 1e-2, out=to)
+    check_result(r, before, 2, 1e-2)
+    s = r[1].cpu()
+    for t, o, b in zip(ts, to, before):
+        assert torch.equal(t, b) and torch.equal(o.cpu(), b.cpu().float() * s)
     r = nsa.grad_clip_batched(ts, 1e-2)
     check_result(r, before, 2, 1e-2)
     s = r[1].cpu()

@@ -55,7 +55,7 @@ def clip_call(lib, numels=(5, 7), g=None, dtype=None, out=None, out_dtype=None, 
 
 def test_grad_workspace(lib):
     def want(n):
-        return up(32 * n, 256) + up(4 * (n + 1), 256) + 8 * 2048
+        return up(16 * (n + 1), 256) + up(8 * n, 256) + 8 * 2048
 
     for numels in ([], [0], [1], [5, 0, 16384 * 3 + 1], [7] * 300):
         assert nsa.grad_workspace_bytes(numels) == want(len(numels))
