@@ -15,6 +15,7 @@ from typing import List, NamedTuple, Optional, Sequence, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libmuon_mi355x.so")
+LISTS_PATH = os.path.join(_PKG, "lib", "tensor_lists.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "muon_mi355x.h")
 
 MUON_BF16, MUON_FP32 = 0, 1
@@ -123,8 +124,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_timing_reset.restype = i32
     lib.muon_hbm_stream.argtypes = [i32, vpp, i32, vpp, sz, i32, vp]
     lib.muon_hbm_stream.restype = i32
-    # The calls below take their host arrays as addresses (of an array.array's
-    # buffer, or a ctypes array).
+    # The calls below take their host arrays as bytes objects or ctypes arrays.
     lib.muon_grad_workspace_bytes.argtypes = [i32, vp]
     lib.muon_grad_workspace_bytes.restype = sz
     lib.muon_grad_norm_batched.argtypes = [i32, vp, vp, vp, ctypes.POINTER(GradNormParams), vp, vp,
@@ -149,6 +149,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_f8_matmul_batched.restype = i32
     _lib_handle = lib
     return lib
+
+
+@functools.lru_cache(maxsize=None)
+def _lists():
+    """The extension that reads lists of tensors (csrc/tensor_lists.cpp)."""
+    import importlib.machinery
+    import importlib.util
+
+    import torch  # noqa: F401  the extension links against it
+
+    if not os.path.exists(LISTS_PATH):
+        raise RuntimeError(f"{LISTS_PATH} is missing: build the library first "
+                           "(python -m newton_schulz_03_amd.build, or __graft_entry__.build())")
+    loader = importlib.machinery.ExtensionFileLoader("tensor_lists", LISTS_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("tensor_lists", loader))
+    loader.exec_module(module)
+    return module
 
 
 def status_string(status: int) -> str:
@@ -405,47 +422,36 @@ def adamw_batched(params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg
     dev = ps[0].device
     if dev.type != "cuda":
         raise ValueError(f"params must live on a HIP device, got {dev}")
+    lists = _lists()
+    ptrs = []
     for group, want in ((ps, ps[0].dtype), (gs, ps[0].dtype), (ms, torch.float32),
                         (vs, torch.float32)):
-        if not _all_same(group, dev, want):
+        index, flags, _, numels, where, _, _ = lists.scan(group)
+        if index != dev.index or group[0].dtype != want or flags & _FLAT != _FLAT:
             raise ValueError("tensors must be contiguous on one device; p and g share a "
                              "dtype, the moments are float32")
-    shapes = [p.shape for p in ps]
-    if not (shapes == [g.shape for g in gs] == [m.shape for m in ms] == [v.shape for v in vs]):
+        ptrs.append(where)
+    if not all(lists.same_shapes(ps, group) for group in (gs, ms, vs)):
         raise ValueError("p, g, m and v of one entry must have the same shape")
     code = _dtype_code(ps[0].dtype)
-    numels = array("q", map(torch.Tensor.numel, ps))
     if workspace is None:
         workspace = _byte_workspace(_adamw_table_bytes(len(ps)), dev)
     b1, b2 = (float(b) for b in betas)
     prm = AdamWParams(float(lr), b1, b2, float(eps), float(weight_decay), int(step))
-    ptrs = [array("Q", map(torch.Tensor.data_ptr, group)) for group in (ps, gs, ms, vs)]
     fn, scale = lib.muon_adamw_batched, ()
     if grad_scale is not None:
         fn, scale = lib.muon_adamw_batched_scaled, (_scale_pointer(grad_scale, dev),)
-    _call(fn, dev, workspace, len(ps), _addr(numels), *map(_addr, ptrs), code, ctypes.byref(prm),
-          *scale)
+    _call(fn, dev, workspace, len(ps), numels, *ptrs, code, ctypes.byref(prm), *scale)
+
+
+_FLAT = 7  # of the lists' flags: one device, contiguous, one dtype
+_SAME_DEVICE, _CONTIGUOUS, _SAME_DTYPE, _MATRICES = 1, 2, 4, 8
 
 
 @functools.lru_cache(maxsize=None)
 def _adamw_table_bytes(batch: int) -> int:
     # the workspace is the descriptor table, whatever the sizes
     return adamw_workspace_bytes([0] * batch)
-
-
-def _addr(a: array) -> int:
-    """Address of an array's buffer; the array must outlive its use."""
-    return a.buffer_info()[0]
-
-
-def _all_same(ts, dev, dtype) -> bool:
-    """Whether every tensor is contiguous, on `dev` and of `dtype`."""
-    import torch
-
-    n = len(ts)
-    return ([t.dtype for t in ts].count(dtype) == n
-            and list(map(torch.Tensor.get_device, ts)).count(dev.index) == n
-            and all(map(torch.Tensor.is_contiguous, ts)))
 
 
 def _call(fn, dev, workspace, *args) -> None:
@@ -483,25 +489,20 @@ def _byte_workspace(nbytes: int, dev):
 
 def _flat_tensors(ts, name, dev=None):
     """(device, dtype codes, element counts, pointers) of contiguous bf16 / fp32
-    tensors, the last three as arrays."""
+    tensors, the last three as the bytes of C arrays."""
     import torch
 
-    dev = ts[0].device if dev is None else dev
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: tensors must live on a HIP device, got {dev}")
-    n = len(ts)
-    dtypes = [t.dtype for t in ts]
-    if dtypes.count(torch.bfloat16) == n:
-        codes = array("i", [MUON_BF16]) * n
-    elif dtypes.count(torch.float32) == n:
-        codes = array("i", [MUON_FP32]) * n
-    else:
-        codes = array("i", map(_dtype_code, dtypes))
-    if list(map(torch.Tensor.get_device, ts)).count(dev.index) != n or \
-            not all(map(torch.Tensor.is_contiguous, ts)):
+    index, flags, codes, numels, ptrs, _, _ = _lists().scan(ts)
+    if dev is None:
+        dev = ts[0].device
+        if index < 0:
+            raise ValueError(f"{name}: tensors must live on a HIP device, got {dev}")
+    if flags & (_SAME_DEVICE | _CONTIGUOUS) != _SAME_DEVICE | _CONTIGUOUS or index != dev.index:
         raise ValueError(f"{name}: tensors must be contiguous on one device")
-    return (dev, codes, array("q", map(torch.Tensor.numel, ts)),
-            array("Q", map(torch.Tensor.data_ptr, ts)))
+    if b"\xff\xff\xff\xff" in codes:
+        bad = next(t.dtype for t in ts if t.dtype not in (torch.bfloat16, torch.float32))
+        raise TypeError(f"{name}: unsupported dtype {bad}: use torch.bfloat16 or torch.float32")
+    return dev, codes, numels, ptrs
 
 
 def grad_workspace_bytes(numels: Sequence[int]) -> int:
@@ -558,8 +559,8 @@ def grad_norm_batched(grads: Sequence, max_norm: Optional[float] = None, norm_ty
     result = _norm_result(result, dev)
     if workspace is None:
         workspace = _byte_workspace(_grad_table_bytes(len(grads)), dev)
-    _call(load_library().muon_grad_norm_batched, dev, workspace, len(grads), _addr(numels),
-          _addr(ptrs), _addr(codes), ctypes.byref(p), result.data_ptr())
+    _call(load_library().muon_grad_norm_batched, dev, workspace, len(grads), numels,
+          ptrs, codes, ctypes.byref(p), result.data_ptr())
     return result
 
 
@@ -591,8 +592,8 @@ def grad_scale_batched(grads: Sequence, scale, out: Optional[Sequence] = None,
     factor = _scale_pointer(scale, dev)
     if workspace is None:
         workspace = _byte_workspace(_grad_table_bytes(len(grads)), dev)
-    _call(load_library().muon_grad_scale_batched, dev, workspace, len(grads), _addr(numels),
-          _addr(ptrs), _addr(codes), _addr(optrs), _addr(ocodes), factor)
+    _call(load_library().muon_grad_scale_batched, dev, workspace, len(grads), numels,
+          ptrs, codes, optrs, ocodes, factor)
     return out
 
 
@@ -615,8 +616,8 @@ def grad_clip_batched(grads: Sequence, max_norm: float, norm_type: float = 2.0, 
     result = _norm_result(result, dev)
     if workspace is None:
         workspace = _byte_workspace(_grad_table_bytes(len(grads)), dev)
-    _call(load_library().muon_grad_clip_batched, dev, workspace, len(grads), _addr(numels),
-          _addr(ptrs), _addr(codes), _addr(optrs), _addr(ocodes), ctypes.byref(p),
+    _call(load_library().muon_grad_clip_batched, dev, workspace, len(grads), numels,
+          ptrs, codes, optrs, ocodes, ctypes.byref(p),
           result.data_ptr())
     return result
 
@@ -649,29 +650,24 @@ def f8_empty(rows: int, cols: int, device) -> F8Operand:
                      torch.empty((kp // F8_BLOCK, rp), dtype=torch.uint8, device=device))
 
 
-def _f8_pointers(ops, name, dev, shapes=None):
-    """(shapes, value pointers, scale pointers) of operands; shapes: what they must be."""
-    import torch
-
-    qs, ss = [o[0] for o in ops], [o[1] for o in ops]
-    n = len(qs)
-    if [q.dtype for q in qs].count(torch.float8_e4m3fn) != n or \
-            [s.dtype for s in ss].count(torch.uint8) != n:
+def _f8_pointers(ops, name, dev):
+    """(rows, padded contracted sides, value pointers, scale pointers) of operands,
+    as the bytes of C arrays."""
+    index, bad, kind, rows, kps, qs, ss = _lists().scan_f8(ops, F8_BLOCK)
+    if bad >= 0 and kind == 1:
         raise TypeError(f"{name}: an operand is a float8_e4m3fn tensor and a uint8 tensor")
-    if list(map(torch.Tensor.get_device, qs + ss)).count(dev.index) != 2 * n or \
-            not all(map(torch.Tensor.is_contiguous, qs + ss)):
+    if index != dev.index or (bad >= 0 and kind == 2):
         raise ValueError(f"{name}: operands must be contiguous 2-D tensors on one HIP device")
-    got = [tuple(q.shape) for q in qs]
-    for i, (x, s) in enumerate(zip(got, ss)):
-        if len(x) != 2 or x[1] % F8_BLOCK or s.shape != (x[1] // F8_BLOCK, -(-x[0] // 16) * 16):
-            raise ValueError(f"{name}: operand {i} has values {x} and scales "
-                             f"{tuple(s.shape)}: want (R, Kp) with Kp a multiple of {F8_BLOCK}, and "
-                             "(Kp / 128, R up to a multiple of 16)")
-    if shapes is not None and got != shapes:
-        i = next(i for i, (x, y) in enumerate(zip(got, shapes)) if x != y)
-        raise ValueError(f"{name}: operand {i} has values {got[i]}, want {shapes[i]}")
-    return (got, array("Q", map(torch.Tensor.data_ptr, qs)),
-            array("Q", map(torch.Tensor.data_ptr, ss)))
+    if bad >= 0:
+        q, s = ops[bad]
+        raise ValueError(f"{name}: operand {bad} has values {tuple(q.shape)} and scales "
+                         f"{tuple(s.shape)}: want (R, Kp) with Kp a multiple of {F8_BLOCK}, and "
+                         "(Kp / 128, R up to a multiple of 16)")
+    return rows, kps, qs, ss
+
+
+def _i64_bytes(vals) -> bytes:
+    return array("q", vals).tobytes()
 
 
 def f8_workspace_bytes(batch: int) -> int:
@@ -704,28 +700,28 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
         raise ValueError("out goes with normal, out_t with transpose")
     if not xs:
         return ([], []) if normal and transpose else []
-    dev = _check_matrices(xs, "xs")
+    dev, rows, cols, ptrs = _matrices(xs, "xs")
     code = _dtype_code(xs[0].dtype)
-    shapes = [tuple(x.shape) for x in xs]
 
-    def side(wanted, given, name, dims):
+    def side(wanted, given, name, r, k):
         if not wanted:
             return None, None, None
-        ops = [f8_empty(r, k, dev) for r, k in dims] if given is None else list(given)
+        r, k = array("q", r), array("q", k)
+        ops = [f8_empty(x, y, dev) for x, y in zip(r, k)] if given is None else list(given)
         if len(ops) != len(xs):
             raise ValueError(f"{name} must have one operand per matrix")
-        _, q, s = _f8_pointers(ops, name, dev, [(r, -(-k // F8_BLOCK) * F8_BLOCK) for r, k in dims])
+        got_r, got_k, q, s = _f8_pointers(ops, name, dev)
+        if got_r != r.tobytes() or got_k != _i64_bytes(-(-x // F8_BLOCK) * F8_BLOCK for x in k):
+            raise ValueError(f"{name}: an operand's values must be (rows, contracted side up to a "
+                             f"multiple of {F8_BLOCK})")
         return ops, q, s
 
-    ops, q, s = side(normal, out, "out", shapes)
-    ops_t, qt, st_ = side(transpose, out_t, "out_t", [(c, r) for r, c in shapes])
+    ops, q, s = side(normal, out, "out", rows, cols)
+    ops_t, qt, st_ = side(transpose, out_t, "out_t", cols, rows)
     if workspace is None:
         workspace = _byte_workspace(f8_workspace_bytes(len(xs)), dev)
-    rows, cols = array("q", [r for r, _ in shapes]), array("q", [c for _, c in shapes])
-    ptrs = array("Q", map(torch.Tensor.data_ptr, xs))
-    _call(load_library().muon_f8_quantize_batched, dev, workspace, len(xs), _addr(rows), _addr(cols),
-          _addr(ptrs), code, int(block_rows),
-          *(None if a is None else _addr(a) for a in (q, s, qt, st_)))
+    _call(load_library().muon_f8_quantize_batched, dev, workspace, len(xs), rows, cols, ptrs, code,
+          int(block_rows), q, s, qt, st_)
     return (ops, ops_t) if normal and transpose else ops if normal else ops_t
 
 
@@ -752,44 +748,42 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
     dev = a[0][0].device
     if dev.type != "cuda":
         raise ValueError(f"a: operands must live on a HIP device, got {dev}")
-    ash, aq, asc = _f8_pointers(a, "a", dev)
-    bsh, bq, bsc = _f8_pointers(b, "b", dev)
-    if [x[1] for x in ash] != [y[1] for y in bsh]:
-        i = next(i for i, (x, y) in enumerate(zip(ash, bsh)) if x[1] != y[1])
-        raise ValueError(f"product {i}: contracted sides {ash[i][1]} and {bsh[i][1]} differ")
-    shapes = [(x[0], y[0]) for x, y in zip(ash, bsh)]
+    m, ka, aq, asc = _f8_pointers(a, "a", dev)
+    n, kb, bq, bsc = _f8_pointers(b, "b", dev)
+    if ka != kb:
+        i, x, y = next((i, x, y) for i, (x, y) in enumerate(zip(array("q", ka), array("q", kb)))
+                       if x != y)
+        raise ValueError(f"product {i}: contracted sides {x} and {y} differ")
     if out is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
         _dtype_code(dt)
-        out = [torch.empty(s, dtype=dt, device=dev) for s in shapes]
+        out = [torch.empty(s, dtype=dt, device=dev) for s in zip(array("q", m), array("q", n))]
     else:
         out = list(out)
         if len(out) != len(a):
             raise ValueError("out must have one tensor per product")
         if out_dtype is not None and any(o.dtype != out_dtype for o in out):
             raise ValueError("out has another dtype than out_dtype")
-    if _check_matrices(out, "out") != dev:
+    odev, rows, cols, ptrs = _matrices(out, "out")
+    if odev != dev:
         raise ValueError("out must live on the operands' device")
-    if [tuple(o.shape) for o in out] != shapes:
+    if rows != m or cols != n:
         raise ValueError("out must have the shape (rows of a, rows of b)")
     code = _dtype_code(out[0].dtype)
     if workspace is None:
         workspace = _byte_workspace(f8_workspace_bytes(len(a)), dev)
-    m, n = array("q", [s[0] for s in shapes]), array("q", [s[1] for s in shapes])
-    k = array("q", [s[1] for s in ash])
-    ptrs = array("Q", map(torch.Tensor.data_ptr, out))
-    _call(load_library().muon_f8_matmul_batched, dev, workspace, len(a), _addr(m), _addr(n),
-          _addr(k), _addr(aq), _addr(asc), _addr(bq), _addr(bsc), _addr(ptrs), code,
-          1 if accumulate else 0)
+    _call(load_library().muon_f8_matmul_batched, dev, workspace, len(a), m, n, ka, aq, asc, bq, bsc,
+          ptrs, code, 1 if accumulate else 0)
     return out
 
 
-def _check_matrices(ts, name):
-    """_check_tensors over whole lists at a time."""
-    dev = ts[0].device
-    if dev.type != "cuda" or not _all_same(ts, dev, ts[0].dtype) or any(t.dim() != 2 for t in ts):
-        return _check_tensors(ts, name)  # says what is wrong
-    return dev
+def _matrices(ts, name):
+    """(device, rows, columns, pointers) of contiguous 2-D tensors of one dtype, the
+    last three as the bytes of C arrays."""
+    index, flags, _, _, ptrs, rows, cols = _lists().scan(ts)
+    if index < 0 or flags & (_FLAT | _MATRICES) != _FLAT | _MATRICES:
+        _check_tensors(ts, name)  # says what is wrong
+    return ts[0].device, rows, cols, ptrs
 
 
 def hbm_stream(ins: Sequence, outs: Sequence, nontemporal: bool = False) -> None:

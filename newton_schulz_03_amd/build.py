@@ -7,7 +7,8 @@ objects are linked into newton_schulz_03_amd/lib/libmuon_mi355x.so.  A second
 library, libmuon_mi355x_tiletrace.so, links the same objects except the bf16
 matrix-core source, compiled with -DMUON_TILE_TRACE: its kernels record a
 per-workgroup timeline (`python bench.py --tile-timeline` reads it).  The
-default library's kernels carry none of that code.
+default library's kernels carry none of that code.  tensor_lists.so, host code
+against the installed torch's headers, reads lists of tensors for the binding.
 """
 from __future__ import annotations
 
@@ -26,6 +27,8 @@ LIBDIR = os.path.join(PKG, "lib")
 LIBNAME = "libmuon_mi355x.so"
 TRACE_LIBNAME = "libmuon_mi355x_tiletrace.so"
 TRACE_SOURCE = "gemm_bf16.hip"  # the one source with timeline hooks
+LISTS_SOURCE = "tensor_lists.cpp"  # CPython extension: lists of torch tensors
+LISTS_LIBNAME = "tensor_lists.so"
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
@@ -82,6 +85,31 @@ def _link(objs, name: str, verbose: bool) -> str:
     return out
 
 
+def _build_lists(verbose: bool) -> str:
+    """The CPython extension that reads lists of torch tensors (host code, g++)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    out = os.path.join(LIBDIR, LISTS_LIBNAME)
+    tmp = out + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f for d in [sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+             for f in ("-isystem", d)),
+           os.path.join(CSRC, LISTS_SOURCE), "-o", tmp,
+           *(f"-L{d}" for d in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {LISTS_SOURCE}:\n{res.stdout}{res.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def build(verbose: bool = False, save_temps: str | None = None) -> str:
     """Compile every kernel source and link the shared library (and the
     timeline build beside it); returns the library's path."""
@@ -89,8 +117,10 @@ def build(verbose: bool = False, save_temps: str | None = None) -> str:
     os.makedirs(LIBDIR, exist_ok=True)
     srcs = sources()
     jobs = [(s, False) for s in srcs] + [(os.path.join(CSRC, TRACE_SOURCE), True)]
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
+        lists = ex.submit(_build_lists, verbose)
         objs = list(ex.map(lambda j: _compile(j[0], save_temps, verbose, j[1]), jobs))
+        lists.result()
     plain, trace_obj = objs[:len(srcs)], objs[-1]
     out = _link(plain, LIBNAME, verbose)
     _link([trace_obj if os.path.basename(s) == TRACE_SOURCE else o for s, o in zip(srcs, plain)],
