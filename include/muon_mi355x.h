@@ -294,6 +294,9 @@ int32_t muon_adamw_batched(int32_t batch, const int64_t* numel, void* const* p,
  *    each gradient by the factor in fp32 as they read it: no extra pass, and no
  *    rounding of s * g to the gradient's type.
  *
+ * A tensor may appear more than once in a norm; no output may overlap another
+ * tensor's gradient or output.
+ *
  * These tensors may have different types: dtype[i] (and out_dtype[i]) is
  * MUON_BF16 or MUON_FP32 for tensor i.  Other conventions are those at the top
  * of this header; in addition these calls enqueue kernel launches only, so they
@@ -365,7 +368,7 @@ int32_t muon_adamw_batched_scaled(int32_t batch, const int64_t* numel, void* con
  * multiple of 16:
  *   values  R x Kp bytes, row-major: OCP e4m3 (no infinity, largest 448),
  *           columns K .. Kp-1 zero
- *   scales  Kp/MUON_F8_BLOCK x Rp bytes, row-major: byte [kb][r] = e + 127, the
+ *   scales  Kp/MUON_F8_BLOCK x Rp bytes, row-major: byte [kb][r] = e + 127 (0 .. 254), the
  *           power of two 2^e that scales columns 128 kb .. 128 kb + 127 of row r;
  *           entries r >= R zero
  * Both 16-byte aligned.  A value stands for e4m3 * 2^e.

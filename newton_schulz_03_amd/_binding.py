@@ -487,6 +487,16 @@ def _byte_workspace(nbytes: int, dev):
     return ws[off:off + nbytes]
 
 
+def _workspace(given, nbytes, dev):
+    import torch
+
+    if given is None:
+        return _byte_workspace(nbytes, dev)
+    if given.device != dev or given.dtype != torch.uint8 or not given.is_contiguous():
+        raise ValueError("workspace: a contiguous uint8 tensor on the device of the other tensors")
+    return given
+
+
 def _flat_tensors(ts, name, dev=None):
     """(device, dtype codes, element counts, pointers) of contiguous bf16 / fp32
     tensors, the last three as the bytes of C arrays."""
@@ -557,8 +567,7 @@ def grad_norm_batched(grads: Sequence, max_norm: Optional[float] = None, norm_ty
     p = _norm_params(max_norm, norm_type, eps)
     dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
     result = _norm_result(result, dev)
-    if workspace is None:
-        workspace = _byte_workspace(_grad_table_bytes(len(grads)), dev)
+    workspace = _workspace(workspace, _grad_table_bytes(len(grads)), dev)
     _call(load_library().muon_grad_norm_batched, dev, workspace, len(grads), numels,
           ptrs, codes, ctypes.byref(p), result.data_ptr())
     return result
@@ -590,8 +599,7 @@ def grad_scale_batched(grads: Sequence, scale, out: Optional[Sequence] = None,
     dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
     out, ocodes, optrs = _grad_outputs(grads, out, dev, codes, numels, ptrs)
     factor = _scale_pointer(scale, dev)
-    if workspace is None:
-        workspace = _byte_workspace(_grad_table_bytes(len(grads)), dev)
+    workspace = _workspace(workspace, _grad_table_bytes(len(grads)), dev)
     _call(load_library().muon_grad_scale_batched, dev, workspace, len(grads), numels,
           ptrs, codes, optrs, ocodes, factor)
     return out
@@ -614,8 +622,7 @@ def grad_clip_batched(grads: Sequence, max_norm: float, norm_type: float = 2.0, 
     dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
     _, ocodes, optrs = _grad_outputs(grads, out, dev, codes, numels, ptrs)
     result = _norm_result(result, dev)
-    if workspace is None:
-        workspace = _byte_workspace(_grad_table_bytes(len(grads)), dev)
+    workspace = _workspace(workspace, _grad_table_bytes(len(grads)), dev)
     _call(load_library().muon_grad_clip_batched, dev, workspace, len(grads), numels,
           ptrs, codes, optrs, ocodes, ctypes.byref(p),
           result.data_ptr())
@@ -718,8 +725,7 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
 
     ops, q, s = side(normal, out, "out", rows, cols)
     ops_t, qt, st_ = side(transpose, out_t, "out_t", cols, rows)
-    if workspace is None:
-        workspace = _byte_workspace(f8_workspace_bytes(len(xs)), dev)
+    workspace = _workspace(workspace, f8_workspace_bytes(len(xs)), dev)
     _call(load_library().muon_f8_quantize_batched, dev, workspace, len(xs), rows, cols, ptrs, code,
           int(block_rows), q, s, qt, st_)
     return (ops, ops_t) if normal and transpose else ops if normal else ops_t
@@ -770,8 +776,7 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
     if rows != m or cols != n:
         raise ValueError("out must have the shape (rows of a, rows of b)")
     code = _dtype_code(out[0].dtype)
-    if workspace is None:
-        workspace = _byte_workspace(f8_workspace_bytes(len(a)), dev)
+    workspace = _workspace(workspace, f8_workspace_bytes(len(a)), dev)
     _call(load_library().muon_f8_matmul_batched, dev, workspace, len(a), m, n, ka, aq, asc, bq, bsc,
           ptrs, code, 1 if accumulate else 0)
     return out

@@ -61,10 +61,12 @@ __device__ __forceinline__ void adamw_update(const AdamParams& a, float& p, floa
 }
 
 template <typename T, bool SCALED>
-__global__ __launch_bounds__(kThreads) void k_adamw(ArgTable, AdamCtx c, AdamParams a) {
+__global__ __launch_bounds__(kThreads) void k_adamw(ArgTable, AdamCtx c, AdamParams a,
+                                                    int32_t nblocks) {
   __shared__ int slot;
+  const int32_t b = block_number();
+  if (b >= nblocks) return;
   const float gs = SCALED ? *a.g_scale : 1.f;
-  const int32_t b = blockIdx.x;
   const char* const table = table_base(c.table);
   const int32_t* const prefix = reinterpret_cast<const int32_t*>(table + c.prefix_off);
   const int j = __builtin_amdgcn_readfirstlane(locate_matrix(prefix, c.batch, b, &slot));
@@ -113,7 +115,8 @@ namespace {
 
 template <typename T, bool SCALED>
 hipError_t run_adamw(const ArgTable& t, const AdamCtx& c, int32_t nblocks, const AdamParams& a) {
-  hipLaunchKernelGGL((k_adamw<T, SCALED>), dim3(nblocks), dim3(kThreads), 0, c.stream, t, c, a);
+  hipLaunchKernelGGL((k_adamw<T, SCALED>), block_grid(nblocks), dim3(kThreads), 0, c.stream,
+                     t, c, a, nblocks);
   return hipGetLastError();
 }
 

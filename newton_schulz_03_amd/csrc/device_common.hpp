@@ -155,6 +155,18 @@ __device__ __forceinline__ const char* table_base(const void* mem) {
                         : (const char*)(__builtin_amdgcn_kernarg_segment_ptr());
 }
 
+// A launch of many small blocks spreads them over two grid dimensions: one
+// dimension holds fewer than 2^32 threads, which the largest tensors of this
+// GPU's memory pass.  At most one block per row of the grid is idle.
+constexpr int64_t kGridRow = 1 << 16;
+inline dim3 block_grid(int64_t nblocks) {
+  const int64_t y = (nblocks + kGridRow - 1) / kGridRow;
+  return dim3(static_cast<uint32_t>((nblocks + y - 1) / y), static_cast<uint32_t>(y));
+}
+__device__ __forceinline__ int32_t block_number() {
+  return static_cast<int32_t>(blockIdx.y * gridDim.x + blockIdx.x);
+}
+
 // Index j with prefix[j] <= b < prefix[j+1] (b < prefix[batch]); exactly one
 // interval holds b, and empty intervals never match.  Up to kLocateScan
 // matrices the whole block finds it at once: every thread tests a few

@@ -266,15 +266,17 @@ __device__ __forceinline__ void scale_span(const Ti* g, To* o, int64_t n, float 
 template <bool NT>
 __global__ __launch_bounds__(kThreads) void k_grad_scale(ArgTable, GradCtx ctx, const float* scale,
                                                          GradNormArgs p, int32_t kind,
-                                                         int32_t nparts) {
+                                                         int32_t nparts, int32_t chunks) {
   constexpr int kPer = static_cast<int>(kGradSpan / kScaleSpan);  // blocks per chunk
+  const int32_t b = block_number();
+  if (b / kPer >= chunks) return;
   float s;
   if (nparts == 0)
     s = *scale;
   else
     s = kind == 0 ? factor_of_few<SumSq>(p, nparts) : factor_of_few<MaxAbs>(p, nparts);
-  const Chunk k = find_chunk(ctx, blockIdx.x / kPer);
-  const int64_t off = static_cast<int64_t>(blockIdx.x % kPer) * kScaleSpan;
+  const Chunk k = find_chunk(ctx, b / kPer);
+  const int64_t off = static_cast<int64_t>(b % kPer) * kScaleSpan;
   const int64_t left = k.n - off, n = left < kScaleSpan ? left : kScaleSpan;
   if (n <= 0 || (s == 1.f && k.out == k.g)) return;
   const uint16_t* gh = static_cast<const uint16_t*>(k.g) + k.base + off;
@@ -332,15 +334,15 @@ hipError_t launch_grad_scale(const ArgTable& t, const GradCtx& c, int32_t chunks
                              const float* scale, const GradNormArgs* joined, int32_t kind,
                              int64_t bytes) {
   if (chunks <= 0) return hipSuccess;
-  const dim3 grid(static_cast<uint32_t>(chunks) * static_cast<uint32_t>(kGradSpan / kScaleSpan));
+  const dim3 grid = block_grid(chunks * (kGradSpan / kScaleSpan));
   const GradNormArgs p = joined != nullptr ? *joined : GradNormArgs{};
   const int32_t nparts = joined != nullptr ? norm_grid(chunks) : 0;
   if (bytes > kNtScaleBytes)
     hipLaunchKernelGGL(k_grad_scale<true>, grid, dim3(kThreads), 0, c.stream, t, c, scale, p, kind,
-                       nparts);
+                       nparts, chunks);
   else
     hipLaunchKernelGGL(k_grad_scale<false>, grid, dim3(kThreads), 0, c.stream, t, c, scale, p, kind,
-                       nparts);
+                       nparts, chunks);
   return hipGetLastError();
 }
 

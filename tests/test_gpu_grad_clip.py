@@ -115,6 +115,23 @@ def test_norm_more_chunks_than_blocks():
         check_result(nsa.grad_norm_batched(ts, max_norm=0.25, norm_type=kind), ts, kind, 0.25)
 
 
+def test_more_blocks_than_a_grid_row():
+    """The scale pass gives 4096 elements to a block and AdamW 1024; 65536 blocks
+    fill a row of their grids.  The elements around that edge and at the end."""
+    row = 65536
+    g = torch.full((row * 4096 + 5000,), 3.0, dtype=BF16, device="cuda")
+    nsa.grad_scale_batched([g], torch.full((1,), 0.5, device="cuda"))
+    assert bool((g == 1.5).all())
+    n = row * 1024 + 1500
+    p, d = torch.full((n,), 2.0, device="cuda"), torch.ones(n, device="cuda")
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    nsa.adamw_batched([p], [d], [m], [v], lr=0.25, betas=(0.5, 0.5), eps=0.0, weight_decay=0.0)
+    # by the formulas, all exact: m = v = 1/2, the corrected moments are 1, p = 2 - 1/4 * 1 / 1
+    # up to the roundings of lr / (1 - 1/2), sqrt(1/2) and its inverse: 8 half units
+    assert bool((m == 0.5).all()) and bool((v == 0.5).all())
+    assert float((p - 1.75).abs().max()) <= 8 * U32
+
+
 def test_norm_over_the_range_of_fp32():
     # squares beyond fp32's range on either side
     for v, kinds in ((1e25, (2, math.inf)), (1e-25, (2, math.inf)), (3e38, (math.inf,)),
@@ -332,3 +349,10 @@ def test_binding_refuses_what_the_library_cannot_see():
         nsa.grad_norm_batched([t[1:]])  # not 16-byte aligned
     with pytest.raises(nsa.MuonError):
         nsa.grad_norm_batched([t], max_norm=-1.0)
+    n = nsa.grad_workspace_bytes([64])
+    for bad in (torch.empty(n, dtype=torch.uint8), torch.empty(n, device="cuda"),
+                torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            nsa.grad_norm_batched([t], workspace=bad)
+    with pytest.raises(nsa.MuonError):
+        nsa.grad_norm_batched([t], workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
