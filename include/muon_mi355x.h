@@ -400,8 +400,9 @@ int32_t muon_adamw_batched_scaled(int32_t batch, const int64_t* numel, void* con
  * products take the same call: dX = dY W with operands dY and W^T, and
  * dW = dY^T X with operands dY^T and X^T.
  *
- * Every size lies in [0, MUON_F8_MAX_DIM]; pointers of empty operands are not
- * read.  workspace: at least muon_f8_workspace_bytes(batch) bytes, 256-byte
+ * Every size lies in [0, MUON_F8_MAX_DIM], and a call's outputs hold fewer than
+ * about 1.7e10 elements (MUON_ERR_UNSUPPORTED otherwise); pointers of empty
+ * operands are not read.  workspace: at least muon_f8_workspace_bytes(batch) bytes, 256-byte
  * aligned.  Like the calls above, both can be captured into a HIP graph.
  */
 #define MUON_F8_BLOCK 128

@@ -181,9 +181,12 @@ int32_t check_ptr(const void* p, const char* what, int32_t i) {
   return MUON_OK;
 }
 
+// A launch holds fewer than 2^32 threads; outputs of 1.7e10 elements or more
+// reach that.
+constexpr int64_t kMaxBlocks = (1ll << 24) - 1;
 int32_t add_blocks(int64_t a, int64_t b, int64_t& total) {
-  total += a * b;  // at most 2^27 blocks of one matrix
-  if (total > INT32_MAX) return fail(MUON_ERR_UNSUPPORTED, "batch needs more than 2^31 blocks");
+  total += a * b;  // at most 2^32 blocks of one matrix
+  if (total > kMaxBlocks) return fail(MUON_ERR_UNSUPPORTED, "batch needs 2^24 blocks or more");
   return MUON_OK;
 }
 
@@ -312,7 +315,7 @@ int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int3
       const int64_t left = std::max<int64_t>(0, d.m - static_cast<int64_t>(d.full) * kF8Tile);
       if ((st = add_blocks(d.full, tn, nf)) != MUON_OK) return st;
       if ((st = add_blocks(cdiv(left, kF8Tile / 2), tn, nh)) != MUON_OK) return st;
-      if (nf + nh > INT32_MAX) return fail(MUON_ERR_UNSUPPORTED, "batch needs more than 2^31 blocks");
+      if (nf + nh > kMaxBlocks) return fail(MUON_ERR_UNSUPPORTED, "batch needs 2^24 blocks or more");
     } else if (d.m > 0) {
       if ((st = add_blocks(cdiv(d.m, 16 * sp.mt), cdiv(d.n, 16 * sp.nt), ns)) != MUON_OK) return st;
     }

@@ -100,12 +100,17 @@ PyObject* same_shapes(PyObject*, PyObject* args) {
   Py_ssize_t n, m;
   if (items(a, &n) == nullptr || items(b, &m) == nullptr) return nullptr;
   if (n != m) Py_RETURN_FALSE;
-  for (Py_ssize_t i = 0; i < n; ++i) {
-    const at::Tensor *x = tensor_at(a, i), *y = tensor_at(b, i);
-    if (x == nullptr || y == nullptr) return nullptr;
-    if (x->sizes() != y->sizes()) Py_RETURN_FALSE;
+  try {
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      const at::Tensor *x = tensor_at(a, i), *y = tensor_at(b, i);
+      if (x == nullptr || y == nullptr) return nullptr;
+      if (x->sizes() != y->sizes()) Py_RETURN_FALSE;
+    }
+    Py_RETURN_TRUE;
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
   }
-  Py_RETURN_TRUE;
 }
 
 // scan_f8(operands, block) -> (device, bad, kind, rows, padded K, values, scales)

@@ -169,6 +169,8 @@ def test_quantize_refusals(lib):
     assert call(rows=(nsa.F8_MAX_DIM + 1,)) == UNSUPPORTED
     assert call(cols=(nsa.F8_MAX_DIM + 1,)) == UNSUPPORTED
     assert call(rows=(1 << 40,)) == UNSUPPORTED
+    # 2^26 tiles of 128 x 128: more threads than one launch holds
+    assert call(rows=(nsa.F8_MAX_DIM,), cols=(nsa.F8_MAX_DIM,)) == UNSUPPORTED
     for bad in (0, FAKE + 8):
         assert call(x=(bad,)) == INVALID
         assert call(q=(bad,)) == INVALID
@@ -194,6 +196,7 @@ def test_matmul_refusals(lib):
     for dim in ("m", "n", "k"):
         assert call(**{dim: (-1,)}) == INVALID
         assert call(**{dim: (nsa.F8_MAX_DIM + 1,)}) == UNSUPPORTED
+    assert call(m=(nsa.F8_MAX_DIM,), n=(nsa.F8_MAX_DIM,)) == UNSUPPORTED
     for arr in ("a", "sa", "b", "sb", "c"):
         assert call(**{arr: None}) == INVALID
         assert call(**{arr: (0,)}) == INVALID
