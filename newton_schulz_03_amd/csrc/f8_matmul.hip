@@ -502,6 +502,28 @@ __device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32
 
 }  // namespace
 
+namespace {
+
+// Block `blk` of the n that the prefixes number: its product (*j) and its tile
+// there.  Each XCD takes one contiguous range of the launch (neighbouring tiles
+// share operands), or, with `spread`, one contiguous eighth of every product:
+// block g then belongs to the product that holds g, and the product's blocks of
+// one XCD (equal g % 8) become neighbours.
+__device__ __forceinline__ int32_t place_block(const F8ProdCtx& c, const int32_t* prefix,
+                                               int32_t blk, int32_t n, int* slot, int* j) {
+  const int32_t b = c.spread ? blk : xcd_remap(blk, n);
+  *j = __builtin_amdgcn_readfirstlane(locate_matrix(prefix, c.batch, b, slot));
+  const int32_t p0 = load_const(prefix + *j);
+  if (!c.spread) return b - p0;
+  const int32_t p1 = load_const(prefix + *j + 1), x = blk % kXcd;
+  // blocks below p on XCDs below x, and on XCD x
+  auto before = [&](int32_t p) { return p / kXcd * x + min(p % kXcd, x); };
+  auto mine = [&](int32_t p) { return (p + kXcd - 1 - x) / kXcd; };
+  return before(p1) - before(p0) + blk / kXcd - mine(p0);
+}
+
+}  // namespace
+
 // The launch's tiles: full ones of 256 x 256 first, then half ones of 128 x 256
 // (F8ProdDesc::full: the product's rows of full tiles; the half ones follow
 // them), which end ragged products and fill the launch's last round.  Both add
@@ -514,10 +536,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c, 
   const bool half = static_cast<int32_t>(blockIdx.x) >= nfull;
   const int32_t* const prefix =
       reinterpret_cast<const int32_t*>(table + c.prefix_off) + (half ? c.batch + 1 : 0);
-  const int32_t b = half ? xcd_remap(blockIdx.x - nfull, gridDim.x - nfull) : xcd_remap(blockIdx.x, nfull);
-  const int j = __builtin_amdgcn_readfirstlane(locate_matrix(prefix, c.batch, b, &slot));
+  int j;
+  const int32_t t = half ? place_block(c, prefix, blockIdx.x - nfull, gridDim.x - nfull, &slot, &j)
+                         : place_block(c, prefix, blockIdx.x, nfull, &slot, &j);
   const F8ProdDesc d = load_const(reinterpret_cast<const F8ProdDesc*>(table) + j);
-  const int32_t t = b - load_const(prefix + j);
   // down a column of tiles: B stays
   if (!half) {
     prod_tile<T, ADD, 4>(d, t % d.full * kTile, t / d.full * kTile, smem);
@@ -623,12 +645,11 @@ __global__ __launch_bounds__(kThreads) void k_f8_small(ArgTable, F8ProdCtx c) {
   constexpr int BM = 16 * MT, BN = 16 * NT, PITCH = S::kPitch;
   __shared__ __attribute__((aligned(1024))) char smem[4 * S::kWaveBytes];
   __shared__ int slot;
-  const int32_t blk = xcd_remap(blockIdx.x, gridDim.x);
   const char* const table = table_base(c.table);
   const int32_t* const prefix = reinterpret_cast<const int32_t*>(table + c.prefix_off);
-  const int j = __builtin_amdgcn_readfirstlane(locate_matrix(prefix, c.batch, blk, &slot));
+  int j;
+  const int32_t t = place_block(c, prefix, blockIdx.x, gridDim.x, &slot, &j);
   const F8ProdDesc d = load_const(reinterpret_cast<const F8ProdDesc*>(table) + j);
-  const int32_t t = blk - load_const(prefix + j);
   const int32_t tm = (d.m + BM - 1) / BM;
   const int32_t m0 = t % tm * BM, n0 = t / tm * BN;
   const int lane = threadIdx.x & 63;

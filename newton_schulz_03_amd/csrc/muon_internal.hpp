@@ -253,6 +253,7 @@ struct F8ProdCtx {
   int32_t prefix_off;      // of the prefixes of the kernel launched
   int32_t batch;
   int32_t accumulate;
+  int32_t spread;          // 1: every XCD takes an eighth of every product
   hipStream_t stream;
 };
 // Two prefix arrays: full tiles (nfull of them), half tiles.

@@ -245,6 +245,21 @@ def test_matmul_large_tiles(out, accumulate):
         assert (room[i][:16] == 3).all() and (room[i][16 + s[0] * s[1]:] == 3).all(), s
 
 
+@pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("m,n", [(1100, 1290), (1290, 1500), (16, 2000), (70, 900)])
+def test_matmul_lengths_that_differ(out, m, n):
+    # every product's blocks are dealt over the chip, longest sums first
+    shapes = [(m, n, k) for k in (130, 256, 4000, 300, 2000, 0, 700)] + [(m // 2, n // 3, 3900)]
+    a, b = operands(shapes, 2500, b_rows=128)
+    room = [torch.full((16 + r * c + 16,), 3.0, dtype=out, device="cuda") for r, c, _ in shapes]
+    c = [x[16:16 + s[0] * s[1]].view(s[:2]) for x, s in zip(room, shapes)]
+    nsa.f8_matmul_batched(a, b, out=c)
+    torch.cuda.synchronize()
+    for i, s in enumerate(shapes):
+        check_product(c[i], a[i], b[i], None, s)
+        assert (room[i][:16] == 3).all() and (room[i][16 + s[0] * s[1]:] == 3).all(), s
+
+
 @pytest.mark.parametrize("tiles", [255, 257, 300, 513])
 def test_matmul_last_round_in_half_tiles(tiles):
     # one row of tiles more or less than whole rounds of the chip: the bits of a
