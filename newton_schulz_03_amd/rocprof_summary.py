@@ -57,7 +57,10 @@ SHORT_NAMES = (("k_gemm_bf16<0,false,false,false>", "gram"), ("k_gemm_bf16<1,fal
                ("k_gemm_bf16<2,true,true,false>", "prod_finish_budget"),
                ("k_gemm_bf16<2,true,true,true>", "prod_finish_first_budget"),
                ("k_gemm_staged", "gemm_fp32"), ("k_prepare", "prepare"), ("k_finish", "finish"),
-               ("k_finalize", "norm"), ("k_adamw", "adamw"))
+               ("k_finalize", "norm"), ("k_adamw", "adamw"),
+               ("k_grad_norm", "grad_norm"), ("k_grad_finish", "grad_finish"),
+               ("k_grad_scale", "grad_scale"), ("k_f8_quantize", "f8_quantize"),
+               ("k_f8_prod", "f8_prod"), ("k_f8_small", "f8_prod_few"))
 
 
 def kernel_source_digest() -> str:
