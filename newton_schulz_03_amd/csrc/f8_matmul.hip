@@ -170,8 +170,8 @@ __device__ __forceinline__ void set_half(i32x8_t& f, int h, const u32x4_t& v) {
 // chunk c of row r at c ^ r; they come out as whole rows, so that every store
 // covers full 128-byte lines (written from the accumulators, 16 bytes a row,
 // the store ran at 2.5 TB/s).  ADD: the old C of one ni is requested while the
-// one before it is stored.
-template <typename T, bool ADD, int NQ>
+// one before it is stored.  NT: C passes the caches by (F8ProdCtx::nt).
+template <typename T, bool ADD, int NQ, bool NT>
 __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][NQ], char* lds, T* c, int32_t m0,
                                            int32_t n0, int32_t m, int32_t n, int lane) {
   constexpr int V = Elt<T>::kVec;            // columns per lane: 16 bytes
@@ -189,7 +189,10 @@ __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][NQ], char* l
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int32_t r = NQ * (RPI * i + rr0) + ni;
-      if (fast && m0 + r < m) to[i] = ld16(corner + static_cast<int64_t>(r) * n);
+      if (fast && m0 + r < m) {
+        const T* const at = corner + static_cast<int64_t>(r) * n;
+        to[i] = NT ? ld16_nt(at) : ld16(at);
+      }
     }
   };
   if constexpr (ADD) request(0, old[0]);
@@ -227,7 +230,10 @@ __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][NQ], char* l
 #pragma unroll
           for (int e = 0; e < V; ++e) v[e] += o[e];
         }
-        st16(to, f32_to_vec<T>(v));
+        if constexpr (NT)
+          st16_nt(to, f32_to_vec<T>(v));
+        else
+          st16(to, f32_to_vec<T>(v));
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -240,7 +246,8 @@ __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][NQ], char* l
 
 // One tile: 256 columns of C from n0, 64 NQ rows from m0.
 template <typename T, bool ADD, int NQ>
-__device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32_t n0, char* smem) {
+__device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32_t n0, char* smem,
+                                          bool nt) {
   constexpr int kRows = 64 * NQ;
   constexpr int kPLoads = RowStream<4>::kLoads, kQLoads = RowStream<NQ>::kLoads;
   constexpr int kLoads = kPLoads + kQLoads + 1;  // per wave and block
@@ -496,8 +503,12 @@ __device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32
     wait_vm<0>();  // no load may still target LDS: the buffers are reused for the store
   }
   __syncthreads();
-  store_part<T, ADD, NQ>(acc, smem + wave * 16384, static_cast<T*>(d.c), m0 + 32 * NQ * wn,
-                         n0 + 128 * wm, d.m, d.n, lane);
+  if (nt)
+    store_part<T, ADD, NQ, true>(acc, smem + wave * 16384, static_cast<T*>(d.c), m0 + 32 * NQ * wn,
+                                 n0 + 128 * wm, d.m, d.n, lane);
+  else
+    store_part<T, ADD, NQ, false>(acc, smem + wave * 16384, static_cast<T*>(d.c), m0 + 32 * NQ * wn,
+                                  n0 + 128 * wm, d.m, d.n, lane);
 }
 
 }  // namespace
@@ -542,10 +553,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c, 
   const F8ProdDesc d = load_const(reinterpret_cast<const F8ProdDesc*>(table) + j);
   // down a column of tiles: B stays
   if (!half) {
-    prod_tile<T, ADD, 4>(d, t % d.full * kTile, t / d.full * kTile, smem);
+    prod_tile<T, ADD, 4>(d, t % d.full * kTile, t / d.full * kTile, smem, c.nt != 0);
   } else {
     const int32_t halves = (d.m - d.full * kTile + kTile / 2 - 1) / (kTile / 2);
-    prod_tile<T, ADD, 2>(d, d.full * kTile + t % halves * (kTile / 2), t / halves * kTile, smem);
+    prod_tile<T, ADD, 2>(d, d.full * kTile + t % halves * (kTile / 2), t / halves * kTile, smem,
+                         c.nt != 0);
   }
 }
 

@@ -254,6 +254,7 @@ struct F8ProdCtx {
   int32_t batch;
   int32_t accumulate;
   int32_t spread;          // 1: every XCD takes an eighth of every product
+  int32_t nt;              // 1: C is read and written with the nontemporal hint
   hipStream_t stream;
 };
 // Two prefix arrays: full tiles (nfull of them), half tiles.

@@ -273,6 +273,20 @@ def test_matmul_last_round_in_half_tiles(tiles):
         check_product(c[rows.cuda()], (part[0], part[1]), b, what=tiles)
 
 
+@pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_matmul_outputs_past_the_caches(out, accumulate):
+    # more than 256 MB, which passes the caches by; rows at the tiles' edges and others
+    m, n = 8300, 8200 if out == FP32 else 16400
+    (a,), (b,) = operands([(m, n, 200)], 3500)
+    c = torch.ones(m, n, dtype=out, device="cuda")
+    nsa.f8_matmul_batched([a], [b], out=[c], accumulate=accumulate)
+    rows = torch.cat([torch.arange(250, 260), torch.arange(m - 140, m),
+                      torch.randperm(m, generator=torch.Generator().manual_seed(2))[:150]]).cuda()
+    part = (a.q[rows], torch.nn.functional.pad(a.scales[:, rows], (0, 4)))  # up to 304
+    check_product(c[rows], part, b, np.ones((300, n)) if accumulate else None)
+
+
 @pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 31, 33, 48, 64, 65, 100, 129, 200])
 def test_matmul_few_rows(m):
     shapes = [(m, 520, 1280), (m, 136, 256), (m, 33, 4096)]
