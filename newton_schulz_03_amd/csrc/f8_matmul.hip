@@ -67,7 +67,8 @@ __device__ __forceinline__ i32x4_t make_rsrc(const uint8_t* base, uint32_t bytes
   return r;
 }
 
-// One operand's 64 N rows of the tile (N = 4, or 2 for A in a half tile), 128
+// One operand's 64 N rows of the tile (N = 4; 2 or 1 for A in a half or quarter
+// tile), 128
 // bytes of each per block.  LDS row 32 (N h + i) + r holds tile row
 // 32 N h + N r + i, its 16-byte chunk c at c ^ ((r / 2) % 8): the rows of a
 // fragment read then fall on distinct banks.
@@ -293,8 +294,10 @@ __device__ __forceinline__ void prod_tile(const F8ProdDesc& d, int32_t m0, int32
     auto q_scales = [&](const char* buf) -> int32_t {
       if constexpr (NQ == 4)
         return *reinterpret_cast<const int32_t*>(buf + qsc);
-      else
+      else if constexpr (NQ == 2)
         return *reinterpret_cast<const uint16_t*>(buf + qsc);
+      else
+        return *reinterpret_cast<const uint8_t*>(buf + qsc);
     };
 
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LDS_AS char*)smem));
@@ -536,28 +539,42 @@ __device__ __forceinline__ int32_t place_block(const F8ProdCtx& c, const int32_t
 }  // namespace
 
 // The launch's tiles: full ones of 256 x 256 first, then half ones of 128 x 256
-// (F8ProdDesc::full: the product's rows of full tiles; the half ones follow
-// them), which end ragged products and fill the launch's last round.  Both add
-// every element up the same way.
+// and quarter ones of 64 x 256 (F8ProdDesc: the product's rows of each; the
+// quarter ones take the rest), which end ragged products and fill the launch's
+// last round.  All of them add every element up the same way.
 template <typename T, bool ADD>
-__global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c, int32_t nfull) {
+__global__ __launch_bounds__(kThreads, 1) void k_f8_prod(ArgTable, F8ProdCtx c, int32_t nfull,
+                                                         int32_t nhalf) {
   __shared__ __attribute__((aligned(1024))) char smem[LDS8];
   __shared__ int slot;
   const char* const table = table_base(c.table);
-  const bool half = static_cast<int32_t>(blockIdx.x) >= nfull;
+  int32_t blk = blockIdx.x, n = nfull, kind = 0;
+  if (blk >= nfull) {
+    blk -= nfull;
+    n = nhalf;
+    kind = 1;
+    if (blk >= nhalf) {
+      blk -= nhalf;
+      n = static_cast<int32_t>(gridDim.x) - nfull - nhalf;
+      kind = 2;
+    }
+  }
   const int32_t* const prefix =
-      reinterpret_cast<const int32_t*>(table + c.prefix_off) + (half ? c.batch + 1 : 0);
+      reinterpret_cast<const int32_t*>(table + c.prefix_off) + kind * (c.batch + 1);
   int j;
-  const int32_t t = half ? place_block(c, prefix, blockIdx.x - nfull, gridDim.x - nfull, &slot, &j)
-                         : place_block(c, prefix, blockIdx.x, nfull, &slot, &j);
+  const int32_t t = place_block(c, prefix, blk, n, &slot, &j);
   const F8ProdDesc d = load_const(reinterpret_cast<const F8ProdDesc*>(table) + j);
+  const int32_t full = d.full, half = d.half;
   // down a column of tiles: B stays
-  if (!half) {
-    prod_tile<T, ADD, 4>(d, t % d.full * kTile, t / d.full * kTile, smem, c.nt != 0);
-  } else {
-    const int32_t halves = (d.m - d.full * kTile + kTile / 2 - 1) / (kTile / 2);
-    prod_tile<T, ADD, 2>(d, d.full * kTile + t % halves * (kTile / 2), t / halves * kTile, smem,
+  if (kind == 0) {
+    prod_tile<T, ADD, 4>(d, t % full * kTile, t / full * kTile, smem, c.nt != 0);
+  } else if (kind == 1) {
+    prod_tile<T, ADD, 2>(d, full * kTile + t % half * (kTile / 2), t / half * kTile, smem,
                          c.nt != 0);
+  } else {
+    const int32_t row0 = full * kTile + half * (kTile / 2);
+    const int32_t rows = (d.m - row0 + kTile / 4 - 1) / (kTile / 4);
+    prod_tile<T, ADD, 1>(d, row0 + t % rows * (kTile / 4), t / rows * kTile, smem, c.nt != 0);
   }
 }
 
@@ -835,21 +852,23 @@ hipError_t launch_f8_small(const ArgTable& t, const F8ProdCtx& c, int32_t nblock
 namespace {
 
 template <typename T>
-hipError_t run_prod(const ArgTable& t, const F8ProdCtx& c, int32_t nfull, int32_t nhalf) {
-  const dim3 grid(nfull + nhalf);
+hipError_t run_prod(const ArgTable& t, const F8ProdCtx& c, int32_t nfull, int32_t nhalf,
+                    int32_t nquarter) {
+  const dim3 grid(nfull + nhalf + nquarter);
   if (c.accumulate)
-    hipLaunchKernelGGL((k_f8_prod<T, true>), grid, dim3(kThreads), 0, c.stream, t, c, nfull);
+    hipLaunchKernelGGL((k_f8_prod<T, true>), grid, dim3(kThreads), 0, c.stream, t, c, nfull, nhalf);
   else
-    hipLaunchKernelGGL((k_f8_prod<T, false>), grid, dim3(kThreads), 0, c.stream, t, c, nfull);
+    hipLaunchKernelGGL((k_f8_prod<T, false>), grid, dim3(kThreads), 0, c.stream, t, c, nfull, nhalf);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_f8_prod(const ArgTable& t, const F8ProdCtx& c, int32_t nfull, int32_t nhalf,
-                          bool is_bf16) {
-  if (nfull + nhalf <= 0) return hipSuccess;
-  return is_bf16 ? run_prod<uint16_t>(t, c, nfull, nhalf) : run_prod<float>(t, c, nfull, nhalf);
+                          int32_t nquarter, bool is_bf16) {
+  if (nfull + nhalf + nquarter <= 0) return hipSuccess;
+  return is_bf16 ? run_prod<uint16_t>(t, c, nfull, nhalf, nquarter)
+                 : run_prod<float>(t, c, nfull, nhalf, nquarter);
 }
 
 }  // namespace muon

@@ -245,11 +245,12 @@ struct F8ProdDesc {
   const uint8_t *b, *sb;   // n rows
   void* c;                 // m x n, bf16 or fp32
   int32_t m, n, kp;        // kp: the operands' padded K
-  int32_t full;            // rows of full tiles in the large-tile kernel; half tiles follow
+  uint16_t full, half;     // rows of full and half tiles in the large-tile kernel; quarter
+                           // tiles follow
 };
 struct F8ProdCtx {
-  const void* table;       // as GradCtx: descriptors, then batch+1 prefixes of full tiles,
-                           // of half tiles and of the few-rows kernel's blocks
+  const void* table;       // as GradCtx: descriptors, then batch+1 prefixes of full, half and
+                           // quarter tiles and of the few-rows kernel's blocks
   int32_t prefix_off;      // of the prefixes of the kernel launched
   int32_t batch;
   int32_t accumulate;
@@ -257,9 +258,9 @@ struct F8ProdCtx {
   int32_t nt;              // 1: C is read and written with the nontemporal hint
   hipStream_t stream;
 };
-// Two prefix arrays: full tiles (nfull of them), half tiles.
+// Three prefix arrays: full, half and quarter tiles.
 hipError_t launch_f8_prod(const ArgTable& t, const F8ProdCtx& c, int32_t nfull, int32_t nhalf,
-                          bool is_bf16);
+                          int32_t nquarter, bool is_bf16);
 constexpr int kF8Tile = 256;  // output tile (both sides)
 // The kernel of few rows: blocks of 16 mt x 16 nt, mt in {1, 2, 4}, nt in {1, 4}.
 hipError_t launch_f8_small(const ArgTable& t, const F8ProdCtx& c, int32_t nblocks, bool is_bf16,

@@ -171,7 +171,7 @@ size_t f8_desc_bytes(int32_t batch) {
                   kAlign);
 }
 size_t f8_ws_bytes(int32_t batch) {
-  return f8_desc_bytes(batch) + align_up(3 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1), kAlign);
+  return f8_desc_bytes(batch) + align_up(4 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1), kAlign);
 }
 
 int32_t check_ptr(const void* p, const char* what, int32_t i) {
@@ -202,67 +202,143 @@ constexpr int64_t kNtBytes = 256'000'000;
 constexpr double kFixedSlices = 12;  // a tile's fixed cost in K slices of 64
 constexpr double kUneven = 1.05;
 constexpr int64_t kSpreadTiles = 16;
-constexpr double kCus = 256;
+constexpr int64_t kCus = 256;
 
 struct SmallPlan {
   int32_t mt = 1, nt = 4;
 };
 
-// Rounds that F full tiles and then H half ones take on the chip, in full tiles
-// (a half tile took 0.65 of a full one's time).
-constexpr double kHalfCost = 0.65;
-double rounds(int64_t f, int64_t h) {
-  const int64_t cus = static_cast<int64_t>(kCus), q = f / cus, r = f % cus;
-  const double t = static_cast<double>(q);
-  if (h == 0) return t + (r > 0 ? 1.0 : 0.0);
-  const double alone = kHalfCost * static_cast<double>(cdiv(h, cus - r));
-  if (r == 0) return t + alone;
-  if (alone <= 1.0) return t + 1.0;
-  return t + std::max(1.0, (static_cast<double>(r) + kHalfCost * static_cast<double>(h)) / kCus + 0.5 * kHalfCost);
+// Prefixes over the products (batch + 1 each): their full, half and quarter tiles
+// and their blocks in the kernel of few rows.
+struct BlockCounts {
+  static constexpr int kKinds = 4;
+  size_t batch;
+  std::vector<int32_t> prefix;
+  explicit BlockCounts(size_t n) : batch(n), prefix(kKinds * (n + 1), 0) {}
+  int32_t* at(int kind) { return prefix.data() + kind * (batch + 1); }
+  const int32_t* at(int kind) const { return prefix.data() + kind * (batch + 1); }
+  int32_t total(int kind) const { return at(kind)[batch]; }
+};
+
+// Times of a full, a half and a quarter tile, us, by the K slices of 64 (fitted
+// to launches of two whole rounds at K = 2048 and 6144; bf16, K = 6144: 87, 52 and
+// 33 us), and what a launch takes besides.
+struct TileTimes {
+  double t[3];
+  TileTimes(bool bf16, double slices)
+      : t{bf16 ? 6.4 + 0.84 * slices : 9.8 + 1.54 * slices,
+          bf16 ? 5.3 + 0.48 * slices : 9.9 + 0.77 * slices,
+          bf16 ? 5.2 + 0.29 * slices : 6.5 + 0.53 * slices} {}
+};
+constexpr double kLaunch = 4;
+
+// When the launch's last CU ends: its full tiles, then the half ones, then the
+// quarter ones, each on the CU that is free first.
+double launch_end(const TileTimes& c, const int64_t (&n)[3]) {
+  // CUs by the time at which they are free, earliest first: one group, and one
+  // more for each kind that ends within a group
+  struct Group {
+    double at;
+    int64_t cus;
+  } g[5] = {{0.0, kCus}};
+  int groups = 1;
+  double end = 0;
+  for (int k = 0; k < 3; ++k) {
+    int64_t left = n[k];
+    if (left == 0) continue;
+    if (left >= 4 * kCus) {  // whole rounds of one kind
+      const int64_t r = left / kCus - 2;
+      for (int i = 0; i < groups; ++i) g[i].at += static_cast<double>(r) * c.t[k];
+      left -= r * kCus;
+    }
+    while (left > 0) {
+      const double at = g[0].at + c.t[k];
+      const int64_t take = std::min(left, g[0].cus);
+      left -= take;
+      if ((g[0].cus -= take) == 0) {
+        for (int i = 1; i < groups; ++i) g[i - 1] = g[i];
+        --groups;
+      }
+      int to = groups;
+      for (; to > 0 && g[to - 1].at > at; --to) g[to] = g[to - 1];
+      g[to] = {at, take};
+      ++groups;
+    }
+    end = g[groups - 1].at;
+  }
+  return end;
 }
 
-// Rows of full and half tiles of the products that the large-tile kernel takes:
-// a rest of up to 128 rows is one half tile, and where it shortens the launch's
-// last round, the last full tiles become two half ones each.
-double cut_rows(std::vector<F8ProdDesc>& desc, const std::vector<char>& large) {
-  int64_t f = 0, h = 0;
+// Rows of full, half and quarter tiles of the products that the large-tile
+// kernel takes: a product's rest of up to 64, 128 or 192 rows is a quarter tile, a
+// half one, or one of each (or quarter ones only), and where it ends the launch
+// earlier, full tiles of its last round become two half or four quarter ones
+// each.  (2048^3, 64 full tiles: 15.7 us in quarter tiles, 18.3 in half ones; with an
+// fp32 result 26 and 37; 16 products 1089 x 2048 x 6144: 196 us, with half tiles only
+// 201.)  Returns when the launch ends.
+double cut_rows(std::vector<F8ProdDesc>& desc, const std::vector<char>& large, const TileTimes& c) {
+  int64_t f = 0, base[2][3] = {};  // by whether the rests take half tiles
   for (size_t i = 0; i < desc.size(); ++i) {
     F8ProdDesc& d = desc[i];
     if (!large[i]) continue;
-    const int32_t rest = d.m % kF8Tile;
-    d.full = d.m / kF8Tile + (rest > kF8Tile / 2 ? 1 : 0);
-    const int64_t tn = cdiv(d.n, kF8Tile);
+    const int64_t tn = cdiv(d.n, kF8Tile), q = cdiv(d.m % kF8Tile, kF8Tile / 4);
+    d.full = static_cast<uint16_t>(d.m / kF8Tile + (q == 4 ? 1 : 0));
     f += d.full * tn;
-    h += rest > 0 && rest <= kF8Tile / 2 ? tn : 0;
-  }
-  // one row of tiles at a time, from the end, as long as a whole last round's
-  // worth has not been split
-  const int64_t most = f % static_cast<int64_t>(kCus);
-  double best = rounds(f, h);
-  int64_t take = 0, bf = f, bh = h, taken = 0;
-  for (size_t i = desc.size(); i-- > 0 && taken < most;) {
-    if (!large[i]) continue;
-    const F8ProdDesc& d = desc[i];
-    const int64_t tn = cdiv(d.n, kF8Tile);
-    for (int32_t k = 0; k < d.full && taken < most; ++k) {
-      // the last full row may hold fewer than 256 rows, but more than 128
-      taken += tn;
-      bf -= tn;
-      bh += 2 * tn;
-      if (const double r = rounds(bf, bh); r < best) {
-        best = r;
-        take = taken;
-      }
+    if (q < 4) {
+      base[0][2] += q * tn;
+      base[1][1] += q / 2 * tn;
+      base[1][2] += q % 2 * tn;
     }
   }
-  for (size_t i = desc.size(); i-- > 0 && take > 0;) {
+  // one row of tiles at a time, from the end, as long as a whole last round's
+  // worth has not been cut
+  const int64_t most = f % kCus, step = most / 16;
+  int64_t best_take = 0;
+  int best_kind = 1, best_rest = 1;
+  const double uncut = launch_end(c, {f, base[1][1], base[1][2]});
+  // more and smaller tiles have to gain 5%: they load more, and this knows
+  // nothing of the clock (16 products 300 x 2048 x 6144, bf16: one round with whole
+  // tiles 76 us, two without 86)
+  double best = 0.95 * uncut;
+  auto consider = [&](int64_t taken) {
+    for (int rest = base[1][1] > 0 ? 0 : 1; rest < 2; ++rest)
+      for (int kind = 1; kind < (taken > 0 ? 3 : 2); ++kind) {
+        int64_t n[3] = {f - taken, base[rest][1], base[rest][2]};
+        n[kind] += taken * 2 * kind;
+        const double r = launch_end(c, n);
+        if (r < best) {
+          best = r;
+          best_take = taken;
+          best_kind = kind;
+          best_rest = rest;
+        }
+      }
+  };
+  consider(0);
+  int64_t taken = 0, next = 0;
+  for (size_t i = desc.size(); i-- > 0 && taken < most;) {
+    if (!large[i]) continue;
+    const int64_t tn = cdiv(desc[i].n, kF8Tile);
+    for (int32_t k = 0; k < desc[i].full && taken < most; ++k) {
+      taken += tn;
+      if (taken < next && taken < most) continue;
+      consider(taken);
+      next = taken + step;
+    }
+  }
+  if (best_take == 0 && best_rest == 1) best = uncut;
+  taken = best_take;
+  for (size_t i = desc.size(); i-- > 0;) {
     if (!large[i]) continue;
     F8ProdDesc& d = desc[i];
     const int64_t tn = cdiv(d.n, kF8Tile);
-    while (d.full > 0 && take > 0) {
+    const int64_t q = cdiv(d.m % kF8Tile, kF8Tile / 4);
+    int64_t half = best_rest == 1 && q < 4 ? q / 2 : 0;
+    for (; d.full > 0 && taken > 0; taken -= tn) {
       --d.full;
-      take -= tn;
+      half += best_kind == 1 ? 2 : 0;
     }
+    d.half = static_cast<uint16_t>(half);
   }
   return best;
 }
@@ -273,13 +349,12 @@ double cut_rows(std::vector<F8ProdDesc>& desc, const std::vector<char>& large) {
 // Products of up to kFewRows rows go to that kernel: B's bytes bound them, and
 // its blocks are as many as B's 64-row pieces (24 products 4 x 2048 x 6144: 50 us
 // against 91 in 256 x 256 tiles).  The others go, all of them to one kernel, where
-// these estimates say that the call ends first: us per tile or block on one of
-// the 256 CUs, a fixed part and one per K slice (64 deep in the tiles; 512 in the
-// blocks, whose four waves share K), which grows in the tiles as the chip fills
-// up.  (bf16, 1024^3: 21 us in tiles, 6.5 in blocks; 2048^3: 18.5 and 28;
-// 4096^3: 67 and 189.)
-int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int32_t>& full,
-                      std::vector<int32_t>& half, std::vector<int32_t>& small, SmallPlan& sp) {
+// these estimates say that the call ends first: TileTimes, or us per block on one
+// of the 256 CUs, a fixed part and one per 512 of K, which its four waves share.
+// (bf16, 1024^3: 14 us in tiles, 6.5 in blocks; 2048^3: 15.7 and 28; 4096^3: 58 and
+// 189.)
+int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, BlockCounts& out,
+                      SmallPlan& sp) {
   double tiles = 0, slices = 0, blocks = 0, steps = 0;
   int32_t few_rows = 0;
   std::vector<char> large(desc.size(), 0);
@@ -299,9 +374,7 @@ int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int3
   }
   bool all_small = true;
   if (tiles > 0) {
-    const double filled = std::min(1.0, tiles / kCus);
-    const double fixed = bf16 ? 8 : 13, slice = bf16 ? 0.45 + 0.33 * filled : 1.25 + 0.1 * filled;
-    const double large_us = cut_rows(desc, large) * (fixed + slice * slices / tiles);
+    const double large_us = kLaunch + cut_rows(desc, large, TileTimes(bf16, slices / tiles));
     const double small_us = std::ceil(blocks / kCus) * (3.0 + 1.25 * steps / blocks);
     all_small = small_us < large_us;
   }
@@ -315,22 +388,22 @@ int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int3
     if (const F8ProdDesc& d = desc[i]; d.m > 0 && !large[i])
       n64 += static_cast<double>(cdiv(d.m, 16 * sp.mt)) * static_cast<double>(cdiv(d.n, 64));
   sp.nt = n64 >= 96 ? 4 : n64 >= 48 ? 2 : 1;
-  int64_t nf = 0, nh = 0, ns = 0;
+  int64_t n[BlockCounts::kKinds] = {};
   int32_t st;
   for (size_t i = 0; i < desc.size(); ++i) {
     const F8ProdDesc& d = desc[i];
     if (large[i]) {
       const int64_t tn = cdiv(d.n, kF8Tile);
-      const int64_t left = std::max<int64_t>(0, d.m - static_cast<int64_t>(d.full) * kF8Tile);
-      if ((st = add_blocks(d.full, tn, nf)) != MUON_OK) return st;
-      if ((st = add_blocks(cdiv(left, kF8Tile / 2), tn, nh)) != MUON_OK) return st;
-      if (nf + nh > kMaxBlocks) return fail(MUON_ERR_UNSUPPORTED, "batch needs 2^24 blocks or more");
+      const int64_t left = d.m - static_cast<int64_t>(d.full) * kF8Tile - d.half * (kF8Tile / 2);
+      const int64_t rows[3] = {d.full, d.half, left > 0 ? cdiv(left, kF8Tile / 4) : 0};
+      for (int k = 0; k < 3; ++k)
+        if ((st = add_blocks(rows[k], tn, n[k])) != MUON_OK) return st;
+      if (n[0] + n[1] + n[2] > kMaxBlocks)
+        return fail(MUON_ERR_UNSUPPORTED, "batch needs 2^24 blocks or more");
     } else if (d.m > 0) {
-      if ((st = add_blocks(cdiv(d.m, 16 * sp.mt), cdiv(d.n, 16 * sp.nt), ns)) != MUON_OK) return st;
+      if ((st = add_blocks(cdiv(d.m, 16 * sp.mt), cdiv(d.n, 16 * sp.nt), n[3])) != MUON_OK) return st;
     }
-    full[i + 1] = static_cast<int32_t>(nf);
-    half[i + 1] = static_cast<int32_t>(nh);
-    small[i + 1] = static_cast<int32_t>(ns);
+    for (int k = 0; k < BlockCounts::kKinds; ++k) out.at(k)[i + 1] = static_cast<int32_t>(n[k]);
   }
   return MUON_OK;
 }
@@ -344,8 +417,8 @@ int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, std::vector<int3
 // products 1024 x 2048 x 6144: 195 us against 184; 8 tiles a product, 32 products
 // 512 x 1024, K 1059 to 2931: 52 against 43.  Products of fewer than
 // kSpreadTiles tiles on average stay whole.
-bool uneven(const std::vector<F8ProdDesc>& desc, const std::vector<int32_t>& prefix) {
-  const int64_t n = prefix.back();
+bool uneven(const std::vector<F8ProdDesc>& desc, const int32_t* prefix) {
+  const int64_t n = prefix[desc.size()];
   double all = 0, most = 0, sum = 0;
   int64_t at = 0;
   int32_t x = 0;
@@ -563,8 +636,6 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
         b == nullptr || sb == nullptr || c == nullptr)
       return fail(MUON_ERR_INVALID_ARG, "an argument array is null");
     std::vector<F8ProdDesc> desc(batch);
-    // tiles of the two kernels, each product's in one of them
-    std::vector<int32_t> full(static_cast<size_t>(batch) + 1, 0), half(full), small(full);
     int32_t st;
     int64_t bytes = 0;
     for (int32_t i = 0; i < batch; ++i) {
@@ -596,25 +667,24 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
         d.m = 0;
       }
     }
+    BlockCounts blocks(batch);
     SmallPlan sp;
-    if ((st = plan_products(desc, dtype == MUON_BF16, full, half, small, sp)) != MUON_OK) return st;
-    const bool spread_tiles = full[batch] >= kSpreadTiles * batch && uneven(desc, full);
-    const bool spread_small = uneven(desc, small);
+    if ((st = plan_products(desc, dtype == MUON_BF16, blocks, sp)) != MUON_OK) return st;
+    const bool spread_tiles =
+        blocks.total(0) >= kSpreadTiles * batch && uneven(desc, blocks.at(0));
+    const bool spread_small = uneven(desc, blocks.at(3));
     if (spread_tiles || spread_small) {
       std::stable_sort(desc.begin(), desc.end(),
                        [](const F8ProdDesc& x, const F8ProdDesc& y) { return x.kp > y.kp; });
-      if ((st = plan_products(desc, dtype == MUON_BF16, full, half, small, sp)) != MUON_OK) return st;
+      if ((st = plan_products(desc, dtype == MUON_BF16, blocks, sp)) != MUON_OK) return st;
     }
     if ((st = check_workspace(workspace, workspace_bytes, f8_ws_bytes(batch))) != MUON_OK) return st;
     char* ws = static_cast<char*>(workspace);
     hipStream_t stm = static_cast<hipStream_t>(stream);
-    std::vector<int32_t> prefix(full);
-    prefix.insert(prefix.end(), half.begin(), half.end());
-    prefix.insert(prefix.end(), small.begin(), small.end());
     ArgTable t;
     F8ProdCtx x{};
-    if ((st = place_table(desc.data(), sizeof(F8ProdDesc) * batch, prefix.data(),
-                          sizeof(int32_t) * prefix.size(), ws, stm, t, &x.table)) != MUON_OK)
+    if ((st = place_table(desc.data(), sizeof(F8ProdDesc) * batch, blocks.prefix.data(),
+                          sizeof(int32_t) * blocks.prefix.size(), ws, stm, t, &x.table)) != MUON_OK)
       return st;
     x.prefix_off = static_cast<int32_t>(align_up(sizeof(F8ProdDesc) * batch, kAlign));
     x.batch = batch;
@@ -623,10 +693,11 @@ extern "C" int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const
     x.nt = bytes > kNtBytes ? 1 : 0;
     x.stream = stm;
     TimedLaunch tl(MUON_K_F8_PROD, stm);
-    hipError_t e = launch_f8_prod(t, x, full[batch], half[batch], dtype == MUON_BF16);
+    hipError_t e = launch_f8_prod(t, x, blocks.total(0), blocks.total(1), blocks.total(2),
+                                  dtype == MUON_BF16);
     x.spread = spread_small ? 1 : 0;
-    x.prefix_off += 2 * static_cast<int32_t>(sizeof(int32_t)) * (batch + 1);
-    if (e == hipSuccess) e = launch_f8_small(t, x, small[batch], dtype == MUON_BF16, sp.mt, sp.nt);
+    x.prefix_off += 3 * static_cast<int32_t>(sizeof(int32_t)) * (batch + 1);
+    if (e == hipSuccess) e = launch_f8_small(t, x, blocks.total(3), dtype == MUON_BF16, sp.mt, sp.nt);
     if (e != hipSuccess) return hip_fail(e, "launch e4m3 product");
     tl.done();
     return MUON_OK;

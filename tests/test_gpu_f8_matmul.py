@@ -246,6 +246,41 @@ def test_matmul_large_tiles(out, accumulate):
 
 
 @pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("shapes", [[(2048, 2048, 700)], [(1536, 1500, 1400)],
+                                    [(2048 + r, 1100, 500 + r) for r in (0, 20, 64, 100, 150, 192, 200)]])
+def test_matmul_smaller_tiles(out, shapes):
+    # launches of less than a round, and rests of rows of every kind
+    a, b = operands(shapes, 2700, b_rows=128)
+    room = [torch.full((16 + m * n + 16,), 3.0, dtype=out, device="cuda") for m, n, _ in shapes]
+    c = [x[16:16 + s[0] * s[1]].view(s[:2]) for x, s in zip(room, shapes)]
+    g = torch.Generator().manual_seed(7)
+    for x in c:
+        x.copy_(torch.randn(tuple(x.shape), generator=g))
+    old = [host_f64(x) for x in c]
+    nsa.f8_matmul_batched(a, b, out=c, accumulate=True)
+    torch.cuda.synchronize()
+    for i, s in enumerate(shapes):
+        check_product(c[i], a[i], b[i], old[i], s)
+        assert (room[i][:16] == 3).all() and (room[i][16 + s[0] * s[1]:] == 3).all(), s
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_matmul_tiles_of_every_size_give_the_same_bits(out):
+    # 2048 rows alone are cut into small tiles, among 16384 into whole ones
+    (a,), (b,) = operands([(16384, 2048, 700)], 2800)
+    (whole,) = nsa.f8_matmul_batched([a], [b], out_dtype=out)
+    for first, rows in ((0, 2048), (4096, 1536), (8192, 2048 + 160)):
+        part = (a.q[first:first + rows], a.scales[:, first:first + rows].contiguous())
+        (c,) = nsa.f8_matmul_batched([part], [b], out_dtype=out)
+        if out == FP32 and rows == 1536:
+            # 192 quarter tiles are estimated at 16.9 us and 768 blocks of the kernel of
+            # few rows at 16.5: that kernel's four waves share K, another order of the sum
+            check_product(c, part, b)
+        else:
+            assert torch.equal(c, whole[first:first + rows]), (first, rows)
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
 @pytest.mark.parametrize("m,n", [(1100, 1290), (1290, 1500), (16, 2000), (70, 900)])
 def test_matmul_lengths_that_differ(out, m, n):
     # every product's blocks are dealt over the chip, longest sums first

@@ -144,7 +144,7 @@ def test_scaled_steps_refuse_a_missing_factor(lib):
 
 def test_f8_workspace():
     for n in (0, 1, 7, 384):
-        assert nsa.f8_workspace_bytes(n) == up(56 * n, 256) + up(3 * 4 * (n + 1), 256)
+        assert nsa.f8_workspace_bytes(n) == up(56 * n, 256) + up(4 * 4 * (n + 1), 256)
     with pytest.raises(nsa.MuonError):
         nsa.f8_workspace_bytes(-1)
 
