@@ -192,7 +192,7 @@ int32_t add_blocks(int64_t a, int64_t b, int64_t& total) {
 
 int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
-constexpr int32_t kFewRows = 64;
+constexpr int32_t kFewRows = 64;  // most rows of one block of the kernel of few rows
 // Bytes of operands and outputs from which the outputs pass the caches by, which
 // leaves the operands there (8 products 4096 x 6144 x 2048, bf16: 367 us against
 // 403; 8 of 2048 x 6144 x 4096 added to fp32: 752 against 770).  Smaller calls gain
@@ -343,44 +343,79 @@ double cut_rows(std::vector<F8ProdDesc>& desc, const std::vector<char>& large, c
   return best;
 }
 
-// Which kernel takes which product, the rows of its tiles, and the block shape
-// of the kernel of few rows.
-//
-// Products of up to kFewRows rows go to that kernel: B's bytes bound them, and
-// its blocks are as many as B's 64-row pieces (24 products 4 x 2048 x 6144: 50 us
-// against 91 in 256 x 256 tiles).  The others go, all of them to one kernel, where
-// these estimates say that the call ends first: TileTimes, or us per block on one
-// of the 256 CUs, a fixed part and one per 512 of K, which its four waves share.
-// (bf16, 1024^3: 14 us in tiles, 6.5 in blocks; 2048^3: 15.7 and 28; 4096^3: 58 and
-// 189.)
-int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, BlockCounts& out,
-                      SmallPlan& sp) {
-  double tiles = 0, slices = 0, blocks = 0, steps = 0;
-  int32_t few_rows = 0;
-  std::vector<char> large(desc.size(), 0);
-  for (size_t i = 0; i < desc.size(); ++i) {
-    const F8ProdDesc& d = desc[i];
-    if (d.m <= kFewRows) {
-      few_rows = std::max(few_rows, d.m);
-      continue;
-    }
-    large[i] = 1;
+// What the estimates take from a set of products.
+struct Load {
+  double tiles = 0, slices = 0;  // full tiles, and the K slices of 64 in them
+  double blocks = 0, steps = 0;  // 64 x 64 blocks, and the steps of 512 in them
+  double bytes = 0;              // of the operands
+  int32_t rows = 0;              // most rows of a product
+  void add(const F8ProdDesc& d) {
     const double t = static_cast<double>(cdiv(d.m, kF8Tile)) * static_cast<double>(cdiv(d.n, kF8Tile));
     tiles += t;
     slices += t * (d.kp / 64);
     const double b = static_cast<double>(cdiv(d.m, 64)) * static_cast<double>(cdiv(d.n, 64));
     blocks += b;
     steps += b * static_cast<double>(cdiv(d.kp, 4 * kF8Block));
+    bytes += (static_cast<double>(d.m) + d.n) * d.kp;
+    rows = std::max(rows, d.m);
   }
-  bool all_small = true;
-  if (tiles > 0) {
-    const double large_us = kLaunch + cut_rows(desc, large, TileTimes(bf16, slices / tiles));
-    const double small_us = std::ceil(blocks / kCus) * (3.0 + 1.25 * steps / blocks);
-    all_small = small_us < large_us;
+};
+
+int32_t few_rows_mt(int32_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
+// When a call of the kernel of few rows ends, us: per block on one of the 256 CUs
+// a fixed part and one per 512 of K, which its four waves share, or the operands'
+// bytes at the rates measured with 16, 32 and 64 rows (5.4, 4.9, 4.5 TB/s).
+double blocks_end(const Load& l) {
+  if (l.blocks == 0) return 0;
+  const int32_t mt = few_rows_mt(l.rows);
+  return std::max(std::ceil(l.blocks / kCus) * (3.0 + 1.25 * l.steps / l.blocks),
+                  l.bytes / (mt == 1 ? 5.4e6 : mt == 2 ? 4.95e6 : 4.5e6));
+}
+
+// When a launch of tiles ends: TileTimes, or the operands' bytes at 5.5 TB/s
+// (fp32 results: 4.75).
+double tiles_end(std::vector<F8ProdDesc>& desc, const std::vector<char>& large, const Load& l,
+                 bool bf16) {
+  if (l.tiles == 0) return 0;
+  return std::max(kLaunch + cut_rows(desc, large, TileTimes(bf16, l.slices / l.tiles)),
+                  l.bytes / (bf16 ? 5.5e6 : 4.75e6));
+}
+
+// Which kernel takes which product, the rows of its tiles, and the block shape
+// of the kernel of few rows: all of the products in tiles, all in blocks, or those
+// of up to kFewRows rows in blocks and the others in tiles, as the estimates say.
+// (bf16, 1024^3: 14 us in tiles, 6.5 in blocks; 2048^3: 15.7 and 28; 4096^3: 58 and
+// 189; 8 products 8 x 2048 x 6144: 31 and 18; 32 of 48 rows 75 and 87, with fp32
+// results 87 and 97, of 8 rows 84 and 76.)
+int32_t plan_products(std::vector<F8ProdDesc>& desc, bool bf16, BlockCounts& out,
+                      SmallPlan& sp) {
+  Load few, many, all;
+  std::vector<char> large(desc.size(), 0);
+  auto take = [&](int32_t above) {  // products of more rows than this in tiles
+    for (size_t i = 0; i < desc.size(); ++i) large[i] = desc[i].m > above;
+  };
+  for (const F8ProdDesc& d : desc) {
+    if (d.m == 0) continue;
+    (d.m <= kFewRows ? few : many).add(d);
+    all.add(d);
   }
-  if (all_small && tiles > 0) few_rows = kFewRows;
-  if (all_small) std::fill(large.begin(), large.end(), 0);
-  sp.mt = few_rows <= 16 ? 1 : few_rows <= 32 ? 2 : 4;
+  const bool mixed = few.tiles > 0 && many.tiles > 0;
+  double best = 0.97 * blocks_end(all);  // near the same: blocks (16 of 4 rows: 32 us, tiles 34)
+  int32_t above = INT32_MAX;
+  for (int32_t a : {0, kFewRows}) {
+    if (a > 0 && !mixed) continue;
+    take(a);
+    const double us = tiles_end(desc, large, a > 0 ? many : all, bf16) + (a > 0 ? blocks_end(few) : 0);
+    if (us < best) {
+      best = us;
+      above = a;
+    }
+  }
+  take(above);
+  if (above == 0) tiles_end(desc, large, all, bf16);  // the rows of its tiles
+  if (above == kFewRows) tiles_end(desc, large, many, bf16);
+  sp.mt = few_rows_mt(above == INT32_MAX ? all.rows : few.rows);
   // narrower blocks while there are too few to occupy the chip (one product 4 x
   // 2048 x 6144: 9.3 us in 32 blocks, 7.6 in 64, 7.2 in 128)
   double n64 = 0;
