@@ -349,6 +349,7 @@ struct Load {
   double blocks = 0, steps = 0;  // 64 x 64 blocks, and the steps of 512 in them
   double bytes = 0;              // of the operands
   int32_t rows = 0;              // most rows of a product
+  int32_t kp = 0;                // longest sum
   void add(const F8ProdDesc& d) {
     const double t = static_cast<double>(cdiv(d.m, kF8Tile)) * static_cast<double>(cdiv(d.n, kF8Tile));
     tiles += t;
@@ -358,28 +359,31 @@ struct Load {
     steps += b * static_cast<double>(cdiv(d.kp, 4 * kF8Block));
     bytes += (static_cast<double>(d.m) + d.n) * d.kp;
     rows = std::max(rows, d.m);
+    kp = std::max(kp, d.kp);
   }
 };
 
 int32_t few_rows_mt(int32_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
 // When a call of the kernel of few rows ends, us: per block on one of the 256 CUs
-// a fixed part and one per 512 of K, which its four waves share, or the operands'
-// bytes at the rates measured with 16, 32 and 64 rows (5.4, 4.9, 4.5 TB/s).
+// a fixed part and one per 512 of K, which its four waves share, one block of the
+// longest sum, or the operands' bytes at the rates measured with 16, 32 and 64 rows (5.4, 4.9, 4.5 TB/s).
 double blocks_end(const Load& l) {
   if (l.blocks == 0) return 0;
   const int32_t mt = few_rows_mt(l.rows);
-  return std::max(std::ceil(l.blocks / kCus) * (3.0 + 1.25 * l.steps / l.blocks),
-                  l.bytes / (mt == 1 ? 5.4e6 : mt == 2 ? 4.95e6 : 4.5e6));
+  return std::max({std::ceil(l.blocks / kCus) * (3.0 + 1.25 * l.steps / l.blocks),
+                   3.0 + 1.25 * static_cast<double>(cdiv(l.kp, 4 * kF8Block)),
+                   l.bytes / (mt == 1 ? 5.4e6 : mt == 2 ? 4.95e6 : 4.5e6)});
 }
 
-// When a launch of tiles ends: TileTimes, or the operands' bytes at 5.5 TB/s
-// (fp32 results: 4.75).
+// When a launch of tiles ends: TileTimes at the mean length of the sums, a
+// quarter tile of the longest one, or the operands' bytes at 5.5 TB/s (fp32
+// results: 4.75).
 double tiles_end(std::vector<F8ProdDesc>& desc, const std::vector<char>& large, const Load& l,
                  bool bf16) {
   if (l.tiles == 0) return 0;
-  return std::max(kLaunch + cut_rows(desc, large, TileTimes(bf16, l.slices / l.tiles)),
-                  l.bytes / (bf16 ? 5.5e6 : 4.75e6));
+  return std::max({kLaunch + cut_rows(desc, large, TileTimes(bf16, l.slices / l.tiles)),
+                   kLaunch + TileTimes(bf16, l.kp / 64).t[2], l.bytes / (bf16 ? 5.5e6 : 4.75e6)});
 }
 
 // Which kernel takes which product, the rows of its tiles, and the block shape

@@ -332,6 +332,34 @@ def test_matmul_few_rows(m):
             check_product(c[i], a[i], b[i], what=s)
 
 
+@pytest.mark.parametrize("m", [3, 20, 50])
+@pytest.mark.parametrize("n", [3900, 7000])
+def test_matmul_few_rows_many_columns(m, n):
+    # wider blocks than the shapes above take
+    shapes = [(m, n, 700), (m - 2, 33, 300)]
+    a, b = operands(shapes, 60 + m + n, b_rows=128)
+    for out in (BF16, FP32):
+        c = nsa.f8_matmul_batched(a, b, out_dtype=out)
+        for i, s in enumerate(shapes):
+            check_product(c[i], a[i], b[i], what=s)
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("shapes", [[(4096, 4000, 300), (8, 64, 24000)],
+                                    [(4096, 4000, 300), (8, 64, 24000), (33, 70, 12000), (2048, 2048, 128)]])
+def test_matmul_long_sums_of_few_rows_beside_large_products(out, shapes):
+    # the few rows' long sums would outlast the tiles: the first call takes both
+    # kernels, the second one that of few rows
+    a, b = operands(shapes, 70, b_rows=128)
+    room = [torch.full((16 + m * n + 16,), 3.0, dtype=out, device="cuda") for m, n, _ in shapes]
+    c = [x[16:16 + s[0] * s[1]].view(s[:2]) for x, s in zip(room, shapes)]
+    nsa.f8_matmul_batched(a, b, out=c)
+    torch.cuda.synchronize()
+    for i, s in enumerate(shapes):
+        check_product(c[i], a[i], b[i], None, s)
+        assert (room[i][:16] == 3).all() and (room[i][16 + s[0] * s[1]:] == 3).all(), s
+
+
 @pytest.mark.parametrize("k", [1, 128, 129, 256, 320, 512, 640, 896, 1152])
 def test_matmul_lengths_of_the_sum(k):
     # one block, two, odd numbers of them
