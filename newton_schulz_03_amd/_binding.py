@@ -697,7 +697,7 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
     block_rows: 1 for a scale per 1 x 128 block along the contracted side
     (activations, gradients), 128 for one per 128 x 128 block (weights).
     Returns the operands, the transposes' operands, or a pair of both lists, in
-    `out` and `out_t` where given.
+    `out` and `out_t` where given; new ones of one list share an allocation.
     """
     import torch
 
@@ -714,12 +714,14 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
     def side(wanted, given, name, r, k):
         if not wanted:
             return None, None, None
-        r, k = array("q", r), array("q", k)
-        ops = [f8_empty(x, y, dev) for x, y in zip(r, k)] if given is None else list(given)
+        if given is None:
+            ops = _lists().room_f8(r, k, F8_BLOCK, dev.index, F8Operand)
+            return ops, *_f8_pointers(ops, name, dev)[2:]
+        ops = list(given)
         if len(ops) != len(xs):
             raise ValueError(f"{name} must have one operand per matrix")
         got_r, got_k, q, s = _f8_pointers(ops, name, dev)
-        if got_r != r.tobytes() or got_k != _i64_bytes(-(-x // F8_BLOCK) * F8_BLOCK for x in k):
+        if got_r != r or got_k != _i64_bytes(-(-x // F8_BLOCK) * F8_BLOCK for x in array("q", k)):
             raise ValueError(f"{name}: an operand's values must be (rows, contracted side up to a "
                              f"multiple of {F8_BLOCK})")
         return ops, q, s
@@ -738,8 +740,8 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
 
     a, b: sequences of F8Operand (or (values, scales) pairs) with equal
     contracted sides.  out: contiguous bf16 or fp32 tensors of (A's rows, B's
-    rows); without it new ones of out_dtype (bfloat16).  accumulate: the
-    products are added to `out`.  Sums are fp32, rounded once.  For
+    rows); without it new ones of out_dtype (bfloat16), in one allocation.
+    accumulate: the products are added to `out`.  Sums are fp32, rounded once.  For
     Y = X W^T: dX = dY W takes the operands of dY and W^T, and dW = dY^T X those
     of dY^T and X^T (f8_quantize_batched's transpose).  Returns the outputs.
     """
@@ -763,8 +765,7 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
         raise ValueError(f"product {i}: contracted sides {x} and {y} differ")
     if out is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
-        _dtype_code(dt)
-        out = [torch.empty(s, dtype=dt, device=dev) for s in zip(array("q", m), array("q", n))]
+        out = _lists().room(m, n, _dtype_code(dt), dev.index)
     else:
         out = list(out)
         if len(out) != len(a):

@@ -543,6 +543,33 @@ def test_a_training_step_of_two_experts():
         check_operand(o, host_f64(w), 128, "weights after the step")
 
 
+def test_new_outputs_are_ordinary_tensors():
+    # pieces of one allocation: shapes, neighbours, in-place work, gradients, lifetime
+    xs = [matrix(r, c, BF16, 40 + r, 1.0).cuda() for r, c in ((3, 130), (0, 40), (70, 300), (20, 0))]
+    ops, ops_t = nsa.f8_quantize_batched(xs, transpose=True)
+    for x, o, t in zip(xs, ops, ops_t):
+        r, c = x.shape
+        assert o.q.dtype == torch.float8_e4m3fn and o.scales.dtype == torch.uint8
+        assert o.q.shape == (r, up(c, BLOCK)) and o.scales.shape == (up(c, BLOCK) // BLOCK, up(r, 16))
+        assert t.q.shape == (c, up(r, BLOCK)) and t.scales.shape == (up(r, BLOCK) // BLOCK, up(c, 16))
+        for y in (*o, *t):
+            assert y.is_contiguous() and y.device == x.device and not y.requires_grad
+            assert y.numel() == 0 or y.data_ptr() % 16 == 0
+    c = nsa.f8_matmul_batched(ops, ops, out_dtype=FP32)
+    assert [tuple(y.shape) for y in c] == [(3, 3), (0, 0), (70, 70), (20, 20)]
+    kept = [y.clone() for y in c]
+    c[2].mul_(2)
+    assert torch.equal(c[2], 2 * kept[2]) and torch.equal(c[0], kept[0]) and torch.equal(c[3], kept[3])
+    w = c[2].requires_grad_()
+    (w * w).sum().backward()
+    assert torch.equal(w.grad, 2 * w.detach())
+    last = c[3]
+    del c, w
+    torch.cuda.synchronize()
+    junk = [torch.full((1 << 16,), 9.0, device="cuda") for _ in range(8)]
+    assert torch.equal(last, kept[3]) and len(junk) == 8
+
+
 def test_binding_refusals_on_the_gpu():
     a, b = operands([(5, 6, 200)], 900)
     with pytest.raises(ValueError):
