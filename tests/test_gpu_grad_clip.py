@@ -276,6 +276,23 @@ def test_adamw_with_a_factor(dtype):
         assert np.all(np.abs(got - pr) <= bp), float(np.max(np.abs(got - pr) / bp))
 
 
+@pytest.mark.parametrize("batch,numel", [(83, 100), (84, 100), (250, 3000), (84, 210000), (200, 130000)])
+def test_adamw_of_many_tensors_equals_one_at_a_time(batch, numel):
+    # up to 83 tensors in one argument table; more in a table in the workspace, or in
+    # several launches where each has 8192 blocks of 1024 elements
+    rng = np.random.default_rng(batch)
+    numels = [int(n) for n in rng.integers(numel - 50, numel + 50, batch)]
+    numels[0], numels[batch // 2], numels[-1] = 0, 0, 1
+    p, g, m, v = adamw_state(numels, BF16, batch)
+    q, n, w = ([x.clone() for x in t] for t in (p, m, v))
+    s = torch.full((1,), 0.3, device="cuda")
+    nsa.adamw_batched(p, g, m, v, step=2, grad_scale=s)
+    for a, b, c, d in zip(q, g, n, w):
+        nsa.adamw_batched([a], [b], [c], [d], step=2, grad_scale=s)
+    for x, y in ((p, q), (m, n), (v, w)):
+        assert all(torch.equal(a, b) for a, b in zip(x, y))
+
+
 def test_a_factor_of_one_changes_nothing():
     one = torch.ones(1, device="cuda")
     for dtype in (BF16, FP32):
