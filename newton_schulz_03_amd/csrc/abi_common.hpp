@@ -22,10 +22,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 int32_t check_workspace(const void* ws, size_t ws_bytes, size_t need);
 
 // A call's descriptor table: n descriptors of `desc_bytes` together, then a
-// second array (prefixes, or pointers; align_up(desc_bytes, kAlign) on).  Where it fits it becomes the
-// kernels' argument table; otherwise kernels that carry its pieces write it to
-// `ws`.  *mem: where it lies (null: the argument table).  Kernel launches only,
-// so that calls can be captured into a graph.
+// second array (prefixes, or pointers; align_up(desc_bytes, kAlign) on).  Where
+// it fits it becomes the kernels' argument table; otherwise kernels that carry
+// its pieces write it to `ws`.  *mem: where it lies (null: the argument table).
+// Kernel launches only, so that calls can be captured into a graph.
 int32_t place_table(const void* desc, size_t desc_bytes, const void* second, size_t second_bytes,
                     char* ws, hipStream_t stream, ArgTable& args, const void** mem);
 

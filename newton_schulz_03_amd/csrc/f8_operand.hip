@@ -5,8 +5,8 @@
 // 2^e: the smallest power of two, at least 2^-127, with the block's largest
 // finite magnitude at most 448 * 2^e (448: e4m3's largest value), so that
 // nothing saturates.  An element x is stored as the e4m3 rounding (to nearest
-// even) of x * 2^-e in one conversion (v_cvt_scalef32_pk_fp8_*).  Infinities and NaNs become NaN and take no part
-// in the scale.
+// even) of x * 2^-e in one conversion (v_cvt_scalef32_pk_fp8_*).  Infinities and
+// NaNs become NaN and take no part in the scale.
 //
 // Bandwidth-bound: one block per 128 x 128 tile reads it once, 16 bytes a lane
 // and every load issued first, and writes whole 128-byte rows of values; the

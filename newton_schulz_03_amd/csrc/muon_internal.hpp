@@ -179,7 +179,7 @@ hipError_t launch_adamw(const AdamCtx& c, int32_t nblocks, bool is_bf16, const A
 
 // Global gradient norm, clip factor and scaled gradients over a ragged batch.
 // Every tensor is cut into chunks of kGradSpan elements, numbered through the
-// batch by the prefix table.
+// batch.
 constexpr int64_t kGradSpan = 16384;
 constexpr int32_t kNormBlocks = 2048;  // most blocks (and partials) of the norm pass
 // 16 bytes a tensor, so that the gradients of a whole model (239 tensors) travel
@@ -262,7 +262,7 @@ struct F8ProdCtx {
 hipError_t launch_f8_prod(const ArgTable& t, const F8ProdCtx& c, int32_t nfull, int32_t nhalf,
                           int32_t nquarter, bool is_bf16);
 constexpr int kF8Tile = 256;  // output tile (both sides)
-// The kernel of few rows: blocks of 16 mt x 16 nt, mt in {1, 2, 4}, nt in {1, 4}.
+// The kernel of few rows: blocks of 16 mt x 16 nt, mt and nt in {1, 2, 4}.
 hipError_t launch_f8_small(const ArgTable& t, const F8ProdCtx& c, int32_t nblocks, bool is_bf16,
                            int32_t mt, int32_t nt);
 
