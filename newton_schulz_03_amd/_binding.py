@@ -539,15 +539,22 @@ def _norm_params(max_norm, norm_type, eps) -> GradNormParams:
                           0.0 if max_norm is None else float(max_norm), float(eps))
 
 
-def _norm_result(result, dev):
+def _norm_room(workspace, result, batch, dev):
+    """(workspace, result) of a norm: those given, or new ones."""
     import torch
 
+    nbytes = _grad_table_bytes(batch)
+    if workspace is None and result is None:
+        workspace, result = _lists().room_norm(nbytes, dev.index)
+        if workspace.data_ptr() % 256 == 0:  # as torch's allocator gives it
+            return workspace, result
+        workspace = None
     if result is None:
-        return torch.empty(2, dtype=torch.float32, device=dev)
-    if result.device != dev or result.dtype != torch.float32 or tuple(result.shape) != (2,) or \
+        result = torch.empty(2, dtype=torch.float32, device=dev)
+    elif result.device != dev or result.dtype != torch.float32 or tuple(result.shape) != (2,) or \
             not result.is_contiguous():
         raise ValueError("result: a contiguous float32 tensor of 2 elements on the gradients' device")
-    return result
+    return _workspace(workspace, nbytes, dev), result
 
 
 def grad_norm_batched(grads: Sequence, max_norm: Optional[float] = None, norm_type: float = 2.0,
@@ -567,8 +574,7 @@ def grad_norm_batched(grads: Sequence, max_norm: Optional[float] = None, norm_ty
         raise ValueError("grads: at least one tensor (its device holds the result)")
     p = _norm_params(max_norm, norm_type, eps)
     dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
-    result = _norm_result(result, dev)
-    workspace = _workspace(workspace, _grad_table_bytes(len(grads)), dev)
+    workspace, result = _norm_room(workspace, result, len(grads), dev)
     _call(load_library().muon_grad_norm_batched, dev, workspace, len(grads), numels,
           ptrs, codes, ctypes.byref(p), result.data_ptr())
     return result
@@ -622,8 +628,7 @@ def grad_clip_batched(grads: Sequence, max_norm: float, norm_type: float = 2.0, 
     p = _norm_params(max_norm, norm_type, eps)
     dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
     _, ocodes, optrs = _grad_outputs(grads, out, dev, codes, numels, ptrs)
-    result = _norm_result(result, dev)
-    workspace = _workspace(workspace, _grad_table_bytes(len(grads)), dev)
+    workspace, result = _norm_room(workspace, result, len(grads), dev)
     _call(load_library().muon_grad_clip_batched, dev, workspace, len(grads), numels,
           ptrs, codes, optrs, ocodes, ctypes.byref(p),
           result.data_ptr())

@@ -172,7 +172,7 @@ PyObject* scan_f8(PyObject*, PyObject* args) {
 }
 
 // Room for tensors on one HIP device: one allocation, cut into contiguous
-// two-dimensional pieces at multiples of 256 bytes.
+// pieces at multiples of 256 bytes.
 class Room {
  public:
   // Counts a piece; returns its offset.
@@ -185,11 +185,11 @@ class Room {
     whole_ = at::empty({bytes_}, at::TensorOptions().dtype(at::kByte).device(
                                      at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(device))));
   }
-  PyObject* piece(int64_t at, int64_t rows, int64_t cols, at::ScalarType type) const {
+  PyObject* piece(int64_t at, c10::IntArrayRef sizes, at::ScalarType type) const {
     auto impl = c10::make_intrusive<c10::TensorImpl>(
         c10::Storage(whole_.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
         c10::scalarTypeToTypeMeta(type));
-    impl->set_sizes_contiguous({rows, cols});
+    impl->set_sizes_contiguous(sizes);
     impl->set_storage_offset((whole_.storage_offset() + at) / static_cast<int64_t>(c10::elementSize(type)));
     return THPVariable_Wrap(at::Tensor(std::move(impl)));
   }
@@ -228,7 +228,7 @@ PyObject* room(PyObject*, PyObject* args) {
     all.allocate(device);
     list = PyList_New(n);
     for (Py_ssize_t i = 0; list != nullptr && i < n; ++i) {
-      PyObject* t = all.piece(at[i], rows[i], cols[i], type);
+      PyObject* t = all.piece(at[i], {rows[i], cols[i]}, type);
       if (t == nullptr) {
         Py_CLEAR(list);
         break;
@@ -265,9 +265,9 @@ PyObject* room_f8(PyObject*, PyObject* args) {
     list = PyList_New(n);
     for (Py_ssize_t i = 0; list != nullptr && i < n; ++i) {
       const int64_t kb = (cols[i] + block - 1) / block;
-      PyObject* a = all.piece(q[i], rows[i], kb * block, at::kFloat8_e4m3fn);
+      PyObject* a = all.piece(q[i], {rows[i], kb * block}, at::kFloat8_e4m3fn);
       PyObject* b = a == nullptr ? nullptr
-                                 : all.piece(s[i], kb, (rows[i] + 15) / 16 * 16, at::kByte);
+                                 : all.piece(s[i], {kb, (rows[i] + 15) / 16 * 16}, at::kByte);
       PyObject* op = b == nullptr ? nullptr : PyObject_CallFunctionObjArgs(kind, a, b, nullptr);
       Py_XDECREF(a);
       Py_XDECREF(b);
@@ -285,7 +285,25 @@ PyObject* room_f8(PyObject*, PyObject* args) {
   }
 }
 
+// room_norm(bytes, device) -> (workspace of so many bytes, two float32)
+PyObject* room_norm(PyObject*, PyObject* args) {
+  long long bytes;
+  int device;
+  if (!PyArg_ParseTuple(args, "Li", &bytes, &device)) return nullptr;
+  try {
+    Room all;
+    const int64_t ws = all.add(1, bytes, 1), result = all.add(1, 2, 4);
+    all.allocate(device);
+    return Py_BuildValue("NN", all.piece(ws, {static_cast<int64_t>(bytes)}, at::kByte),
+                         all.piece(result, {2}, at::kFloat));
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
 PyMethodDef methods[] = {
+    {"room_norm", room_norm, METH_VARARGS, "room_norm(bytes, device)"},
     {"room", room, METH_VARARGS, "room(rows, columns, dtype code, device)"},
     {"room_f8", room_f8, METH_VARARGS, "room_f8(rows, columns, block, device, kind)"},
     {"scan", scan, METH_O, "scan(tensors): device, flags, dtype codes, sizes, pointers"},
