@@ -424,14 +424,14 @@ def adamw_batched(params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg
     if dev.type != "cuda":
         raise ValueError(f"params must live on a HIP device, got {dev}")
     lists = _lists()
-    ptrs = []
-    for group, want in ((ps, ps[0].dtype), (gs, ps[0].dtype), (ms, torch.float32),
-                        (vs, torch.float32)):
-        index, flags, _, numels, where, _, _ = lists.scan(group)
+    ptrs = {}
+    for name, group, want in (("p", ps, ps[0].dtype), ("m", ms, torch.float32),
+                              ("v", vs, torch.float32), ("g", gs, ps[0].dtype)):
+        index, flags, _, numels, where, _, _ = lists.scan(group, name != "g")
         if index != dev.index or group[0].dtype != want or flags & _FLAT != _FLAT:
             raise ValueError("tensors must be contiguous on one device; p and g share a "
                              "dtype, the moments are float32")
-        ptrs.append(where)
+        ptrs[name] = where
     if not all(lists.same_shapes(ps, group) for group in (gs, ms, vs)):
         raise ValueError("p, g, m and v of one entry must have the same shape")
     code = _dtype_code(ps[0].dtype)
@@ -442,7 +442,8 @@ def adamw_batched(params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg
     fn, scale = lib.muon_adamw_batched, ()
     if grad_scale is not None:
         fn, scale = lib.muon_adamw_batched_scaled, (_scale_pointer(grad_scale, dev),)
-    _call(fn, dev, workspace, len(ps), numels, *ptrs, code, ctypes.byref(prm), *scale)
+    _call(fn, dev, workspace, len(ps), numels, ptrs["p"], ptrs["g"], ptrs["m"], ptrs["v"],
+          code, ctypes.byref(prm), *scale)
 
 
 _FLAT = 7  # of the lists' flags: one device, contiguous, one dtype
@@ -498,17 +499,17 @@ def _workspace(given, nbytes, dev):
     return given
 
 
-def _flat_tensors(ts, name, dev=None):
+def _flat_tensors(ts, name, written):
     """(device, dtype codes, element counts, pointers) of contiguous bf16 / fp32
-    tensors, the last three as the bytes of C arrays."""
+    tensors, the last three as the bytes of C arrays.  The lists that a call writes
+    are asked for before those it only reads."""
     import torch
 
-    index, flags, codes, numels, ptrs, _, _ = _lists().scan(ts)
-    if dev is None:
-        dev = ts[0].device
-        if index < 0:
-            raise ValueError(f"{name}: tensors must live on a HIP device, got {dev}")
-    if flags & (_SAME_DEVICE | _CONTIGUOUS) != _SAME_DEVICE | _CONTIGUOUS or index != dev.index:
+    index, flags, codes, numels, ptrs, _, _ = _lists().scan(ts, written)
+    dev = ts[0].device
+    if index < 0:
+        raise ValueError(f"{name}: tensors must live on a HIP device, got {dev}")
+    if flags & (_SAME_DEVICE | _CONTIGUOUS) != _SAME_DEVICE | _CONTIGUOUS:
         raise ValueError(f"{name}: tensors must be contiguous on one device")
     if b"\xff\xff\xff\xff" in codes:
         bad = next(t.dtype for t in ts if t.dtype not in (torch.bfloat16, torch.float32))
@@ -573,24 +574,29 @@ def grad_norm_batched(grads: Sequence, max_norm: Optional[float] = None, norm_ty
     if not grads:
         raise ValueError("grads: at least one tensor (its device holds the result)")
     p = _norm_params(max_norm, norm_type, eps)
-    dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
+    dev, codes, numels, ptrs = _flat_tensors(grads, "grads", False)
     workspace, result = _norm_room(workspace, result, len(grads), dev)
     _call(load_library().muon_grad_norm_batched, dev, workspace, len(grads), numels,
           ptrs, codes, ctypes.byref(p), result.data_ptr())
     return result
 
 
-def _grad_outputs(grads, out, dev, codes, numels, ptrs):
-    """(outputs, their dtype codes, their pointers)."""
+def _grads_and_outputs(grads, out):
+    """(device, dtype codes, element counts, pointers) of the gradients, then the
+    outputs, their dtype codes and pointers."""
     if out is None:
-        return grads, codes, ptrs
+        dev, codes, numels, ptrs = _flat_tensors(grads, "grads", True)
+        return dev, codes, numels, ptrs, grads, codes, ptrs
     out = list(out)
     if len(out) != len(grads):
         raise ValueError("out must have one tensor per gradient")
-    _, ocodes, onumels, optrs = _flat_tensors(out, "out", dev)
+    odev, ocodes, onumels, optrs = _flat_tensors(out, "out", True)
+    dev, codes, numels, ptrs = _flat_tensors(grads, "grads", False)
+    if odev != dev:
+        raise ValueError("out must live on the gradients' device")
     if onumels != numels:
         raise ValueError("out must have the gradients' sizes")
-    return out, ocodes, optrs
+    return dev, codes, numels, ptrs, out, ocodes, optrs
 
 
 def grad_scale_batched(grads: Sequence, scale, out: Optional[Sequence] = None,
@@ -603,8 +609,7 @@ def grad_scale_batched(grads: Sequence, scale, out: Optional[Sequence] = None,
     grads = list(grads)
     if not grads:
         return []
-    dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
-    out, ocodes, optrs = _grad_outputs(grads, out, dev, codes, numels, ptrs)
+    dev, codes, numels, ptrs, out, ocodes, optrs = _grads_and_outputs(grads, out)
     factor = _scale_pointer(scale, dev)
     workspace = _workspace(workspace, _grad_table_bytes(len(grads)), dev)
     _call(load_library().muon_grad_scale_batched, dev, workspace, len(grads), numels,
@@ -626,8 +631,7 @@ def grad_clip_batched(grads: Sequence, max_norm: float, norm_type: float = 2.0, 
     if max_norm is None:
         raise ValueError("max_norm is needed")
     p = _norm_params(max_norm, norm_type, eps)
-    dev, codes, numels, ptrs = _flat_tensors(grads, "grads")
-    _, ocodes, optrs = _grad_outputs(grads, out, dev, codes, numels, ptrs)
+    dev, codes, numels, ptrs, _, ocodes, optrs = _grads_and_outputs(grads, out)
     workspace, result = _norm_room(workspace, result, len(grads), dev)
     _call(load_library().muon_grad_clip_batched, dev, workspace, len(grads), numels,
           ptrs, codes, optrs, ocodes, ctypes.byref(p),
@@ -663,10 +667,10 @@ def f8_empty(rows: int, cols: int, device) -> F8Operand:
                      torch.empty((kp // F8_BLOCK, rp), dtype=torch.uint8, device=device))
 
 
-def _f8_pointers(ops, name, dev):
+def _f8_pointers(ops, name, dev, written=False):
     """(rows, padded contracted sides, value pointers, scale pointers) of operands,
     as the bytes of C arrays."""
-    index, bad, kind, rows, kps, qs, ss = _lists().scan_f8(ops, F8_BLOCK)
+    index, bad, kind, rows, kps, qs, ss = _lists().scan_f8(ops, F8_BLOCK, written)
     if bad >= 0 and kind == 1:
         raise TypeError(f"{name}: an operand is a float8_e4m3fn tensor and a uint8 tensor")
     if index != dev.index or (bad >= 0 and kind == 2):
@@ -713,6 +717,16 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
         raise ValueError("out goes with normal, out_t with transpose")
     if not xs:
         return ([], []) if normal and transpose else []
+
+    def written(given, name):
+        if given is None:
+            return None
+        ops = list(given)
+        if len(ops) != len(xs):
+            raise ValueError(f"{name} must have one operand per matrix")
+        return ops, *_f8_pointers(ops, name, xs[0].device, True)
+
+    out, out_t = written(out, "out"), written(out_t, "out_t")  # before what is read
     dev, rows, cols, ptrs = _matrices(xs, "xs")
     code = _dtype_code(xs[0].dtype)
 
@@ -722,10 +736,7 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
         if given is None:
             ops = _lists().room_f8(r, k, F8_BLOCK, dev.index, F8Operand)
             return ops, *_f8_pointers(ops, name, dev)[2:]
-        ops = list(given)
-        if len(ops) != len(xs):
-            raise ValueError(f"{name} must have one operand per matrix")
-        got_r, got_k, q, s = _f8_pointers(ops, name, dev)
+        ops, got_r, got_k, q, s = given
         if got_r != r or got_k != _i64_bytes(-(-x // F8_BLOCK) * F8_BLOCK for x in array("q", k)):
             raise ValueError(f"{name}: an operand's values must be (rows, contracted side up to a "
                              f"multiple of {F8_BLOCK})")
@@ -762,6 +773,15 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
     dev = a[0][0].device
     if dev.type != "cuda":
         raise ValueError(f"a: operands must live on a HIP device, got {dev}")
+    if out is not None:
+        out = list(out)
+        if len(out) != len(a):
+            raise ValueError("out must have one tensor per product")
+        if out_dtype is not None and any(o.dtype != out_dtype for o in out):
+            raise ValueError("out has another dtype than out_dtype")
+        odev, rows, cols, ptrs = _matrices(out, "out", True)  # before what is read
+        if odev != dev:
+            raise ValueError("out must live on the operands' device")
     m, ka, aq, asc = _f8_pointers(a, "a", dev)
     n, kb, bq, bsc = _f8_pointers(b, "b", dev)
     if ka != kb:
@@ -771,15 +791,7 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
     if out is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
         out = _lists().room(m, n, _dtype_code(dt), dev.index)
-    else:
-        out = list(out)
-        if len(out) != len(a):
-            raise ValueError("out must have one tensor per product")
-        if out_dtype is not None and any(o.dtype != out_dtype for o in out):
-            raise ValueError("out has another dtype than out_dtype")
-    odev, rows, cols, ptrs = _matrices(out, "out")
-    if odev != dev:
-        raise ValueError("out must live on the operands' device")
+        _, rows, cols, ptrs = _matrices(out, "out")
     if rows != m or cols != n:
         raise ValueError("out must have the shape (rows of a, rows of b)")
     code = _dtype_code(out[0].dtype)
@@ -789,10 +801,10 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
     return out
 
 
-def _matrices(ts, name):
+def _matrices(ts, name, written=False):
     """(device, rows, columns, pointers) of contiguous 2-D tensors of one dtype, the
     last three as the bytes of C arrays."""
-    index, flags, _, _, ptrs, rows, cols = _lists().scan(ts)
+    index, flags, _, _, ptrs, rows, cols = _lists().scan(ts, written)
     if index < 0 or flags & (_FLAT | _MATRICES) != _FLAT | _MATRICES:
         _check_tensors(ts, name)  # says what is wrong
     return ts[0].device, rows, cols, ptrs

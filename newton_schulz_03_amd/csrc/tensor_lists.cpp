@@ -56,10 +56,23 @@ PyObject* as_bytes(const std::vector<T>& v) {
                                    static_cast<Py_ssize_t>(v.size() * sizeof(T)));
 }
 
-// scan(tensors) -> (device, flags, dtype codes, element counts, pointers, rows, columns)
+// A tensor's address.  For one that the call writes, a tensor that shares its
+// data copy-on-write is given memory of its own first, as Tensor.data_ptr() does;
+// one that is only read keeps sharing.
+int64_t address(const at::Tensor& t, bool written) {
+  const void* p = written ? t.mutable_data_ptr() : t.const_data_ptr();
+  return static_cast<int64_t>(reinterpret_cast<intptr_t>(p));
+}
+
+// scan(tensors, written) -> (device, flags, dtype codes, element counts, pointers, rows, columns)
 // device: of the first tensor, -1 if that is no HIP device; the arrays as bytes
 // (int32, then int64); rows and columns of two-dimensional tensors, else 0.
-PyObject* scan(PyObject*, PyObject* arg) {
+// The written lists of a call go first: to give one tensor its own memory moves
+// every tensor of the same storage, whose address, taken before, is then another's.
+PyObject* scan(PyObject*, PyObject* args) {
+  PyObject* arg;
+  int written;
+  if (!PyArg_ParseTuple(args, "Op", &arg, &written)) return nullptr;
   Py_ssize_t n;
   PyObject* list = items(arg, &n);
   if (list == nullptr) return nullptr;
@@ -87,7 +100,7 @@ PyObject* scan(PyObject*, PyObject* arg) {
       }
       codes[i] = dtype_code(*t);
       numels[i] = t->numel();
-      ptrs[i] = static_cast<int64_t>(reinterpret_cast<intptr_t>(t->const_data_ptr()));
+      ptrs[i] = address(*t, written != 0);
     }
     return Py_BuildValue("ilNNNNN", device, flags, as_bytes(codes), as_bytes(numels),
                          as_bytes(ptrs), as_bytes(rows), as_bytes(cols));
@@ -117,14 +130,15 @@ PyObject* same_shapes(PyObject*, PyObject* args) {
   }
 }
 
-// scan_f8(operands, block) -> (device, bad, kind, rows, padded K, values, scales)
-// of (values, scales) pairs.  bad: the first operand that is none, or -1; kind:
-// what is wrong with it: 1 the dtypes, 2 device, contiguity or dimensions, 3 the
-// shapes.
+// scan_f8(operands, block, written) -> (device, bad, kind, rows, padded K, values,
+// scales) of (values, scales) pairs.  bad: the first operand that is none, or -1;
+// kind: what is wrong with it: 1 the dtypes, 2 device, contiguity or dimensions, 3
+// the shapes.  written: as in scan.
 PyObject* scan_f8(PyObject*, PyObject* args) {
   PyObject* arg;
   long block;
-  if (!PyArg_ParseTuple(args, "Ol", &arg, &block)) return nullptr;
+  int written;
+  if (!PyArg_ParseTuple(args, "Olp", &arg, &block, &written)) return nullptr;
   Py_ssize_t n;
   PyObject* list = items(arg, &n);
   if (list == nullptr) return nullptr;
@@ -159,8 +173,8 @@ PyObject* scan_f8(PyObject*, PyObject* args) {
       if (wrong == 0) {
         rows[i] = q->size(0);
         kps[i] = q->size(1);
-        qs[i] = static_cast<int64_t>(reinterpret_cast<intptr_t>(q->const_data_ptr()));
-        ss[i] = static_cast<int64_t>(reinterpret_cast<intptr_t>(s->const_data_ptr()));
+        qs[i] = address(*q, written != 0);
+        ss[i] = address(*s, written != 0);
       }
     }
     return Py_BuildValue("iniNNNN", device, bad, kind, as_bytes(rows), as_bytes(kps), as_bytes(qs),
@@ -306,9 +320,9 @@ PyMethodDef methods[] = {
     {"room_norm", room_norm, METH_VARARGS, "room_norm(bytes, device)"},
     {"room", room, METH_VARARGS, "room(rows, columns, dtype code, device)"},
     {"room_f8", room_f8, METH_VARARGS, "room_f8(rows, columns, block, device, kind)"},
-    {"scan", scan, METH_O, "scan(tensors): device, flags, dtype codes, sizes, pointers"},
+    {"scan", scan, METH_VARARGS, "scan(tensors, written): device, flags, dtype codes, sizes, pointers"},
     {"same_shapes", same_shapes, METH_VARARGS, "same_shapes(a, b)"},
-    {"scan_f8", scan_f8, METH_VARARGS, "scan_f8(operands, block)"},
+    {"scan_f8", scan_f8, METH_VARARGS, "scan_f8(operands, block, written)"},
     {nullptr, nullptr, 0, nullptr},
 };
 
