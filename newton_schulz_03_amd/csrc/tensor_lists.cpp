@@ -299,17 +299,18 @@ PyObject* room_f8(PyObject*, PyObject* args) {
   }
 }
 
-// room_norm(bytes, device) -> (workspace of so many bytes, two float32)
+// room_norm(bytes, device) -> (workspace of so many bytes, two float32).  Two
+// allocations: a caller keeps the result, step after step, and must not keep the
+// workspace (17 KB and more) with it.
 PyObject* room_norm(PyObject*, PyObject* args) {
   long long bytes;
   int device;
   if (!PyArg_ParseTuple(args, "Li", &bytes, &device)) return nullptr;
   try {
-    Room all;
-    const int64_t ws = all.add(1, bytes, 1), result = all.add(1, 2, 4);
-    all.allocate(device);
-    return Py_BuildValue("NN", all.piece(ws, {static_cast<int64_t>(bytes)}, at::kByte),
-                         all.piece(result, {2}, at::kFloat));
+    const at::TensorOptions on = at::TensorOptions().device(
+        at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(device)));
+    return Py_BuildValue("NN", THPVariable_Wrap(at::empty({bytes}, on.dtype(at::kByte))),
+                         THPVariable_Wrap(at::empty({2}, on.dtype(at::kFloat))));
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;
