@@ -299,9 +299,9 @@ int32_t muon_adamw_batched(int32_t batch, const int64_t* numel, void* const* p,
  *
  * These tensors may have different types: dtype[i] (and out_dtype[i]) is
  * MUON_BF16 or MUON_FP32 for tensor i.  Other conventions are those at the top
- * of this header; in addition these calls enqueue kernel launches only, so they
- * can be captured into a HIP graph (with per-kernel timing off) and replayed.
- * A captured call uses its workspace at every replay.
+ * of this header; in addition these calls can be captured into a HIP graph (with
+ * per-kernel timing off) and replayed.  A captured call enqueues kernel launches
+ * only, and uses its workspace at every replay.
  */
 typedef enum { MUON_NORM_L2 = 0, MUON_NORM_MAX = 1 } muon_norm_kind;
 

@@ -178,8 +178,8 @@ __device__ __forceinline__ int32_t block_number() {
 // the same branch.
 constexpr int kLocateScan = 2048;
 __device__ __forceinline__ int locate_matrix(const int32_t* prefix, int batch, int32_t b,
-                                             int* slot) {
-  if (batch > kLocateScan) {
+                                             int* slot, int scan = kLocateScan) {
+  if (batch > scan) {
     int lo = 0, hi = batch;  // prefix[lo] <= b < prefix[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;

@@ -421,8 +421,10 @@ int32_t put_table(const Plan& pl, char* ws, hipStream_t stream) {
 // AdamW: descriptors, then the block prefix array.
 // Tensors whose descriptors and prefixes fit the argument table (3328 + 336 bytes).
 constexpr int32_t kAdamArgs = 83;
-// Blocks from which a launch of its own pays (8.4 M elements, 30 us).
-constexpr int64_t kAdamSplitBlocks = 8192;
+// Blocks from which a launch of its own pays (4.2 M elements, 15 us; bf16, us, one
+// launch and a copied table against launches with their tables as arguments: 2000
+// tensors of 100000 elements 895 and 874, of 30000 272 and 313, 250 of 60000 65 and 71).
+constexpr int64_t kAdamSplitBlocks = 4096;
 
 struct AdamPlan {
   int32_t batch = 0;
@@ -1092,6 +1094,37 @@ extern "C" size_t muon_adamw_workspace_bytes(int32_t batch, const int64_t* numel
 namespace muon {
 namespace {
 
+// Whether `stream` is being captured into a graph (an error, as another stream's
+// capture gives it on the null stream, counts as one).
+bool capturing(hipStream_t stream) {
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(stream, &status) != hipSuccess) {
+    (void)hipGetLastError();
+    return true;
+  }
+  return status != hipStreamCaptureStatusNone;
+}
+
+// AdamW's table in the workspace: one copy from a pinned slot, or, where the stream
+// is being captured (a replay would copy what the slot holds by then), kernels that
+// carry its pieces, 3840 bytes each.  (4000 tensors of 1000 elements, bf16: 45 us a
+// call back to back with the copy, 189 with the kernels; 250: 11 and 16.)
+int32_t upload_adam_table(const AdamPlan& pl, char* ws, hipStream_t s) {
+  if (capturing(s)) {
+    ArgTable unused;
+    const void* mem;
+    return place_table(pl.desc.data(), sizeof(AdamDesc) * pl.desc.size(), pl.prefix.data(),
+                       sizeof(int32_t) * pl.prefix.size(), ws, s, unused, &mem);
+  }
+  return stage_upload(
+      pl.total_bytes,
+      [&](char* h) {
+        std::memcpy(h, pl.desc.data(), sizeof(AdamDesc) * pl.desc.size());
+        std::memcpy(h + pl.prefix_off, pl.prefix.data(), sizeof(int32_t) * pl.prefix.size());
+      },
+      ws, s);
+}
+
 // The AdamW step; g_scale: device factor of the gradients, or null.
 int32_t adamw_batched(int32_t batch, const int64_t* numel, void* const* p, const void* const* g,
                       float* const* m, float* const* v, int32_t dtype,
@@ -1151,28 +1184,34 @@ int32_t adamw_batched(int32_t batch, const int64_t* numel, void* const* p, const
     a.inv_bc2_sqrt = static_cast<float>(1.0 / std::sqrt(bc2));
     a.eps = prm->eps;
     a.g_scale = g_scale;
-    // One launch, or several whose tables are their arguments, if each has enough
-    // to do: the 223 non-expert tensors (175.5 M elements) take 622 us in three
-    // launches and 644 in one after the three that write its table; 250 small
-    // tensors 17 and 10.5.
+    // Launches whose tables are their arguments: one, or several if each has enough
+    // to do.  Otherwise one launch and a table in the workspace.
     const int32_t parts = (pl.batch + kAdamArgs - 1) / kAdamArgs;
-    const bool split = pl.prefix[pl.batch] >= kAdamSplitBlocks * static_cast<int64_t>(parts);
-    const int32_t launches = split ? parts : 1;
+    const bool in_args =
+        parts == 1 || pl.prefix[pl.batch] >= kAdamSplitBlocks * static_cast<int64_t>(parts);
+    if (!in_args && (st = upload_adam_table(pl, ws, s)) != MUON_OK) return st;
     TimedLaunch tl(MUON_K_ADAMW, s);
-    for (int32_t k = 0; k < launches; ++k) {
-      const int32_t i0 = static_cast<int32_t>(static_cast<int64_t>(pl.batch) * k / launches);
-      const int32_t i1 = static_cast<int32_t>(static_cast<int64_t>(pl.batch) * (k + 1) / launches);
+    AdamCtx c{};
+    c.stream = s;
+    ArgTable table;
+    c.args = &table;
+    if (!in_args) {
+      c.table = ws;
+      c.prefix_off = static_cast<int32_t>(pl.prefix_off);
+      c.batch = pl.batch;
+      const hipError_t e = launch_adamw(c, pl.prefix[pl.batch], pl.bf16, a);
+      if (e != hipSuccess) return hip_fail(e, "launch adamw");
+    }
+    for (int32_t k = 0; in_args && k < parts; ++k) {
+      const int32_t i0 = static_cast<int32_t>(static_cast<int64_t>(pl.batch) * k / parts);
+      const int32_t i1 = static_cast<int32_t>(static_cast<int64_t>(pl.batch) * (k + 1) / parts);
       std::vector<int32_t> prefix(pl.prefix.begin() + i0, pl.prefix.begin() + i1 + 1);
       for (int32_t& x : prefix) x -= pl.prefix[i0];
-      ArgTable table;
-      AdamCtx c{};
       st = place_table(pl.desc.data() + i0, sizeof(AdamDesc) * (i1 - i0), prefix.data(),
                        sizeof(int32_t) * prefix.size(), ws, s, table, &c.table);
       if (st != MUON_OK) return st;
-      c.args = &table;
       c.prefix_off = static_cast<int32_t>(align_up(sizeof(AdamDesc) * (i1 - i0), kAlign));
       c.batch = i1 - i0;
-      c.stream = s;
       const hipError_t e = launch_adamw(c, prefix.back(), pl.bf16, a);
       if (e != hipSuccess) return hip_fail(e, "launch adamw");
     }
