@@ -56,6 +56,10 @@
  *    matrix-core launches hand out the last tiles of each XCD's share with
  *    integer atomics on counters in the workspace, to whichever XCD is free;
  *    which CU computes a tile never changes its value.
+ *  - A call on a stream that is being captured into a HIP graph (per-kernel timing
+ *    off) sends its descriptor table in kernel launches instead of a copy, so the
+ *    graph can be replayed; it uses its workspace at every replay.  A step with
+ *    momentum_host = 1 is refused there (MUON_ERR_UNSUPPORTED).
  *  - No C++ exception crosses this interface.
  *
  * Precision.  MUON_BF16: tensors are bf16; products accumulate in fp32 on the
@@ -297,11 +301,9 @@ int32_t muon_adamw_batched(int32_t batch, const int64_t* numel, void* const* p,
  * A tensor may appear more than once in a norm; no output may overlap another
  * tensor's gradient or output.
  *
- * These tensors may have different types: dtype[i] (and out_dtype[i]) is
- * MUON_BF16 or MUON_FP32 for tensor i.  Other conventions are those at the top
- * of this header; in addition these calls can be captured into a HIP graph (with
- * per-kernel timing off) and replayed.  A captured call enqueues kernel launches
- * only, and uses its workspace at every replay.
+ * The tensors of a norm, scale or clip may have different types: dtype[i] (and
+ * out_dtype[i]) is MUON_BF16 or MUON_FP32 for tensor i.  Other conventions are
+ * those at the top of this header.
  */
 typedef enum { MUON_NORM_L2 = 0, MUON_NORM_MAX = 1 } muon_norm_kind;
 
@@ -403,7 +405,7 @@ int32_t muon_adamw_batched_scaled(int32_t batch, const int64_t* numel, void* con
  * Every size lies in [0, MUON_F8_MAX_DIM], and a call's outputs hold fewer than
  * about 1.7e10 elements (MUON_ERR_UNSUPPORTED otherwise); pointers of empty
  * operands are not read.  workspace: at least muon_f8_workspace_bytes(batch) bytes, 256-byte
- * aligned.  Like the calls above, both can be captured into a HIP graph.
+ * aligned.
  */
 #define MUON_F8_BLOCK 128
 #define MUON_F8_MAX_DIM 1048576

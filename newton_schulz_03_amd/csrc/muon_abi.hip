@@ -386,7 +386,38 @@ int32_t stage_upload(size_t bytes, Fill fill, void* dst, hipStream_t stream, siz
   return MUON_OK;
 }
 
-int32_t upload_table(const Plan& pl, void* ws, hipStream_t stream) {
+// Whether `stream` is being captured into a graph (an error, as another stream's
+// capture gives it on the null stream, counts as one).
+bool capturing(hipStream_t stream) {
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(stream, &status) != hipSuccess) {
+    (void)hipGetLastError();
+    return true;
+  }
+  return status != hipStreamCaptureStatusNone;
+}
+
+// The descriptor table as kernel arguments (no staging buffer, nothing but
+// kernel launches on the stream): the allocation-free entry point, captured
+// calls, and the chunks of a step with the momentum in host memory, whose small
+// copies would otherwise queue with the chunks' momentum copies.
+int32_t put_table(const Plan& pl, char* ws, hipStream_t stream) {
+  const size_t desc_bytes = sizeof(MatDesc) * pl.batch;
+  hipError_t e = launch_put_bytes(pl.desc.data(), desc_bytes, ws, stream);
+  if (e == hipSuccess)
+    e = launch_put_bytes(pl.prefix.data(), sizeof(int32_t) * pl.prefix.size(),
+                         ws + align_up(desc_bytes, kAlign), stream);
+  if (e == hipSuccess && !pl.order.empty())
+    e = launch_put_bytes(pl.order.data(), sizeof(int32_t) * pl.order.size(), ws + pl.order_off,
+                         stream);
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "launch descriptor copy");
+}
+
+// The descriptor table from a pinned slot.  Not on a stream that is being captured:
+// a replay would copy what the slot holds by then, and the slot's event would belong
+// to the graph.
+int32_t upload_table(const Plan& pl, char* ws, hipStream_t stream) {
+  if (capturing(stream)) return put_table(pl, ws, stream);
   // the descriptors and prefixes at the workspace's start; the used part of the
   // order table, at its end, from the same staging slot
   const size_t order_bytes = sizeof(int32_t) * pl.order.size();
@@ -399,23 +430,7 @@ int32_t upload_table(const Plan& pl, void* ws, hipStream_t stream) {
         if (order_bytes > 0)
           std::memcpy(h + align_up(pl.table_bytes, kAlign), pl.order.data(), order_bytes);
       },
-      ws, stream, order_bytes, static_cast<char*>(ws) + pl.order_off);
-}
-
-// The descriptor table as kernel arguments (no staging buffer, nothing but
-// kernel launches on the stream): the allocation-free entry point, and the
-// chunks of a step with the momentum in host memory, whose small copies would
-// otherwise queue with the chunks' momentum copies.
-int32_t put_table(const Plan& pl, char* ws, hipStream_t stream) {
-  const size_t desc_bytes = sizeof(MatDesc) * pl.batch;
-  hipError_t e = launch_put_bytes(pl.desc.data(), desc_bytes, ws, stream);
-  if (e == hipSuccess)
-    e = launch_put_bytes(pl.prefix.data(), sizeof(int32_t) * pl.prefix.size(),
-                         ws + align_up(desc_bytes, kAlign), stream);
-  if (e == hipSuccess && !pl.order.empty())
-    e = launch_put_bytes(pl.order.data(), sizeof(int32_t) * pl.order.size(), ws + pl.order_off,
-                         stream);
-  return e == hipSuccess ? MUON_OK : hip_fail(e, "launch descriptor copy");
+      ws, stream, order_bytes, ws + pl.order_off);
 }
 
 // AdamW: descriptors, then the block prefix array.
@@ -1037,6 +1052,8 @@ int32_t step_batched(int32_t batch, const int64_t* rows, const int64_t* cols, vo
                       "matrix %d: momentum_host is set but m is not pinned host memory", i);
         }
       }
+      if (capturing(s))
+        return fail(MUON_ERR_UNSUPPORTED, "a step with momentum_host = 1 cannot be captured");
       return run_chunked(cp, ws, s, ep, p->ns, w, g, m);
     }
     if ((st = check_ws(pl, workspace, workspace_bytes)) != MUON_OK) return st;
@@ -1093,17 +1110,6 @@ extern "C" size_t muon_adamw_workspace_bytes(int32_t batch, const int64_t* numel
 
 namespace muon {
 namespace {
-
-// Whether `stream` is being captured into a graph (an error, as another stream's
-// capture gives it on the null stream, counts as one).
-bool capturing(hipStream_t stream) {
-  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
-  if (hipStreamIsCapturing(stream, &status) != hipSuccess) {
-    (void)hipGetLastError();
-    return true;
-  }
-  return status != hipStreamCaptureStatusNone;
-}
 
 // AdamW's table in the workspace: one copy from a pinned slot, or, where the stream
 // is being captured (a replay would copy what the slot holds by then), kernels that
