@@ -757,9 +757,12 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
     a, b: sequences of F8Operand (or (values, scales) pairs) with equal
     contracted sides.  out: contiguous bf16 or fp32 tensors of (A's rows, B's
     rows); without it new ones of out_dtype (bfloat16), in one allocation.
-    accumulate: the products are added to `out`.  Sums are fp32, rounded once.  For
-    Y = X W^T: dX = dY W takes the operands of dY and W^T, and dW = dY^T X those
-    of dY^T and X^T (f8_quantize_batched's transpose).  Returns the outputs.
+    accumulate: the products are added to `out`.  Sums are fp32, rounded once;
+    for bfloat16 outputs 8 consecutive products at a time first lose what is
+    below 2^-13 of the largest of them.  For float32 outputs operand values of
+    2^128 and more are infinite.  For Y = X W^T: dX = dY W takes the operands of
+    dY and W^T, and dW = dY^T X those of dY^T and X^T (f8_quantize_batched's
+    transpose).  Returns the outputs.
     """
     import torch
 

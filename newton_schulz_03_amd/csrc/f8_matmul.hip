@@ -6,16 +6,18 @@
 // The scales are powers of two, so applying them rounds nothing; C is rounded
 // once, at the store.  Two ways to the sum:
 //  * bf16 C: the scaled matrix instruction (v_mfma_scale_f32_32x32x64_f8f6f4)
-//    on the stored bytes.  It adds 8 consecutive products of a lane in a window
-//    of about 14 binades below the largest before they reach the fp32
-//    accumulator (measured: a product 2^-13 of its group's largest counts, one
-//    of 2^-14 does not).  On Gaussian operands that is 1.5e-5 of the result at
-//    any K, far below the 1.7e-3 of the bf16 rounding.
+//    on the stored bytes.  It adds 8 consecutive products on a common grid
+//    before they reach the fp32 accumulator (measured, for products 8 i .. 8 i + 7:
+//    one of 2^-13 of the 8's largest counts, one of 2^-14 does not; between groups
+//    the sum is fp32's).  That is below 2^-10 of the sum of the magnitudes, and on
+//    Gaussian operands 1.5e-5 of the result at any K, far below the 1.7e-3 of the
+//    bf16 rounding.
 //  * fp32 C: that error would be 250 times the output's own rounding, so the
 //    operands are converted on the way from LDS to bf16, scale included
 //    (v_cvt_scalef32_pk_bf16_fp8: exact, but for values below bf16's smallest,
-//    2^-133), and v_mfma_f32_32x32x16_bf16 sums them with fp32 precision, at
-//    half the matrix rate.
+//    2^-133, and from 2^128 on, which become infinite), and
+//    v_mfma_f32_32x32x16_bf16 sums them with fp32 precision, at half the matrix
+//    rate.
 //
 // 256 x 256 tiles, four waves of 128 x 128, K in blocks of 128 through two LDS
 // buffers filled by direct-to-LDS loads, each block in two slices of 64.  The

@@ -166,3 +166,70 @@ def test_nan_stays_in_its_row_and_column(m, n, out):
     want = (x.double() @ y.double().t().contiguous()).to(out)
     want[m - 1], want[:, 7] = float("nan"), float("nan")
     assert np.array_equal(c.float().cpu().numpy(), want.float().cpu().numpy(), equal_nan=True)
+
+
+def column_scales(n):
+    """Exponents that differ by row of B, and the scale bytes of its one block."""
+    e = torch.tensor([-100, -60, -20, 0, 20, 60, 100], device="cuda")[torch.arange(n, device="cuda") % 7]
+    s = torch.zeros((1, up(n, 16)), dtype=torch.uint8, device="cuda")
+    s[0, :n] = (e + 127).to(torch.uint8)
+    return e, s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", [(255, 70), (2048, 2304)])  # few rows; tiles
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_every_scale_byte(m, n, out):
+    """Each scale byte 0 .. 254 in some row of A, against scales of 2^-100 to 2^100 in B:
+    exact wherever 2^-126 <= 2^(e + f), 512 * 2^(e + f) < 2^127 (the sum of 128 products
+    of at most 4) and, for fp32 results, the operand's values are below 2^128."""
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    v = torch.randint(-2, 3, (m, BLOCK), generator=gen, device="cuda").float()
+    w = torch.randint(-2, 3, (n, BLOCK), generator=gen, device="cuda").float()
+    byte = torch.arange(m, device="cuda") % 255
+    s = torch.zeros((1, up(m, 16)), dtype=torch.uint8, device="cuda")
+    s[0, :m] = byte.to(torch.uint8)
+    f, t = column_scales(n)
+    (c,) = nsa.f8_matmul_batched([(v.to(torch.float8_e4m3fn), s)], [(w.to(torch.float8_e4m3fn), t)],
+                                 out_dtype=out)
+    e = (byte - 127)[:, None] + f[None, :]
+    held = (e >= -126) & (e + 9 < 127)
+    if out == FP32:
+        held &= (byte < 254)[:, None]
+    want = (v.double() @ w.double().t().contiguous()) * torch.exp2(e.double())
+    assert int(held.sum()) > m * n // 2
+    assert bool((c.double() == want)[held].all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", [(40, 70), (2048, 2304)])  # few rows; tiles
+def test_magnitudes_next_to_the_largest_fp32_value(m, n):
+    """248 * 2^120 = 3.3e38 and above round up to the operand value 2^128.  The scaled
+    instruction of bf16 results takes it; fp32 results take operands as fp32 holds them,
+    so there it is infinite.  No other row notices."""
+    x = torch.ones((m, BLOCK), device="cuda")
+    x[3] = 0
+    x[3, 5] = 3.4e38
+    x[7, 9] = -248.0 * 2.0 ** 120
+    x[7, :9] = 0
+    x[7, 10:] = 0
+    x[8] = 0
+    x[8, 1] = 247.0 * 2.0 ** 120  # rounds down, to 240 * 2^120
+    (a,) = nsa.f8_quantize_batched([x])
+    assert a.scales[0, [3, 7, 8]].tolist() == [247] * 3
+    assert a.q.float()[[3, 7, 8], [5, 9, 1]].tolist() == [256.0, -256.0, 240.0]
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    w = torch.randint(1, 3, (n, BLOCK), generator=gen, device="cuda").float()
+    t = torch.zeros((1, up(n, 16)), dtype=torch.uint8, device="cuda")
+    t[0, :n] = 127 - 20
+    b = (w.to(torch.float8_e4m3fn), t)
+    stands = x.double()
+    stands[3, 5], stands[7, 9], stands[8, 1] = 2.0 ** 128, -2.0 ** 128, 240 * 2.0 ** 120
+    want = (stands @ w.double().t().contiguous()) * 2.0 ** -20
+    (c,) = nsa.f8_matmul_batched([a], [b], out_dtype=BF16)
+    assert bool((c.double() == want.float().to(BF16).double()).all())
+    (c,) = nsa.f8_matmul_batched([a], [b], out_dtype=FP32)
+    assert not bool(torch.isfinite(c[[3, 7]]).any())
+    rest = torch.ones(m, dtype=torch.bool, device="cuda")
+    rest[3] = rest[7] = False
+    assert bool((c.double() == want)[rest].all())
