@@ -406,9 +406,11 @@ int32_t muon_adamw_batched_scaled(int32_t batch, const int64_t* numel, void* con
  * leaves c).  Of Y = X W^T, the backward products take the same call: dX = dY W
  * with operands dY and W^T, and dW = dY^T X with operands dY^T and X^T.
  *
- * Every size lies in [0, MUON_F8_MAX_DIM], and a call's outputs hold fewer than
- * about 1.7e10 elements (MUON_ERR_UNSUPPORTED otherwise); pointers of empty
- * operands are not read.  workspace: at least muon_f8_workspace_bytes(batch) bytes, 256-byte
+ * Every size lies in [0, MUON_F8_MAX_DIM] (MUON_ERR_UNSUPPORTED otherwise).  A
+ * launch holds fewer than 2^24 blocks: a quantization whose matrices have that many
+ * tiles of 128 x 128 is refused likewise, and so may be a product whose outputs have
+ * that many of 16 x 64 (partial ones counted whole).  Pointers of empty operands are
+ * not read.  workspace: at least muon_f8_workspace_bytes(batch) bytes, 256-byte
  * aligned.
  */
 #define MUON_F8_BLOCK 128

@@ -181,8 +181,7 @@ int32_t check_ptr(const void* p, const char* what, int32_t i) {
   return MUON_OK;
 }
 
-// A launch holds fewer than 2^32 threads; outputs of 1.7e10 elements or more
-// reach that.
+// A launch holds fewer than 2^32 threads.
 constexpr int64_t kMaxBlocks = (1ll << 24) - 1;
 int32_t add_blocks(int64_t a, int64_t b, int64_t& total) {
   total += a * b;  // at most 2^32 blocks of one matrix
