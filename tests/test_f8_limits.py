@@ -41,7 +41,7 @@ def test_products_that_fit(shapes):
 
 
 def test_products_that_do_not():
-    for shapes in ([(1, TOP)] * 1024, [(TOP, TOP)], [(17, TOP), (1, TOP)] * 512):
+    for shapes in ([(1, TOP)] * 4097, [(TOP, TOP)], [(17, TOP), (1, TOP)] * 2048):
         assert product(shapes) == UNSUPPORTED, shapes[0]
         assert "2^24" in nsa.last_error_detail()
 
