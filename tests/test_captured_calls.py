@@ -112,3 +112,109 @@ def test_the_plain_step_and_the_orthogonalization():
 
     replays(lambda: run(ws, out, ms, rooms), lambda: run(ws2, want, ms2, [None, None]),
             lambda: zip(out + ws + ms, want + ws2 + ms2), change)
+
+
+def room(nbytes):
+    ws = torch.empty(nbytes + 256, dtype=torch.uint8, device="cuda")
+    return ws[(-ws.data_ptr()) % 256:]
+
+
+def gradients(count):
+    gen = torch.Generator().manual_seed(count)
+    return [(torch.randn(100 + 131 * (i % 50), generator=gen) * 1e-3).to(FP32 if i % 3 else BF16).cuda()
+            for i in range(count)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [True, False])  # a workspace of the caller's, or the graph's own
+@pytest.mark.parametrize("count", [159, 160, 300])
+def test_clip_into_other_buffers(count, given):
+    # from 160 tensors on the table is written by kernels inside the graph
+    gs = gradients(count)
+    out, want = ([torch.zeros(g.shape, dtype=BF16, device="cuda") for g in gs] for _ in range(2))
+    res, wres = torch.zeros(2, device="cuda"), torch.zeros(2, device="cuda")
+    ws = room(nsa.grad_workspace_bytes([g.numel() for g in gs])) if given else None
+
+    def change(k):
+        for g in gs:
+            g.mul_(0.7)
+
+    replays(lambda: nsa.grad_clip_batched(gs, 1e-2, out=out, result=res, workspace=ws),
+            lambda: nsa.grad_clip_batched(gs, 1e-2, out=want, result=wres),
+            lambda: zip(out + [res], want + [wres]), change)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("count", [239, 240, 500])
+def test_norm_and_clip_in_place(count):
+    # from 240 tensors on the table is written by kernels inside the graph
+    gs = gradients(count)
+    twins = [g.clone() for g in gs]
+    res, wres = torch.zeros(4, device="cuda"), torch.zeros(4, device="cuda")
+    ws = [room(nsa.grad_workspace_bytes([g.numel() for g in gs])) for _ in range(2)]
+
+    def run(ts, r, ws):
+        nsa.grad_norm_batched(ts, max_norm=1.0, result=r[:2], workspace=ws[0])
+        nsa.grad_clip_batched(ts, 1e-2, result=r[2:], workspace=ws[1])
+
+    def change(k):
+        for a, b in zip(gs, twins):
+            a.mul_(1.7)
+            b.mul_(1.7)
+
+    replays(lambda: run(gs, res, ws), lambda: run(twins, wres, [None, None]),
+            lambda: zip(gs + [res], twins + [wres]), change)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("count", [50, 51, 69, 70, 130])
+def test_quantization_and_product(count, given):
+    # from 70 matrices and 51 products on the tables are written by kernels inside the graph
+    gen = torch.Generator().manual_seed(count)
+    xs = [torch.randn((1 + 7 * (i % 11), 300), generator=gen).to(BF16).cuda() for i in range(count)]
+    wq = nsa.f8_quantize_batched([torch.randn((136, 300), generator=gen).to(BF16).cuda()
+                                  for _ in range(count)], block_rows=128)
+    xq, xt, cs = ([[f(*x.shape) for x in xs] for _ in range(2)]
+                  for f in (lambda r, c: nsa.f8_empty(r, c, "cuda"), lambda r, c: nsa.f8_empty(c, r, "cuda"),
+                            lambda r, c: torch.zeros((r, 136), dtype=FP32, device="cuda")))
+    ws = [room(nsa.f8_workspace_bytes(count)) if given else None for _ in range(2)]
+
+    def run(k, ws):
+        nsa.f8_quantize_batched(xs, transpose=True, out=xq[k], out_t=xt[k], workspace=ws[0])
+        nsa.f8_matmul_batched(xq[k], wq, out=cs[k], accumulate=True, workspace=ws[1])
+
+    def change(k):
+        for x in xs:
+            x.mul_(-1.5)
+
+    def pairs():
+        for a, b in zip(xq[0] + xt[0], xq[1] + xt[1]):
+            yield a.q.view(torch.uint8), b.q.view(torch.uint8)
+            yield a.scales, b.scales
+        yield from zip(*cs)
+
+    replays(lambda: run(0, ws), lambda: run(1, [None, None]), pairs, change)
+
+
+@pytest.mark.gpu
+def test_two_graphs_of_one_workspace():
+    # one after the other on a stream: each writes its table at every replay
+    a, b = gradients(300), gradients(280)
+    ws = room(nsa.grad_workspace_bytes([g.numel() for g in a]))
+    res = [torch.zeros(2, device="cuda") for _ in range(2)]
+    graphs = []
+    torch.cuda.synchronize()
+    for gs, r in zip((a, b), res):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            nsa.grad_norm_batched(gs, max_norm=1e-3, result=r, workspace=ws)
+        graphs.append(graph)
+    for k in range(3):
+        for g in a + b:
+            g.mul_(1.1)
+        want = [nsa.grad_norm_batched(gs, max_norm=1e-3) for gs in (a, b)]
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(res, want)), k
