@@ -568,8 +568,6 @@ def grad_norm_batched(grads: Sequence, max_norm: Optional[float] = None, norm_ty
     bf16 and fp32 tensors, mixed as they come, on one device.  Runs on the
     current HIP stream; nothing waits for the GPU.
     """
-    import torch
-
     grads = list(grads)
     if not grads:
         raise ValueError("grads: at least one tensor (its device holds the result)")
@@ -604,8 +602,6 @@ def grad_scale_batched(grads: Sequence, scale, out: Optional[Sequence] = None,
     """out[i] = scale * grads[i]; scale: a one-element float32 tensor on their
     device.  In place without `out`; out[i] may have the other dtype.  Returns
     the outputs."""
-    import torch
-
     grads = list(grads)
     if not grads:
         return []
@@ -623,8 +619,6 @@ def grad_clip_batched(grads: Sequence, max_norm: float, norm_type: float = 2.0, 
     `out` (whose tensors may have the other dtype: fp32 sums into bf16
     gradients).  Returns the float32 tensor (norm, factor) of grad_norm_batched.
     Nothing waits for the GPU."""
-    import torch
-
     grads = list(grads)
     if not grads:
         raise ValueError("grads: at least one tensor (its device holds the result)")
@@ -708,8 +702,6 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
     Returns the operands, the transposes' operands, or a pair of both lists, in
     `out` and `out_t` where given; new ones of one list share an allocation.
     """
-    import torch
-
     xs = list(xs)
     if not normal and not transpose:
         raise ValueError("one of normal and transpose must be set")

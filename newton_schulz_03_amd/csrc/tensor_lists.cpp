@@ -16,7 +16,7 @@
 
 namespace {
 
-// What holds for every tensor of a list, as bits.
+// What holds for every tensor of a list, as bits (the binding has the same four).
 enum : long {
   kSameDevice = 1,   // the first one's HIP device
   kContiguous = 2,
@@ -333,14 +333,5 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "tensor_lists", nullptr, -1, method
 }  // namespace
 
 PyMODINIT_FUNC PyInit_tensor_lists() {
-  PyObject* m = PyModule_Create(&module);
-  if (m == nullptr) return nullptr;
-  if (PyModule_AddIntConstant(m, "SAME_DEVICE", kSameDevice) != 0 ||
-      PyModule_AddIntConstant(m, "CONTIGUOUS", kContiguous) != 0 ||
-      PyModule_AddIntConstant(m, "SAME_DTYPE", kSameDtype) != 0 ||
-      PyModule_AddIntConstant(m, "MATRICES", kMatrices) != 0) {
-    Py_DECREF(m);
-    return nullptr;
-  }
-  return m;
+  return PyModule_Create(&module);
 }
