@@ -11,11 +11,11 @@
 // Bandwidth-bound (22 bytes an element in bf16, 28 in fp32): each block reads
 // its whole span (p, g, m, v) before the first store.  Every load and store of a
 // wave covers whole 128-byte lines, 4 elements a lane, with the nontemporal
-// hint: 223 bf16 tensors of 175.5 M elements in 639 us, 6.0 TB/s.  (8 elements a
-// lane, which covers each fp32 line in two halves: 705 us with the hint, 731
-// without; 4 elements without the hint 710; more spans per block are slower,
-// 687 us with two.)  Blocks find their tensor through the prefix table in one
-// round of loads, as the other elementwise kernels do.
+// hint: 223 bf16 tensors of 175.5 M elements in 639 us, 6.0 TB/s (633 to 675 us by
+// where the tensors lie).  (8 elements a lane, which covers each fp32 line in two
+// halves: 705 us with the hint, 731 without; 4 elements without the hint 710; more
+// spans per block are slower, 687 us with two.)  Blocks find their tensor through
+// the prefix table, in one round of loads for up to kAdamScan tensors.
 #include "device_common.hpp"
 
 namespace muon {

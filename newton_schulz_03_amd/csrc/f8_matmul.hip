@@ -173,7 +173,10 @@ __device__ __forceinline__ void set_half(i32x8_t& f, int h, const u32x4_t& v) {
 // chunk c of row r at c ^ r; they come out as whole rows, so that every store
 // covers full 128-byte lines (written from the accumulators, 16 bytes a row,
 // the store ran at 2.5 TB/s).  ADD: the old C of one ni is requested while the
-// one before it is stored.  NT: C passes the caches by (F8ProdCtx::nt).
+// one before it is stored.  NT: C passes the caches by (F8ProdCtx::nt).  Rows of C
+// whose length is no multiple of a lane's 16 bytes go element by element: 16
+// products 1024 x 2047 x 6144, bf16: 196 us against 167 of 2048 columns, added to an
+// old C 262 against 185.
 template <typename T, bool ADD, int NQ, bool NT>
 __device__ __forceinline__ void store_part(const f32x16_t (&acc)[4][NQ], char* lds, T* c, int32_t m0,
                                            int32_t n0, int32_t m, int32_t n, int lane) {

@@ -15,6 +15,9 @@
 // converted two at a time with their scale: with the arithmetic done value by
 // value in fp32 (17 instructions a value for both outputs, now 3) the
 // instructions were the bound, 61 us against 44 for the tokens of 32 experts.
+// Columns that are no multiple of 8 (bf16) or 4 (fp32) are read element by element:
+// 16 matrices of 2048 x 6145, both outputs, bf16 270 us against 151 of 2048 x 6144, fp32
+// 376 against 217.
 #include "device_common.hpp"
 
 namespace muon {

@@ -436,9 +436,11 @@ int32_t upload_table(const Plan& pl, char* ws, hipStream_t stream) {
 // AdamW: descriptors, then the block prefix array.
 // Tensors whose descriptors and prefixes fit the argument table (3328 + 336 bytes).
 constexpr int32_t kAdamArgs = 83;
-// Blocks from which a launch of its own pays (4.2 M elements, 15 us; bf16, us, one
-// launch and a copied table against launches with their tables as arguments: 2000
-// tensors of 100000 elements 895 and 874, of 30000 272 and 313, 250 of 60000 65 and 71).
+// Blocks from which a launch of its own pays, for its blocks look through fewer
+// prefixes (4.2 M elements, 15 us; bf16, us, one launch and a copied table against
+// launches with their tables as arguments: 2000 tensors of 100000 elements 895 and
+// 874, of 30000 272 and 313, 250 of 60000 65 and 71; the 223 non-expert tensors 669 and
+// 675 in one place of memory, 640 and 633 in another).
 constexpr int64_t kAdamSplitBlocks = 4096;
 
 struct AdamPlan {
