@@ -700,7 +700,8 @@ def f8_quantize_batched(xs: Sequence, block_rows: int = 1, normal: bool = True,
     block_rows: 1 for a scale per 1 x 128 block along the contracted side
     (activations, gradients), 128 for one per 128 x 128 block (weights).
     Returns the operands, the transposes' operands, or a pair of both lists, in
-    `out` and `out_t` where given; new ones of one list share an allocation.
+    `out` and `out_t` where given; new ones of one list share an allocation, which
+    lives as long as any of them (torch.save of one writes all: save a clone).
     """
     xs = list(xs)
     if not normal and not transpose:
@@ -748,7 +749,8 @@ def f8_matmul_batched(a: Sequence, b: Sequence, out: Optional[Sequence] = None, 
 
     a, b: sequences of F8Operand (or (values, scales) pairs) with equal
     contracted sides.  out: contiguous bf16 or fp32 tensors of (A's rows, B's
-    rows); without it new ones of out_dtype (bfloat16), in one allocation.
+    rows); without it new ones of out_dtype (bfloat16), which share an allocation
+    as those of f8_quantize_batched do.
     accumulate: the products are added to `out`.  Sums are fp32, rounded once;
     for bfloat16 outputs 8 consecutive products at a time first lose what is
     below 2^-13 of the largest of them.  For float32 outputs operand values of
