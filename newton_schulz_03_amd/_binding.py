@@ -231,6 +231,11 @@ def allocate_workspace(shapes, dtype, device, fp8: bool = False, momentum_host: 
     return ws[off:off + max(n, 1)]
 
 
+def _check_workspace(workspace, dev) -> None:
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on the device of the other tensors")
+
+
 def _stream_handle(device) -> int:
     import torch
 
@@ -282,6 +287,7 @@ def ns_batched(xs: Sequence, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7,
     code = _dtype_code(xs[0].dtype)
     if workspace is None:
         workspace = allocate_workspace(shapes, xs[0].dtype, dev, fp8=fp8_steps > 0)
+    _check_workspace(workspace, dev)
     a, b, c = (float(v) for v in coeffs)
     p = NsParams(int(steps), a, b, c, float(eps), int(cu_budget), int(fp8_steps))
     with torch.cuda.device(dev):
@@ -363,6 +369,7 @@ def step_batched(ws: Sequence, gs: Sequence, ms: Sequence, lr: float = 0.02, bet
     if workspace is None:
         workspace = allocate_workspace(shapes, ws[0].dtype, dev, fp8=fp8_steps > 0,
                                        momentum_host=momentum_host)
+    _check_workspace(workspace, dev)
     a, b, c = (float(v) for v in coeffs)
     p = StepParams(float(lr), float(beta), 1 if nesterov else 0,
                    NsParams(int(steps), a, b, c, float(eps), int(cu_budget), int(fp8_steps)),
@@ -437,6 +444,7 @@ def adamw_batched(params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg
     code = _dtype_code(ps[0].dtype)
     if workspace is None:
         workspace = _byte_workspace(_adamw_table_bytes(len(ps)), dev)
+    _check_workspace(workspace, dev)
     b1, b2 = (float(b) for b in betas)
     prm = AdamWParams(float(lr), b1, b2, float(eps), float(weight_decay), int(step))
     fn, scale = lib.muon_adamw_batched, ()
