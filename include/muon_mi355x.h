@@ -429,6 +429,142 @@ int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const int64_t* n
                                int32_t dtype, int32_t accumulate, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/*
+ * Tokens to the experts and back, around the products of an expert layer.  Token t
+ * of `tokens` has top_k slots s = t * top_k + k, each with an expert's id; an id
+ * outside [0, experts) drops the slot (padding, or an expert that is full).
+ *
+ * muon_moe_sort makes the plan that the other calls read, on the device: kept
+ * slots by expert, those of one expert in the order of s.
+ *   ids      tokens x top_k integers of id_bytes (4 or 8) bytes
+ *   offsets  experts + 1: the sorted rows of expert e are offsets[e] .. offsets[e+1] - 1
+ *   active   experts + 1: active[0] experts have rows, active[1 ..] are their ids,
+ *            ascending, then -1
+ *   rows     tokens x top_k: the sorted row of each slot, -1 for a dropped one
+ *   slots    tokens x top_k: the slot of each sorted row, -1 behind the last
+ *
+ * With that plan (slots that are dropped, or whose row is not below y_rows or
+ * out_rows, take no part: their weights and rows are not read, and nothing is
+ * written for them):
+ *   muon_moe_dispatch          out[rows[s]] = x[t]
+ *   muon_moe_combine           out[t] = sum_k w[s] y[rows[s]]
+ *   muon_moe_combine_backward  dy[rows[s]] = w[s] dout[t],
+ *                              dw[s] = sum_c dout[t][c] y[rows[s]][c]  (0 if dropped)
+ * Rows have `cols` elements of `dtype` (MUON_BF16 or MUON_FP32) and lie one after
+ * the other; weights and their gradients are fp32.  Sums are fp32, rounded once:
+ * combine's in the order of k; weights may be null there: 1, which is the
+ * gradient of dispatch.  Rows behind the last sorted one are left as they were.
+ * A token without kept slots gets zeros.
+ *
+ * tokens * top_k <= MUON_MOE_MAX_SLOTS, top_k in [1, MUON_MOE_MAX_TOP_K], experts in
+ * [1, MUON_MOE_MAX_EXPERTS], cols <= MUON_F8_MAX_DIM (MUON_ERR_UNSUPPORTED beyond).
+ * x, y, out, dout and dy are 16-byte aligned, the other arrays at their elements'
+ * size.  No output may overlap another array of the call.
+ */
+#define MUON_MOE_MAX_EXPERTS 1024
+#define MUON_MOE_MAX_TOP_K 64
+#define MUON_MOE_MAX_SLOTS 16777215
+
+/* Bytes of device workspace of muon_moe_sort; SIZE_MAX on invalid arguments. */
+size_t muon_moe_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts);
+
+int32_t muon_moe_sort(int64_t tokens, int32_t top_k, int32_t experts, const void* ids,
+                      int32_t id_bytes, int32_t* offsets, int32_t* active, int32_t* rows,
+                      int32_t* slots, void* workspace, size_t workspace_bytes, void* stream);
+
+int32_t muon_moe_dispatch(int64_t tokens, int32_t top_k, int64_t cols, const void* x,
+                          const int32_t* rows, int64_t out_rows, void* out, int32_t dtype,
+                          void* stream);
+
+int32_t muon_moe_combine(int64_t tokens, int32_t top_k, int64_t cols, int64_t y_rows,
+                         const void* y, const int32_t* rows, const float* weights, void* out,
+                         int32_t dtype, void* stream);
+
+int32_t muon_moe_combine_backward(int64_t tokens, int32_t top_k, int64_t cols, const void* dout,
+                                  int64_t y_rows, const void* y, const int32_t* rows,
+                                  const float* weights, void* dy, float* dweights, int32_t dtype,
+                                  void* stream);
+
+/*
+ * Dropout over a ragged batch of tensors, for the rows between an expert's
+ * products.  With t = p * 2^16 rounded to the nearest integer,
+ *     out_ij = 0 if u_ij < t, else x_ij * 2^16 / (2^16 - t)
+ * in fp32, rounded to out's type; t = 2^16 drops everything.  u_ij is 16 bits of
+ * Philox 4x32 with 7 rounds, of the block with counter (j / 8, i, low and high half
+ * of offset) and key (low and high half of seed): half j % 8 of the block's words
+ * (the low half of a word first).  Nothing of it is stored: the gradient is the
+ * same call on the gradients.  A dropped element is 0 whatever x_ij is.
+ *   numel, dtype, out, out_dtype  as for muon_grad_scale_batched (out[i] may be
+ *                 x[i], of the same type), numel[i] below 2^35
+ *   rng           null, or device memory (8-byte aligned): seed and offset, read on
+ *                 the stream in place of those in `params`, so that a captured call
+ *                 takes new ones at every replay
+ *   workspace     at least muon_grad_workspace_bytes() bytes, 256-byte aligned
+ */
+typedef struct {
+  double p;        /* in [0, 1] */
+  uint64_t seed;
+  uint64_t offset; /* another mask for every call of one seed: a step's or layer's number */
+} muon_dropout_params;
+
+int32_t muon_dropout_batched(int32_t batch, const int64_t* numel, const void* const* x,
+                             const int32_t* dtype, void* const* out, const int32_t* out_dtype,
+                             const muon_dropout_params* params, const uint64_t* rng,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * 4-bit weights with group scales, and their products with few rows: the expert
+ * matrices as they serve single tokens.
+ *
+ * An operand holds `count` matrices of `rows` x `cols`, contracted over cols, in
+ * tiles of 16 rows x 128 columns.  With RT = rows / 16 and KT = cols / 128, rounded up:
+ *   q  count x RT x KT x 64 x 16 bytes: chunk 16 c + r of a tile holds columns
+ *      32 i + 8 c + j (i < 4, j < 8) of its row r, OCP e2m1 codes (0, 0.5, 1, 1.5, 2, 3,
+ *      4, 6; 8 more: negative), column 2 j' in the low half of byte 4 i + j'
+ *   s  count x RT x (KT / 4 rounded up) x 16 x 16 bytes: row r's 16 groups of 32
+ *      columns of four tiles, byte e + 127 for the scale 2^e, 255: NaN
+ * Columns past the matrix are zeros; rows past it, and groups past the last
+ * tile, have code 0 and scale 127.  A value stands for code * 2^e.
+ *
+ * muon_f4_quantize forms the operand of count matrices w[i] (rows x cols of the
+ * operand, row-major, contiguous, `dtype`; with transpose = 1 cols x rows, each
+ * transposed on the way).  2^e is the smallest power of two, from 2^-125 to 2^125,
+ * with the group's largest magnitude at most 6 * 2^e; codes are rounded to nearest
+ * even, and saturate (above 6 * 2^125 only).  A group with an infinity or NaN is NaN.
+ *
+ * muon_f4_matmul: y[p] = x[p] W_e^T for the rows p of expert e, offsets[e] <= p <
+ * offsets[e+1] and p < m; rows of y that no expert has are left as they were.
+ *   x        x_rows x cols, bf16, row-major, contiguous
+ *   offsets, active  of muon_moe_sort with experts = count; both null: matrix 0 (count
+ *            must be 1) takes all m rows
+ *   slots    null: row p is x's row p (x_rows >= m); else of muon_moe_sort (m entries
+ *            at least): row p is x's row slots[p] / top_k, the token's own, which
+ *            saves the dispatch.  Needs offsets and active.
+ *   y        m x rows, `dtype` (MUON_BF16 or MUON_FP32)
+ * Products are exact, sums fp32 in an order that the sizes fix, rounded once.
+ * Scale bytes are to lie in [2, 252] or be 255.
+ * Meant for up to some 64 rows an expert, where the weights' bytes bound it; more
+ * are right but read the weights again every 64 (muon_f8_matmul_batched is for
+ * those).
+ *
+ * count in [1, MUON_MOE_MAX_EXPERTS], rows and cols in [0, MUON_F8_MAX_DIM], m and
+ * x_rows at most MUON_MOE_MAX_SLOTS, fewer than 2^28 tiles (MUON_ERR_UNSUPPORTED
+ * beyond).  q, s, x, y: 16-byte aligned.
+ */
+#define MUON_F4_GROUP 32
+
+/* Bytes of device workspace of muon_f4_quantize; SIZE_MAX on invalid arguments. */
+size_t muon_f4_workspace_bytes(int32_t count);
+
+int32_t muon_f4_quantize(int32_t count, int64_t rows, int64_t cols, const void* const* w,
+                         int32_t dtype, int32_t transpose, void* q, void* s, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+int32_t muon_f4_matmul(int32_t count, int64_t rows, int64_t cols, const void* q, const void* s,
+                       int64_t m, const void* x, int64_t x_rows, const int32_t* offsets,
+                       const int32_t* active, const int32_t* slots, int32_t top_k, void* y,
+                       int32_t dtype, void* stream);
+
 /* Kernels of the step, and the momentum copies of a step with the momentum in
  * host memory, for per-kernel timing. */
 typedef enum {
@@ -451,7 +587,14 @@ typedef enum {
   MUON_K_GRAD_SCALE = 16, /* gradients times a factor */
   MUON_K_F8_QUANTIZE = 17, /* muon_f8_quantize_batched */
   MUON_K_F8_PROD = 18,    /* muon_f8_matmul_batched */
-  MUON_K_COUNT = 19
+  MUON_K_MOE_SORT = 19,   /* muon_moe_sort */
+  MUON_K_MOE_DISPATCH = 20, /* muon_moe_dispatch */
+  MUON_K_MOE_COMBINE = 21, /* muon_moe_combine */
+  MUON_K_MOE_BACKWARD = 22, /* muon_moe_combine_backward */
+  MUON_K_DROPOUT = 23,    /* muon_dropout_batched */
+  MUON_K_F4_QUANTIZE = 24, /* muon_f4_quantize */
+  MUON_K_F4_PROD = 25,    /* muon_f4_matmul */
+  MUON_K_COUNT = 26
 } muon_kernel;
 
 /*

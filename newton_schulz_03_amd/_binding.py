@@ -35,10 +35,14 @@ EXPORTED = ("muon_workspace_bytes", "muon_workspace_bytes_ex", "muon_ns_batched"
             "muon_timing_read", "muon_timing_reset", "muon_hbm_stream",
             "muon_grad_workspace_bytes", "muon_grad_norm_batched", "muon_grad_scale_batched",
             "muon_grad_clip_batched", "muon_step_batched_scaled", "muon_adamw_batched_scaled",
-            "muon_f8_workspace_bytes", "muon_f8_quantize_batched", "muon_f8_matmul_batched")
+            "muon_f8_workspace_bytes", "muon_f8_quantize_batched", "muon_f8_matmul_batched",
+            "muon_moe_workspace_bytes", "muon_moe_sort", "muon_moe_dispatch", "muon_moe_combine",
+            "muon_moe_combine_backward", "muon_dropout_batched", "muon_f4_workspace_bytes",
+            "muon_f4_quantize", "muon_f4_matmul")
 KERNELS = ("prepare", "norm", "gram", "poly", "prod", "finish", "adamw", "prod_finish", "prod_first",
            "quant8", "gram8", "poly8", "prod8", "mom_in", "mom_out",
-           "grad_norm", "grad_scale", "f8_quantize", "f8_prod")
+           "grad_norm", "grad_scale", "f8_quantize", "f8_prod", "moe_sort", "moe_dispatch",
+           "moe_combine", "moe_backward", "dropout", "f4_quantize", "f4_prod")
 
 
 class MuonError(RuntimeError):
@@ -69,6 +73,10 @@ class AdamWParams(ctypes.Structure):
 class GradNormParams(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("clip", ctypes.c_int32), ("max_norm", ctypes.c_float),
                 ("eps", ctypes.c_float)]
+
+
+class DropoutParams(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
 
 
 _lib_handle: Optional[ctypes.CDLL] = None
@@ -147,6 +155,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_f8_quantize_batched.restype = i32
     lib.muon_f8_matmul_batched.argtypes = [i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, sz, vp]
     lib.muon_f8_matmul_batched.restype = i32
+    i64 = ctypes.c_int64
+    lib.muon_moe_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.muon_moe_workspace_bytes.restype = sz
+    lib.muon_moe_sort.argtypes = [i64, i32, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.muon_moe_sort.restype = i32
+    lib.muon_moe_dispatch.argtypes = [i64, i32, i64, vp, vp, i64, vp, i32, vp]
+    lib.muon_moe_dispatch.restype = i32
+    lib.muon_moe_combine.argtypes = [i64, i32, i64, i64, vp, vp, vp, vp, i32, vp]
+    lib.muon_moe_combine.restype = i32
+    lib.muon_moe_combine_backward.argtypes = [i64, i32, i64, vp, i64, vp, vp, vp, vp, vp, i32, vp]
+    lib.muon_moe_combine_backward.restype = i32
+    lib.muon_dropout_batched.argtypes = [i32, vp, vp, vp, vp, vp, ctypes.POINTER(DropoutParams), vp,
+                                         vp, sz, vp]
+    lib.muon_dropout_batched.restype = i32
+    lib.muon_f4_workspace_bytes.argtypes = [i32]
+    lib.muon_f4_workspace_bytes.restype = sz
+    lib.muon_f4_quantize.argtypes = [i32, i64, i64, vp, i32, i32, vp, vp, vp, sz, vp]
+    lib.muon_f4_quantize.restype = i32
+    lib.muon_f4_matmul.argtypes = [i32, i64, i64, vp, vp, i64, vp, i64, vp, vp, vp, i32, vp, i32, vp]
+    lib.muon_f4_matmul.restype = i32
     _lib_handle = lib
     return lib
 
@@ -467,9 +495,15 @@ def _adamw_table_bytes(batch: int) -> int:
 def _call(fn, dev, workspace, *args) -> None:
     """Runs an entry point whose last arguments are the workspace, its size and
     the stream, on `dev` and its current stream."""
+    _run(fn, dev, *args, workspace.data_ptr(), workspace.numel())
+
+
+def _run(fn, dev, *args) -> None:
+    """Runs an entry point whose last argument is the stream, on `dev` and its
+    current stream."""
     import torch
 
-    args += (workspace.data_ptr(), workspace.numel(), _stream_handle(dev))
+    args += (_stream_handle(dev),)
     if torch.cuda.current_device() == dev.index:
         st = fn(*args)
     else:
@@ -587,21 +621,21 @@ def grad_norm_batched(grads: Sequence, max_norm: Optional[float] = None, norm_ty
     return result
 
 
-def _grads_and_outputs(grads, out):
+def _grads_and_outputs(grads, out, name="grads"):
     """(device, dtype codes, element counts, pointers) of the gradients, then the
     outputs, their dtype codes and pointers."""
     if out is None:
-        dev, codes, numels, ptrs = _flat_tensors(grads, "grads", True)
+        dev, codes, numels, ptrs = _flat_tensors(grads, name, True)
         return dev, codes, numels, ptrs, grads, codes, ptrs
     out = list(out)
     if len(out) != len(grads):
-        raise ValueError("out must have one tensor per gradient")
+        raise ValueError(f"out must have one tensor for each of {name}")
     odev, ocodes, onumels, optrs = _flat_tensors(out, "out", True)
-    dev, codes, numels, ptrs = _flat_tensors(grads, "grads", False)
+    dev, codes, numels, ptrs = _flat_tensors(grads, name, False)
     if odev != dev:
-        raise ValueError("out must live on the gradients' device")
+        raise ValueError(f"out must live on the device of {name}")
     if onumels != numels:
-        raise ValueError("out must have the gradients' sizes")
+        raise ValueError(f"out must have the sizes of {name}")
     return dev, codes, numels, ptrs, out, ocodes, optrs
 
 
@@ -813,6 +847,368 @@ def _matrices(ts, name, written=False):
     if index < 0 or flags & (_FLAT | _MATRICES) != _FLAT | _MATRICES:
         _check_tensors(ts, name)  # says what is wrong
     return ts[0].device, rows, cols, ptrs
+
+
+# ---------------------------------------------------------------------------
+# Dropout
+# ---------------------------------------------------------------------------
+
+def dropout_batched(xs: Sequence, p: float, seed: int = 0, offset: int = 0, rng=None,
+                    out: Optional[Sequence] = None, workspace=None) -> List:
+    """Dropout over a ragged batch of tensors: out[i] = xs[i] / (1 - p), but 0 where
+    the element's random number is below p (p to the nearest multiple of 2^-16).
+
+    The mask is a function of seed, offset (64 bits each), the tensor's place in
+    the list and the element's place in the tensor, and is never stored: the
+    gradient is the same call on the gradients.  Calls of one seed take different
+    offsets (a step's or layer's number).  rng: an int64 tensor (seed, offset) on
+    the tensors' device, read on the stream in place of both, for calls that are
+    captured into a graph.  xs: contiguous bf16 and fp32 tensors.  In place
+    without `out`; out[i] may have the other dtype.  Returns the outputs.
+    """
+    import torch
+
+    xs = list(xs)
+    if not xs:
+        return []
+    if rng is not None and (seed != 0 or offset != 0):
+        raise ValueError("rng takes the place of seed and offset")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset are unsigned 64-bit numbers")
+    dev, codes, numels, ptrs, out, ocodes, optrs = _grads_and_outputs(xs, out, "xs")
+    state = None
+    if rng is not None:
+        if not isinstance(rng, torch.Tensor) or rng.device != dev or rng.dtype != torch.int64 or \
+                tuple(rng.shape) != (2,) or not rng.is_contiguous():
+            raise ValueError("rng: a contiguous int64 tensor of 2 elements on the device of the other "
+                             "tensors")
+        state = rng.data_ptr()
+    prm = DropoutParams(float(p), seed, offset)
+    workspace = _workspace(workspace, _grad_table_bytes(len(xs)), dev)
+    _call(load_library().muon_dropout_batched, dev, workspace, len(xs), numels, ptrs, codes, optrs,
+          ocodes, ctypes.byref(prm), state)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Tokens to the experts and back
+# ---------------------------------------------------------------------------
+
+MOE_MAX_EXPERTS, MOE_MAX_TOP_K, MOE_MAX_SLOTS = 1024, 64, (1 << 24) - 1
+
+
+def _pointer(t, name, dev, dtypes, shape, written=False):
+    """A tensor's address, checked: contiguous, of one of `dtypes` and of `shape`
+    (None: any) on `dev`.  Those that a call writes are asked for before those it
+    only reads."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor on {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}: use " + " or ".join(map(str, dtypes)))
+    if len(t.shape) != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: want "
+                         + str(tuple("any" if b is None else b for b in shape)))
+    return _lists().address(t, written)
+
+
+def _device_of(t, name):
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name}: a tensor on a HIP device")
+    return t.device
+
+
+class MoePlan(NamedTuple):
+    """Slots (tokens x top_k) sorted by expert, as int32 tensors on the device.
+
+    offsets: experts + 1; the sorted rows of expert e are offsets[e] to offsets[e + 1].
+    active: experts + 1; active[0] experts have rows, active[1:] are their ids, then -1.
+    rows: tokens x top_k; the sorted row of each slot, -1 for a dropped one.
+    slots: tokens * top_k; the slot of each sorted row, -1 behind the last."""
+
+    offsets: object
+    active: object
+    rows: object
+    slots: object
+
+    def sizes(self) -> List[int]:
+        """Rows of each expert, for torch.split of sorted rows into the lists that
+        the batched products take.  Waits for the GPU."""
+        at = self.offsets.tolist()
+        return [b - a for a, b in zip(at, at[1:])]
+
+
+def moe_empty_plan(tokens: int, top_k: int, num_experts: int, device) -> MoePlan:
+    """Room for the plan of tokens x top_k slots."""
+    import torch
+
+    e, n = num_experts + 1, tokens * top_k
+    o, a, r, s = torch.empty(2 * e + 2 * n, dtype=torch.int32, device=device).split([e, e, n, n])
+    return MoePlan(o, a, r.view(tokens, top_k), s)
+
+
+def _plan_pointers(plan, dev, experts=None, written=False):
+    """(tokens, top_k, experts, addresses of offsets, active, rows and slots)."""
+    import torch
+
+    i32 = (torch.int32,)
+    offsets, active, rows, slots = plan
+    prows = _pointer(rows, "plan.rows", dev, i32, (None, None), written)
+    t, k = rows.shape
+    pslots = _pointer(slots, "plan.slots", dev, i32, (t * k,), written)
+    poffsets = _pointer(offsets, "plan.offsets", dev, i32, (None if experts is None else experts + 1,),
+                        written)
+    e = offsets.shape[0] - 1
+    return t, k, e, poffsets, _pointer(active, "plan.active", dev, i32, (e + 1,), written), prows, pslots
+
+
+def moe_workspace_bytes(tokens: int, top_k: int, num_experts: int) -> int:
+    """Device workspace bytes of moe_sort."""
+    n = load_library().muon_moe_workspace_bytes(int(tokens), int(top_k), int(num_experts))
+    if n == SIZE_MAX:
+        raise MuonError(MUON_ERR_INVALID_ARG, "muon_moe_workspace_bytes", last_error_detail())
+    return int(n)
+
+
+def moe_sort(experts, num_experts: int, plan: Optional[MoePlan] = None, workspace=None) -> MoePlan:
+    """Sorts the slots of tokens by expert, on the device.
+
+    experts: tokens x top_k ids, contiguous int32 or int64 (as torch.topk gives
+    them); a slot whose id lies outside [0, num_experts) is dropped.  Slots of one
+    expert keep their order.  Returns the plan (`plan`, if given) that
+    moe_dispatch, moe_combine, moe_combine_backward and f4_matmul read.  Runs on
+    the current HIP stream; nothing waits for the GPU.
+    """
+    import torch
+
+    dev = _device_of(experts, "experts")
+    if experts.dim() != 2:
+        raise ValueError("experts: tokens x top_k ids")
+    t, k = experts.shape
+    num_experts = int(num_experts)
+    nbytes = moe_workspace_bytes(t, k, num_experts)
+    if plan is None:
+        plan = moe_empty_plan(t, k, num_experts, dev)
+    pt, pk, _, *to = _plan_pointers(plan, dev, num_experts, True)
+    if (pt, pk) != (t, k):
+        raise ValueError(f"plan is for {pt} x {pk} slots, experts has {t} x {k}")
+    ids = _pointer(experts, "experts", dev, (torch.int32, torch.int64), (t, k))
+    room = (None, 0)
+    if nbytes > 0:
+        workspace = _workspace(workspace, nbytes, dev)
+        room = (workspace.data_ptr(), workspace.numel())
+    _run(load_library().muon_moe_sort, dev, t, k, num_experts, ids, experts.element_size(), *to, *room)
+    return plan
+
+
+def _floats():
+    import torch
+
+    return torch.bfloat16, torch.float32
+
+
+def moe_dispatch(x, plan: MoePlan, out=None):
+    """The tokens' rows at their sorted places: out[plan.rows[t, k]] = x[t].
+
+    x: tokens x cols, contiguous, bf16 or fp32.  out: rows x cols of the same
+    dtype, for as many rows as are wanted (new: tokens * top_k); rows behind the
+    last sorted one are left as they were.  Its gradient is moe_combine without
+    weights.
+    """
+    import torch
+
+    dev = _device_of(x, "x")
+    t, k, _, _, _, rows, _ = _plan_pointers(plan, dev)
+    if out is None:
+        out = torch.empty((t * k, x.shape[-1]), dtype=x.dtype, device=dev)
+    po = _pointer(out, "out", dev, (x.dtype,), (None, x.shape[-1]), True)
+    px = _pointer(x, "x", dev, _floats(), (t, None))
+    _run(load_library().muon_moe_dispatch, dev, t, k, x.shape[1], px, rows, out.shape[0], po,
+         _dtype_code(x.dtype))
+    return out
+
+
+def moe_combine(ys, plan: MoePlan, weights=None, out=None):
+    """The experts' rows back at their tokens: out[t] = sum_k weights[t, k] *
+    ys[plan.rows[t, k]], in fp32, rounded once.
+
+    ys: sorted rows x cols, contiguous, bf16 or fp32; slots whose row it does not
+    have count as dropped, and dropped ones add nothing.  weights: tokens x top_k,
+    float32; without them 1 (the gradient of moe_dispatch).  Returns out (new:
+    tokens x cols of ys' dtype).
+    """
+    import torch
+
+    dev = _device_of(ys, "ys")
+    t, k, _, _, _, rows, _ = _plan_pointers(plan, dev)
+    if out is None:
+        out = torch.empty((t, ys.shape[-1]), dtype=ys.dtype, device=dev)
+    po = _pointer(out, "out", dev, (ys.dtype,), (t, ys.shape[-1]), True)
+    py = _pointer(ys, "ys", dev, _floats(), (None, None))
+    pw = None if weights is None else _pointer(weights, "weights", dev, (torch.float32,), (t, k))
+    _run(load_library().muon_moe_combine, dev, t, k, ys.shape[1], ys.shape[0], py, rows, pw, po,
+         _dtype_code(ys.dtype))
+    return out
+
+
+def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=None):
+    """The gradient of moe_combine: dys[plan.rows[t, k]] = weights[t, k] * dout[t], and
+    dweights[t, k] = <dout[t], ys[plan.rows[t, k]]> (float32 sums; 0 for dropped slots).
+
+    dout: tokens x cols, ys: sorted rows x cols, of one dtype.  Returns (dys,
+    dweights); rows of dys behind the last sorted one are left as they were.
+    """
+    import torch
+
+    dev = _device_of(dout, "dout")
+    t, k, _, _, _, rows, _ = _plan_pointers(plan, dev)
+    if dys is None:
+        dys = torch.empty_like(ys)
+    if dweights is None:
+        dweights = torch.empty((t, k), dtype=torch.float32, device=dev)
+    f32 = (torch.float32,)
+    pdy = _pointer(dys, "dys", dev, (dout.dtype,), tuple(ys.shape), True)
+    pdw = _pointer(dweights, "dweights", dev, f32, (t, k), True)
+    pd = _pointer(dout, "dout", dev, _floats(), (t, None))
+    py = _pointer(ys, "ys", dev, (dout.dtype,), (None, dout.shape[1]))
+    pw = _pointer(weights, "weights", dev, f32, (t, k))
+    _run(load_library().muon_moe_combine_backward, dev, t, k, dout.shape[1], pd, ys.shape[0], py, rows,
+         pw, pdy, pdw, _dtype_code(dout.dtype))
+    return dys, dweights
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights and their products with few rows
+# ---------------------------------------------------------------------------
+
+F4_GROUP = 32
+
+
+class F4Operand(NamedTuple):
+    """Matrices of 4-bit weights, all rows x cols, contracted over cols, one power-of-
+    two scale per group of F4_GROUP columns.  q: uint8, matrices x rows/16 x
+    cols/128 x 64 x 16; scales: uint8, matrices x rows/16 x cols/512 x 16 x 16
+    (each quotient rounded up), laid out as muon_f4_quantize in the C header says."""
+
+    q: object
+    scales: object
+    rows: int
+    cols: int
+
+
+def f4_empty(matrices: int, rows: int, cols: int, device) -> F4Operand:
+    """Room for the operand of matrices of rows x cols (contracted over cols)."""
+    import torch
+
+    rt, kt = -(-rows // 16), -(-cols // 128)
+    return F4Operand(torch.empty((matrices, rt, kt, 64, 16), dtype=torch.uint8, device=device),
+                     torch.empty((matrices, rt, -(-kt // 4), 16, 16), dtype=torch.uint8, device=device),
+                     rows, cols)
+
+
+def _f4_pointers(w, name, dev, written=False):
+    import torch
+
+    q, s, rows, cols = w
+    rt, kt = -(-rows // 16), -(-cols // 128)
+    u8 = (torch.uint8,)
+    pq = _pointer(q, name + ".q", dev, u8, (None, rt, kt, 64, 16), written)
+    return q.shape[0], pq, _pointer(s, name + ".scales", dev, u8, (q.shape[0], rt, -(-kt // 4), 16, 16),
+                                    written)
+
+
+@functools.lru_cache(maxsize=None)
+def f4_workspace_bytes(matrices: int) -> int:
+    """Device workspace bytes of f4_quantize."""
+    n = load_library().muon_f4_workspace_bytes(int(matrices))
+    if n == SIZE_MAX:
+        raise MuonError(MUON_ERR_INVALID_ARG, "muon_f4_workspace_bytes", last_error_detail())
+    return int(n)
+
+
+def f4_quantize(ws: Sequence, transpose: bool = False, out: Optional[F4Operand] = None,
+                workspace=None) -> F4Operand:
+    """4-bit weights of a list of matrices of one shape (the experts of a layer, in
+    order), as one operand.
+
+    ws: contiguous 2-D bf16 or fp32 tensors (one dtype), rows x cols of the
+    operand, or with transpose its cols x rows (x W instead of x W^T).  The scale
+    of a group is the smallest power of two, from 2^-125 to 2^125, with its largest
+    magnitude at most 6 times it; codes are rounded to nearest even.  A group that
+    holds an infinity or NaN stands for NaN.
+    """
+    ws = list(ws)
+    if not ws:
+        raise ValueError("ws: at least one matrix")
+    shape = tuple(ws[0].shape)
+    if any(tuple(w.shape) != shape for w in ws):
+        raise ValueError("ws: matrices of one shape")
+    if len(shape) != 2:
+        raise ValueError("ws: tensors must be contiguous 2-D matrices")
+    rows, cols = shape[::-1] if transpose else shape
+    dev = _device_of(ws[0], "ws")
+    nbytes = f4_workspace_bytes(len(ws))
+    if out is None:
+        out = f4_empty(len(ws), rows, cols, dev)
+    if (out.rows, out.cols) != (rows, cols) or out.q.shape[0] != len(ws):
+        raise ValueError(f"out is for {out.q.shape[0]} matrices of {out.rows} x {out.cols}, ws are "
+                         f"{len(ws)} of {rows} x {cols}")
+    _, pq, psc = _f4_pointers(out, "out", dev, True)
+    _, _, _, ptrs = _matrices(ws, "ws")
+    workspace = _workspace(workspace, nbytes, dev)
+    _call(load_library().muon_f4_quantize, dev, workspace, len(ws), rows, cols, ptrs,
+          _dtype_code(ws[0].dtype), 1 if transpose else 0, pq, psc)
+    return out
+
+
+def f4_matmul(x, w: F4Operand, plan: Optional[MoePlan] = None, gather: bool = False, out=None,
+              out_dtype=None):
+    """Rows times 4-bit weights: out[p] = x[p] W^T, for single tokens.
+
+    x: contiguous, bf16, rows x w.cols.  Without a plan w holds one matrix.  With
+    one it holds an expert's matrix each, and the sorted rows of expert e take
+    matrix e; gather: x are the tokens' own rows (as moe_dispatch takes them), read
+    through the plan.  Nothing of the plan is read on the host.  out: bf16 or fp32,
+    x's rows (gather: up to tokens * top_k) x w.rows; new ones are of out_dtype
+    (bfloat16).  Rows behind the last sorted one are left as they were.  Products
+    are exact, sums fp32, rounded once.  For many rows an expert
+    f8_matmul_batched is faster.
+    """
+    import torch
+
+    dev = _device_of(x, "x")
+    if gather and plan is None:
+        raise ValueError("gather needs a plan")
+    top_k, offsets, active, slots = 1, None, None, None
+    m = x.shape[0] if x.dim() == 2 else -1
+    if plan is not None:
+        t, top_k, _, offsets, active, _, slots = _plan_pointers(plan, dev, w.q.shape[0])
+        if gather:
+            if m != t:
+                raise ValueError(f"x: the rows of {t} tokens")
+            m = t * top_k
+        else:
+            slots = None
+            if m > t * top_k:
+                raise ValueError(f"x: at most {t * top_k} sorted rows")
+    elif w.q.shape[0] != 1:
+        raise ValueError("without a plan w holds one matrix")
+    if out is None:
+        out = torch.empty((m, w.rows), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+                          device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out has another dtype than out_dtype")
+    po = _pointer(out, "out", dev, _floats(), (None if gather else m, w.rows), True)
+    if out.shape[0] > m:
+        raise ValueError(f"out: at most {m} rows")
+    px = _pointer(x, "x", dev, (torch.bfloat16,), (None, w.cols))
+    count, pq, psc = _f4_pointers(w, "w", dev)
+    _run(load_library().muon_f4_matmul, dev, count, w.rows, w.cols, pq, psc, out.shape[0], px, x.shape[0],
+         offsets, active, slots, top_k, po, _dtype_code(out.dtype))
+    return out
 
 
 def hbm_stream(ins: Sequence, outs: Sequence, nontemporal: bool = False) -> None:

@@ -1,0 +1,118 @@
+// Dropout over a ragged batch of flat tensors, its mask from a counter-based
+// generator and never stored:
+//
+//   y_j = u_j < t ? 0 : x_j * 2^16 / (2^16 - t),   t = round(p * 2^16)
+//
+// u_j is 16 bits of Philox 4x32 with 7 rounds (Salmon, Moraes, Dror and Shaw,
+// "Parallel random numbers: as easy as 1, 2, 3", SC 2011): eight elements share
+// the block of counter (j / 8, tensor, offset) and key (seed), so that the mask
+// depends on the element's place alone and the gradient is the same call on the
+// gradients.  What is dropped is 0 whatever it held.
+#include "grad_chunks.hpp"
+
+namespace muon {
+
+namespace {
+
+// The four words of a block.
+__device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int r = 0; r < kDropRounds; ++r) {
+    const uint64_t p = static_cast<uint64_t>(0xD2511F53u) * c[0];
+    const uint64_t q = static_cast<uint64_t>(0xCD9E8D57u) * c[2];
+    const uint32_t c1 = c[1], c3 = c[3];
+    c[0] = static_cast<uint32_t>(q >> 32) ^ c1 ^ k0;
+    c[1] = static_cast<uint32_t>(q);
+    c[2] = static_cast<uint32_t>(p >> 32) ^ c3 ^ k1;
+    c[3] = static_cast<uint32_t>(p);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
+struct DropKey {
+  uint64_t seed, offset;
+  int32_t tensor;
+  uint32_t threshold;
+  float scale;
+};
+
+// Elements j .. j + 3 of a tensor, j a multiple of 4.
+__device__ __forceinline__ void drop4(const DropKey& k, int64_t j, float* v) {
+  uint32_t c[4] = {static_cast<uint32_t>(j / 8), static_cast<uint32_t>(k.tensor),
+                   static_cast<uint32_t>(k.offset), static_cast<uint32_t>(k.offset >> 32)};
+  philox(c, static_cast<uint32_t>(k.seed), static_cast<uint32_t>(k.seed >> 32));
+  const bool second = (j & 4) != 0;
+  const uint32_t w[2] = {second ? c[2] : c[0], second ? c[3] : c[1]};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t u = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
+    v[e] = u < k.threshold ? 0.f : v[e] * k.scale;
+  }
+}
+
+constexpr int kDropSpan = 4096;  // elements of a block
+
+template <typename Ti, typename To>
+__device__ __forceinline__ void drop_span(const Ti* x, To* y, int64_t at, int64_t n,
+                                          const DropKey& k) {
+  for (int64_t i = static_cast<int64_t>(threadIdx.x) * 4; i < n; i += kThreads * 4) {
+    float v[4];
+    if (i + 4 <= n) {
+      load4<Ti, false>(x + i, v);
+      drop4(k, at + i, v);
+      store4<To, false>(y + i, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = i + e < n ? Elt<Ti>::to_f32(x[i + e]) : 0.f;
+      drop4(k, at + i, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < n) y[i + e] = Elt<To>::from_f32(v[e]);
+    }
+  }
+}
+
+}  // namespace
+
+__global__ __launch_bounds__(kThreads) void k_dropout(ArgTable, GradCtx ctx, DropArgs p,
+                                                      int32_t chunks) {
+  constexpr int kPer = static_cast<int>(kGradSpan / kDropSpan);  // blocks per chunk
+  const int32_t b = block_number();
+  if (b / kPer >= chunks) return;
+  const Chunk c = find_chunk(ctx, b / kPer);
+  const int64_t off = static_cast<int64_t>(b % kPer) * kDropSpan;
+  const int64_t left = c.n - off, n = left < kDropSpan ? left : kDropSpan;
+  if (n <= 0) return;
+  DropKey k;
+  k.seed = p.rng != nullptr ? load_const(p.rng) : p.seed;
+  k.offset = p.rng != nullptr ? load_const(p.rng + 1) : p.offset;
+  k.tensor = c.tensor;
+  k.threshold = p.threshold;
+  k.scale = p.scale;
+  const int64_t at = c.base + off;
+  const uint16_t* xh = static_cast<const uint16_t*>(c.g) + at;
+  const float* xf = static_cast<const float*>(c.g) + at;
+  uint16_t* yh = static_cast<uint16_t*>(c.out) + at;
+  float* yf = static_cast<float*>(c.out) + at;
+  if (c.in_bf16) {
+    if (c.out_bf16)
+      drop_span(xh, yh, at, n, k);
+    else
+      drop_span(xh, yf, at, n, k);
+  } else {
+    if (c.out_bf16)
+      drop_span(xf, yh, at, n, k);
+    else
+      drop_span(xf, yf, at, n, k);
+  }
+}
+
+hipError_t launch_dropout(const ArgTable& t, const GradCtx& c, int32_t chunks, const DropArgs& p) {
+  if (chunks <= 0) return hipSuccess;
+  hipLaunchKernelGGL(k_dropout, block_grid(chunks * (kGradSpan / kDropSpan)), dim3(kThreads), 0,
+                     c.stream, t, c, p, chunks);
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -266,6 +266,81 @@ constexpr int kF8Tile = 256;  // output tile (both sides)
 hipError_t launch_f8_small(const ArgTable& t, const F8ProdCtx& c, int32_t nblocks, bool is_bf16,
                            int32_t mt, int32_t nt);
 
+// Dropout over a ragged batch, on the gradients' tables (GradDesc, GradCtx).
+constexpr int kDropRounds = 7;  // of Philox 4x32, the fewest its authors found no test to fail
+constexpr int64_t kDropMaxNumel = 1ll << 35;  // 2^32 blocks of eight elements
+struct DropArgs {
+  const uint64_t* rng;     // device: seed, offset; or null: the two below
+  uint64_t seed, offset;
+  uint32_t threshold;      // of 2^16: an element whose 16 bits are below it is dropped
+  float scale;             // of those that stay
+};
+hipError_t launch_dropout(const ArgTable& t, const GradCtx& c, int32_t chunks, const DropArgs& p);
+
+// Tokens to the experts and back.
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxTopK = 64;
+constexpr int64_t kMoeMaxSlots = (1 << 24) - 1;  // also fewer blocks than a launch holds
+constexpr int kSortPiece = 8192;  // slots that a block of the sort takes at a time
+struct MoeSortArgs {
+  const void* ids;         // n of 4 or 8 bytes
+  int32_t* offsets;        // experts + 1
+  int32_t* active;         // experts + 1: how many have rows, which, then -1
+  int32_t* rows;           // n
+  int32_t* slots;          // n
+  int64_t n;
+  int32_t experts;
+};
+hipError_t launch_moe_sort(const MoeSortArgs& a, int32_t id_bytes, hipStream_t s);
+inline size_t moe_sort_workspace(int64_t, int32_t) { return 0; }
+
+// Rows of `row_bytes` bytes, of tokens (top_k slots each) and sorted by expert.
+struct MoeRowArgs {
+  const void* tokens;      // dispatch: x; backward: dout
+  const void* sorted;      // combine, backward: y
+  const int32_t* rows;     // the sorted row of each slot
+  const float* weights;    // of each slot, or null (combine): 1
+  void* out;
+  float* dweights;         // backward
+  int64_t tokens_n, sorted_rows, row_bytes;
+  int32_t top_k;
+};
+hipError_t launch_moe_dispatch(const MoeRowArgs& a, hipStream_t s);
+hipError_t launch_moe_combine(const MoeRowArgs& a, bool is_bf16, hipStream_t s);
+hipError_t launch_moe_backward(const MoeRowArgs& a, bool is_bf16, hipStream_t s);
+
+// F4 layout, of a list of matrices of R rows contracted over K columns: tiles of
+// 16 rows x 128 columns (K up to a multiple of 128: ktiles), row-major over each
+// matrix, 1024 bytes each: chunk 16 c + r of 16 bytes holds columns 32 i + 8 c + j
+// (i < 4, j < 8) of row r, two to a byte, the even column in the low half, byte
+// 4 i + j / 2.  Scales: for each tile row and four tiles (rounded up) 16 x 16 bytes,
+// row r's 16 groups of 32 columns; byte e + 127, 255 for NaN.  Columns past the
+// matrix are a group's zeros; rows past it, and groups past the last tile, are
+// code 0 with scale 127.
+constexpr int kF4Tile = 128;
+constexpr int kF4Group = 32;
+struct F4QuantArgs {
+  const void* table;       // as GradCtx: the matrices' pointers
+  char *q, *s;
+  int64_t tiles;           // of all matrices
+  int32_t rows, cols;      // of an operand
+  int32_t rtiles, ktiles;
+};
+hipError_t launch_f4_quantize(const ArgTable& t, const F4QuantArgs& a, bool is_bf16, bool transpose,
+                              hipStream_t s);
+struct F4ProdArgs {
+  const char *q, *s;
+  const void* x;           // bf16, x_rows x cols
+  const int32_t* offsets;  // the sort's, or (with active and slots) null: every row takes matrix 0
+  const int32_t* active;
+  const int32_t* slots;    // row p is x's row slots[p] / top_k; null: row p
+  void* y;                 // m x rows, bf16 or fp32
+  int64_t m, x_rows;
+  int32_t experts, rows, cols, top_k;
+  int32_t rtiles, ktiles;
+};
+hipError_t launch_f4_matmul(const F4ProdArgs& a, bool is_bf16, hipStream_t s);
+
 // Host launchers (one per kernel family).  is_bf16 selects the element type.
 // Momentum (step), U into X ping and the per-block sums of U^2.
 hipError_t launch_prepare(const LaunchCtx& c, int32_t nblocks, bool is_bf16, const ElemParams& p);

@@ -110,6 +110,23 @@ PyObject* scan(PyObject*, PyObject* args) {
   }
 }
 
+// address(tensor, written): of one tensor, as scan gives it.
+PyObject* one_address(PyObject*, PyObject* args) {
+  PyObject* t;
+  int written;
+  if (!PyArg_ParseTuple(args, "Op", &t, &written)) return nullptr;
+  if (!THPVariable_Check(t)) {
+    PyErr_SetString(PyExc_TypeError, "no tensor");
+    return nullptr;
+  }
+  try {
+    return PyLong_FromLongLong(address(THPVariable_Unpack(t), written != 0));
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
 // same_shapes(a, b): whether two equally long lists of tensors have equal shapes.
 PyObject* same_shapes(PyObject*, PyObject* args) {
   PyObject *a, *b;
@@ -322,6 +339,7 @@ PyMethodDef methods[] = {
     {"room", room, METH_VARARGS, "room(rows, columns, dtype code, device)"},
     {"room_f8", room_f8, METH_VARARGS, "room_f8(rows, columns, block, device, kind)"},
     {"scan", scan, METH_VARARGS, "scan(tensors, written): device, flags, dtype codes, sizes, pointers"},
+    {"address", one_address, METH_VARARGS, "address(tensor, written)"},
     {"same_shapes", same_shapes, METH_VARARGS, "same_shapes(a, b)"},
     {"scan_f8", scan_f8, METH_VARARGS, "scan_f8(operands, block, written)"},
     {nullptr, nullptr, 0, nullptr},
