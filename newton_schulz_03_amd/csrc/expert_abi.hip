@@ -124,6 +124,7 @@ extern "C" int32_t muon_moe_sort(int64_t tokens, int32_t top_k, int32_t experts,
     a.active = active;
     a.rows = rows;
     a.slots = slots;
+    a.counts = static_cast<uint32_t*>(workspace);
     a.n = tokens * top_k;
     a.experts = experts;
     const size_t need = moe_sort_workspace(a.n, experts);

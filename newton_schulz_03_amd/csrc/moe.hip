@@ -10,6 +10,12 @@
 //
 // Nothing depends on the order in which blocks or waves run: equal calls give
 // equal bits.
+//
+// The sort: up to kSortFew slots in a kernel that compares all of them (8 slots of
+// 384 experts: 2.2 us, the next one 6.6), up to kSortPiece in one block, more in
+// two launches, counts and rows (524288 slots of 8 bytes, 384 experts: 3.2 + 13.2 us;
+// one block for all of them took 880).  Pieces of 2048 slots: 22 us for the rows, since
+// every block adds up the counts of twice as many.
 #include "device_common.hpp"
 
 namespace muon {
@@ -17,6 +23,10 @@ namespace muon {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSteps = kSortPiece / kSortThreads;  // slots of a thread in a piece
+// Words of 16-bit counts, two experts each.
+constexpr int kPairs = kMoeMaxExperts / 2;
+constexpr int kSumBatch = 16;  // loads of a thread in flight while it adds up the blocks' counts
 
 template <typename I>
 __device__ __forceinline__ int expert_of(const I* ids, int64_t s, int64_t n, int experts) {
@@ -62,92 +72,169 @@ __device__ __forceinline__ int block_before(int v, int* scratch /* kSortWaves */
 
 }  // namespace
 
-// The rows of the slots.  A block takes its slots in pieces of kSortPiece, each
-// wave kSortPiece / 16 of them in a row: the waves' counts of each expert become
-// where their rows begin, and each wave then walks its slots 64 at a time, a
-// slot's row being its expert's next one plus the lanes before it with that id.
+namespace {
+
+// This thread's slots of a piece that starts at s0 (of the thread): each wave
+// holds kSortPiece / 16 slots in a row, 64 at a time.
+template <typename I>
+__device__ __forceinline__ void load_ids(const MoeSortArgs& a, int64_t s0, int (&e)[kSteps]) {
+  const I* const ids = static_cast<const I*>(a.ids);
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) e[u] = expert_of(ids, s0 + u * 64, a.n, a.experts);
+}
+
+// Adds one to expert e's 16 bits.
+__device__ __forceinline__ void count_one(uint32_t* counts, int e) {
+  if (e >= 0) atomicAdd(&counts[e >> 1], 1u << (16 * (e & 1)));
+}
+
+}  // namespace
+
+// How many slots of each expert a block of the sort will find, two 16-bit counts a
+// word.  Only for lists of more than one block.
+template <typename I>
+__global__ __launch_bounds__(kSortThreads) void k_moe_count(MoeSortArgs a) {
+  __shared__ uint32_t counts[kPairs];
+  const int me = threadIdx.x, pairs = (a.experts + 1) / 2;
+  if (me < pairs) counts[me] = 0;
+  __syncthreads();
+  const int64_t from = static_cast<int64_t>(blockIdx.x) * a.span;
+  for (int64_t at = from; at < from + a.span && at < a.n; at += kSortPiece) {
+    int e[kSteps];
+    load_ids<I>(a, at + (me >> 6) * (64 * kSteps) + (me & 63), e);
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) count_one(counts, e[u]);
+  }
+  __syncthreads();
+  if (me < pairs) a.counts[blockIdx.x * pairs + me] = counts[me];
+}
+
+// The rows of the slots.  A block takes `span` slots in pieces of kSortPiece.  The
+// waves' counts of each expert in a piece become where their rows begin, and each
+// wave walks its slots 64 at a time: a slot's row is its expert's next one plus
+// the lanes before it with that id.  Where the block's rows begin follows from all
+// blocks' counts, which every block adds up for itself (128 blocks, 384 experts:
+// 98 KB from the L2).
 template <typename I>
 __global__ __launch_bounds__(kSortThreads) void k_moe_sort(MoeSortArgs a) {
-  constexpr int kSteps = kSortPiece / kSortThreads;
-  constexpr int kPairs = kMoeMaxExperts / 2;
-  __shared__ int32_t base[kMoeMaxExperts];  // the first row of the piece for each expert
-  __shared__ uint32_t next[kSortWaves][kPairs];  // each wave's next row after that, 16 bits each
+  __shared__ int32_t base[kMoeMaxExperts];     // the first row of the piece for each expert
+  __shared__ int32_t totals[kMoeMaxExperts];   // slots of each expert in all blocks
+  __shared__ uint32_t next[kSortWaves * kPairs];  // each wave's next row after that
   __shared__ int scratch[kSortWaves];
   static_assert(kMoeMaxExperts <= kSortThreads && kSortPiece < (1 << 16));
-  const I* const ids = static_cast<const I*>(a.ids);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int me = threadIdx.x;  // the expert that a thread counts for
   const int pairs = (a.experts + 1) / 2;
-  int bits = 0;
-  while ((1 << bits) < a.experts) ++bits;
+  const int bits = 32 - __builtin_clz((a.experts - 1) | 1);
+  const int64_t from = static_cast<int64_t>(blockIdx.x) * a.span;
+  const int64_t to = min(a.n, from + a.span);
+  const bool single = gridDim.x == 1 && to - from <= kSortPiece;
+  uint32_t* const row = next + wave * pairs;
+  volatile uint16_t* const mine = reinterpret_cast<volatile uint16_t*>(row);
 
-  if (me < a.experts) base[me] = 0;
+  int e[kSteps];
+  load_ids<I>(a, from + wave * (64 * kSteps) + lane, e);
+  for (int i = me; i < kSortWaves * pairs; i += kSortThreads) next[i] = 0;
+  base[me] = 0;
+  totals[me] = 0;
   __syncthreads();
-  for (int64_t s = threadIdx.x; s < a.n; s += kSortThreads) {
-    const int e = expert_of(ids, s, a.n, a.experts);
-    if (e >= 0) atomicAdd(&base[e], 1);
-  }
-  __syncthreads();
-  const int count = me < a.experts ? base[me] : 0;
-  int kept, some;
-  const int first = block_before(count, scratch, &kept);
-  const int at = block_before(count > 0 ? 1 : 0, scratch, &some);
-  if (me < a.experts) {
-    base[me] = first;
-    a.offsets[me] = first;
-    if (count > 0) a.active[1 + at] = me;
-    if (me >= some) a.active[1 + me] = -1;
-  }
-  if (me == 0) {
-    a.offsets[a.experts] = kept;
-    a.active[0] = some;
-  }
-  for (int64_t p = kept + threadIdx.x; p < a.n; p += kSortThreads) a.slots[p] = -1;
-
-  volatile uint16_t* const mine = reinterpret_cast<volatile uint16_t*>(next[wave]);
-  for (int64_t from = 0; from < a.n; from += kSortPiece) {
-    for (int i = me; i < kSortWaves * pairs; i += kSortThreads) next[i / pairs][i % pairs] = 0;
-    __syncthreads();
-    const int64_t s0 = from + wave * (64 * kSteps) + lane;
-    for (int u = 0; u < kSteps; ++u) {
-      const int e = expert_of(ids, s0 + u * 64, a.n, a.experts);
-      if (e >= 0) atomicAdd(&next[wave][e / 2], 1u << (16 * (e & 1)));
+  if (!single) {
+    // threads share a pair of experts: `groups` of them, each for every groups-th block
+    const int groups = kSortThreads / pairs, g = me / pairs, p = me - g * pairs;
+    if (g < groups) {
+      int before[2] = {0, 0}, all[2] = {0, 0};
+      const int blocks = static_cast<int>(gridDim.x), here = static_cast<int>(blockIdx.x);
+      for (int b0 = g; b0 < blocks; b0 += kSumBatch * groups) {
+        uint32_t c[kSumBatch];  // all requested before the first is added
+#pragma unroll
+        for (int u = 0; u < kSumBatch; ++u) {
+          const int b = b0 + u * groups;
+          c[u] = b < blocks ? a.counts[b * pairs + p] : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < kSumBatch; ++u) {
+          const int lo = c[u] & 0xffffu, hi = c[u] >> 16;
+          const bool earlier = b0 + u * groups < here;
+          all[0] += lo;
+          all[1] += hi;
+          before[0] += earlier ? lo : 0;
+          before[1] += earlier ? hi : 0;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        atomicAdd(&totals[2 * p + h], all[h]);
+        atomicAdd(&base[2 * p + h], before[h]);
+      }
     }
+  }
+  int64_t piece = from;
+  do {
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) count_one(row, e[u]);
     __syncthreads();
-    for (int i = me; i < pairs; i += kSortThreads) {
+    if (me < pairs) {
       uint32_t sum = 0;
 #pragma unroll
       for (int w = 0; w < kSortWaves; ++w) {
-        const uint32_t t = next[w][i];
-        next[w][i] = sum;
+        const uint32_t t = next[w * pairs + me];
+        next[w * pairs + me] = sum;
         sum += t;
       }
+      if (single) {
+        totals[2 * me] = sum & 0xffffu;
+        totals[2 * me + 1] = sum >> 16;
+      }
     }
     __syncthreads();
+    if (piece == from) {
+      const int count = totals[me];
+      int kept, some;
+      const int first = block_before(count, scratch, &kept);
+      const int at = block_before(count > 0 ? 1 : 0, scratch, &some);
+      base[me] += first;
+      if (blockIdx.x == 0 && me < a.experts) {
+        a.offsets[me] = first;
+        if (count > 0) a.active[1 + at] = me;
+        if (me >= some) a.active[1 + me] = -1;
+        if (me == 0) {
+          a.offsets[a.experts] = kept;
+          a.active[0] = some;
+        }
+      }
+      for (int64_t p = max(static_cast<int64_t>(kept), from) + me; p < to; p += kSortThreads)
+        a.slots[p] = -1;
+      __syncthreads();
+    }
+#pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-      const int64_t s = s0 + u * 64;
-      const int e = expert_of(ids, s, a.n, a.experts);
-      const uint64_t same = same_id(e, bits);
+      const int64_t s = piece + wave * (64 * kSteps) + u * 64 + lane;
+      const uint64_t same = same_id(e[u], bits);
       const int rank = __popcll(same & ((1ull << lane) - 1));
-      int row = -1, begun = 0;
-      if (e >= 0) {
-        begun = mine[e];
-        row = base[e] + begun + rank;
+      int to_row = -1, begun = 0;
+      if (e[u] >= 0) {
+        begun = mine[e[u]];
+        to_row = base[e[u]] + begun + rank;
       }
       __builtin_amdgcn_wave_barrier();  // every lane has read before the first writes
-      if (e >= 0 && rank == 0) mine[e] = static_cast<uint16_t>(begun + __popcll(same));
+      if (e[u] >= 0 && rank == 0) mine[e[u]] = static_cast<uint16_t>(begun + __popcll(same));
       __builtin_amdgcn_wave_barrier();
-      if (s < a.n) {
-        a.rows[s] = row;
-        if (row >= 0) a.slots[row] = static_cast<int32_t>(s);
+      if (s < to) {
+        a.rows[s] = to_row;
+        if (to_row >= 0) a.slots[to_row] = static_cast<int32_t>(s);
       }
     }
+    piece += kSortPiece;
+    if (piece >= to) break;
+    load_ids<I>(a, piece + wave * (64 * kSteps) + lane, e);
     __syncthreads();
     // the last wave's next rows are past all of the piece's
-    if (me < a.experts)
-      base[me] += reinterpret_cast<volatile uint16_t*>(next[kSortWaves - 1])[me];
+    const uint32_t last = next[(kSortWaves - 1) * pairs + (me >> 1)];
+    if (me < a.experts) base[me] += (me & 1 ? last >> 16 : last) & 0xffffu;
     __syncthreads();
-  }
+    for (int i = me; i < kSortWaves * pairs; i += kSortThreads) next[i] = 0;
+    __syncthreads();
+  } while (true);
 }
 
 namespace {
@@ -262,12 +349,105 @@ int piece_bytes(int64_t row_bytes) {
 
 }  // namespace
 
-hipError_t launch_moe_sort(const MoeSortArgs& a, int32_t id_bytes, hipStream_t s) {
-  if (id_bytes == 8)
-    hipLaunchKernelGGL(k_moe_sort<int64_t>, dim3(1), dim3(kSortThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL(k_moe_sort<int32_t>, dim3(1), dim3(kSortThreads), 0, s, a);
+// The plan of up to kSortFew slots, by comparing all of them with each other and
+// with every expert: two barriers and no counts to clear and add up (8 slots of
+// 384 experts 3.6 us; the kernel above 6.6).
+constexpr int kFewThreads = 512;
+template <typename I>
+__global__ __launch_bounds__(kFewThreads) void k_moe_sort_few(MoeSortArgs a) {
+  __shared__ __attribute__((aligned(16))) int id[kSortFew], once[kSortFew];
+  const int me = threadIdx.x, n = static_cast<int>(a.n);
+  const int fours = (n + 3) / 4;
+  const int mine = expert_of(static_cast<const I*>(a.ids), me, n, a.experts);
+  if (me < 4 * fours) id[me] = mine >= 0 ? mine : INT32_MAX;
+  __syncthreads();
+  const int4* const id4 = reinterpret_cast<const int4*>(id);
+  const int4* const once4 = reinterpret_cast<const int4*>(once);
+  if (me < 4 * fours) {
+    int before = 0, kept = 0;
+    bool first = mine >= 0;
+    for (int j = 0; j < fours; ++j) {
+      const int4 v = id4[j];
+      const int w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool earlier = w[c] == mine && 4 * j + c < me;
+        before += w[c] < mine || earlier ? 1 : 0;
+        first = first && !earlier;
+        kept += w[c] != INT32_MAX ? 1 : 0;
+      }
+    }
+    once[me] = first ? mine : INT32_MAX;
+    if (me < n) {
+      a.rows[me] = mine >= 0 ? before : -1;
+      if (mine >= 0) a.slots[before] = me;
+      if (me >= kept) a.slots[me] = -1;
+    }
+  }
+  __syncthreads();
+  for (int e = me; e <= a.experts; e += kFewThreads) {
+    int before = 0, at = 0, some = 0;
+    bool has = false;
+    for (int j = 0; j < fours; ++j) {
+      const int4 v = id4[j], o = once4[j];
+      const int w[4] = {v.x, v.y, v.z, v.w}, f[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        before += w[c] < e ? 1 : 0;
+        at += f[c] < e ? 1 : 0;
+        has = has || f[c] == e;
+        some += f[c] != INT32_MAX ? 1 : 0;
+      }
+    }
+    a.offsets[e] = before;
+    if (e == a.experts) {
+      a.active[0] = some;
+    } else {
+      if (has) a.active[1 + at] = e;
+      if (e >= some) a.active[1 + e] = -1;
+    }
+  }
+}
+
+namespace {
+
+// The most blocks of a sort: each adds up the counts of all.
+constexpr int64_t kSortBlocks = 320;
+
+int64_t sort_span(int64_t n) {
+  const int64_t pieces = (n + kSortPiece - 1) / kSortPiece;
+  return (pieces + kSortBlocks - 1) / kSortBlocks * kSortPiece;
+}
+int64_t sort_blocks(int64_t n) { return n > 0 ? (n + sort_span(n) - 1) / sort_span(n) : 1; }
+static_assert((kMoeMaxSlots / kSortPiece + kSortBlocks) / kSortBlocks * kSortPiece < (1 << 16),
+              "16-bit counts of a block");
+
+template <typename I>
+hipError_t run_sort(const MoeSortArgs& a, hipStream_t s) {
+  if (a.n <= kSortFew) {
+    hipLaunchKernelGGL(k_moe_sort_few<I>, dim3(1), dim3(kFewThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  const dim3 grid(static_cast<uint32_t>(sort_blocks(a.n)));
+  if (grid.x > 1) {
+    hipLaunchKernelGGL(k_moe_count<I>, grid, dim3(kSortThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(k_moe_sort<I>, grid, dim3(kSortThreads), 0, s, a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+size_t moe_sort_workspace(int64_t n, int32_t experts) {
+  const int64_t blocks = sort_blocks(n);
+  return blocks > 1 ? static_cast<size_t>(blocks) * ((experts + 1) / 2) * 4 : 0;
+}
+
+hipError_t launch_moe_sort(MoeSortArgs a, int32_t id_bytes, hipStream_t s) {
+  a.span = a.n > 0 ? sort_span(a.n) : kSortPiece;
+  return id_bytes == 8 ? run_sort<int64_t>(a, s) : run_sort<int32_t>(a, s);
 }
 
 #define MOE_LAUNCH(kernel) \

@@ -281,18 +281,21 @@ hipError_t launch_dropout(const ArgTable& t, const GradCtx& c, int32_t chunks, c
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 64;
 constexpr int64_t kMoeMaxSlots = (1 << 24) - 1;  // also fewer blocks than a launch holds
-constexpr int kSortPiece = 8192;  // slots that a block of the sort takes at a time
+constexpr int kSortFew = 128;   // slots of the sort that compares all of them
+constexpr int kSortPiece = 4096;  // slots that a block of the sort takes at a time
 struct MoeSortArgs {
   const void* ids;         // n of 4 or 8 bytes
   int32_t* offsets;        // experts + 1
   int32_t* active;         // experts + 1: how many have rows, which, then -1
   int32_t* rows;           // n
   int32_t* slots;          // n
+  uint32_t* counts;        // workspace: of each block, two experts' 16-bit counts a word
   int64_t n;
+  int64_t span;            // slots of a block (set by the launch)
   int32_t experts;
 };
-hipError_t launch_moe_sort(const MoeSortArgs& a, int32_t id_bytes, hipStream_t s);
-inline size_t moe_sort_workspace(int64_t, int32_t) { return 0; }
+hipError_t launch_moe_sort(MoeSortArgs a, int32_t id_bytes, hipStream_t s);
+size_t moe_sort_workspace(int64_t n, int32_t experts);
 
 // Rows of `row_bytes` bytes, of tokens (top_k slots each) and sorted by expert.
 struct MoeRowArgs {

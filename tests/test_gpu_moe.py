@@ -54,7 +54,7 @@ def values(shape, dtype, seed):
 
 
 @pytest.mark.parametrize("tokens,top_k,experts", [
-    (0, 2, 5), (1, 1, 1), (1, 8, 384), (2, 64, 3), (63, 1, 7), (64, 1, 8), (65, 1, 9), (129, 8, 384),
+    (0, 2, 5), (1, 1, 1), (1, 8, 384), (2, 64, 3), (63, 1, 7), (64, 1, 8), (65, 1, 9), (16, 8, 700), (127, 1, 3), (128, 1, 1024), (129, 1, 600), (129, 8, 384),
     (1000, 3, 1024), (1024, 8, 1023), (1025, 8, 33), (4096, 8, 384), (3001, 7, 2), (9000, 6, 511)])
 @pytest.mark.parametrize("drop", [0.0, 0.3])
 def test_sort(tokens, top_k, experts, drop):
