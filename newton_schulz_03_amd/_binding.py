@@ -897,20 +897,36 @@ def dropout_batched(xs: Sequence, p: float, seed: int = 0, offset: int = 0, rng=
 MOE_MAX_EXPERTS, MOE_MAX_TOP_K, MOE_MAX_SLOTS = 1024, 64, (1 << 24) - 1
 
 
-def _pointer(t, name, dev, dtypes, shape, written=False):
-    """A tensor's address, checked: contiguous, of one of `dtypes` and of `shape`
-    (None: any) on `dev`.  Those that a call writes are asked for before those it
-    only reads."""
+_BF16, _FP32, _INT32, _INT64, _UINT8 = 1, 2, 4, 8, 16  # kinds of elements, as bits
+_FLOATS = _BF16 | _FP32
+_READ, _WRITTEN = 0, 1
+
+
+def _kind(dtype) -> int:
     import torch
 
-    if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous():
+    return _BF16 if dtype is torch.bfloat16 else _FP32 if dtype is torch.float32 else 0
+
+
+def _pointer(t, name, dev, kinds, written, *sizes):
+    """A tensor's address, checked: contiguous, of one of these kinds of elements and
+    of these sizes (-1: any) on `dev`.  Those that a call writes are asked for
+    before those it only reads."""
+    at = _lists().expect(t, dev.index, kinds, written, *sizes)
+    if at is not None:
+        return at
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.layout != torch.strided or \
+            not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor on {dev}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}: use " + " or ".join(map(str, dtypes)))
-    if len(t.shape) != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}: want "
-                         + str(tuple("any" if b is None else b for b in shape)))
-    return _lists().address(t, written)
+    known = {torch.bfloat16: _BF16, torch.float32: _FP32, torch.int32: _INT32, torch.int64: _INT64,
+             torch.uint8: _UINT8}
+    if not known.get(t.dtype, 0) & kinds:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}: use "
+                        + " or ".join(str(d) for d, kind in known.items() if kind & kinds))
+    raise ValueError(f"{name} has shape {tuple(t.shape)}: want "
+                     + str(tuple("any" if n < 0 else n for n in sizes)))
 
 
 def _device_of(t, name):
@@ -950,21 +966,25 @@ def moe_empty_plan(tokens: int, top_k: int, num_experts: int, device) -> MoePlan
     return MoePlan(o, a, r.view(tokens, top_k), s)
 
 
-def _plan_pointers(plan, dev, experts=None, written=False):
+def _plan_pointers(plan, dev, experts=-1, written=_READ):
     """(tokens, top_k, experts, addresses of offsets, active, rows and slots)."""
-    import torch
-
-    i32 = (torch.int32,)
     offsets, active, rows, slots = plan
-    prows = _pointer(rows, "plan.rows", dev, i32, (None, None), written)
+    prows = _pointer(rows, "plan.rows", dev, _INT32, written, -1, -1)
     t, k = rows.shape
-    pslots = _pointer(slots, "plan.slots", dev, i32, (t * k,), written)
-    poffsets = _pointer(offsets, "plan.offsets", dev, i32, (None if experts is None else experts + 1,),
-                        written)
+    pslots = _pointer(slots, "plan.slots", dev, _INT32, written, t * k)
+    poffsets = _pointer(offsets, "plan.offsets", dev, _INT32, written, experts + 1 if experts >= 0 else -1)
     e = offsets.shape[0] - 1
-    return t, k, e, poffsets, _pointer(active, "plan.active", dev, i32, (e + 1,), written), prows, pslots
+    return t, k, e, poffsets, _pointer(active, "plan.active", dev, _INT32, written, e + 1), prows, pslots
 
 
+def _slots(plan):
+    """(tokens, top_k) of a plan."""
+    if plan.rows.dim() != 2:
+        raise ValueError("plan.rows: tokens x top_k")
+    return plan.rows.shape
+
+
+@functools.lru_cache(maxsize=256)
 def moe_workspace_bytes(tokens: int, top_k: int, num_experts: int) -> int:
     """Device workspace bytes of moe_sort."""
     n = load_library().muon_moe_workspace_bytes(int(tokens), int(top_k), int(num_experts))
@@ -979,11 +999,10 @@ def moe_sort(experts, num_experts: int, plan: Optional[MoePlan] = None, workspac
     experts: tokens x top_k ids, contiguous int32 or int64 (as torch.topk gives
     them); a slot whose id lies outside [0, num_experts) is dropped.  Slots of one
     expert keep their order.  Returns the plan (`plan`, if given) that
-    moe_dispatch, moe_combine, moe_combine_backward and f4_matmul read.  Runs on
-    the current HIP stream; nothing waits for the GPU.
+    moe_dispatch, moe_combine, moe_combine_backward and f4_matmul read; a new one's
+    four tensors share an allocation.  Runs on the current HIP stream; nothing
+    waits for the GPU.
     """
-    import torch
-
     dev = _device_of(experts, "experts")
     if experts.dim() != 2:
         raise ValueError("experts: tokens x top_k ids")
@@ -991,23 +1010,17 @@ def moe_sort(experts, num_experts: int, plan: Optional[MoePlan] = None, workspac
     num_experts = int(num_experts)
     nbytes = moe_workspace_bytes(t, k, num_experts)
     if plan is None:
-        plan = moe_empty_plan(t, k, num_experts, dev)
-    pt, pk, _, *to = _plan_pointers(plan, dev, num_experts, True)
-    if (pt, pk) != (t, k):
+        plan = _lists().room_plan(t, k, num_experts, dev.index, MoePlan)
+    pt, pk, _, *to = _plan_pointers(plan, dev, num_experts, _WRITTEN)
+    if pt != t or pk != k:
         raise ValueError(f"plan is for {pt} x {pk} slots, experts has {t} x {k}")
-    ids = _pointer(experts, "experts", dev, (torch.int32, torch.int64), (t, k))
-    room = (None, 0)
+    ids = _pointer(experts, "experts", dev, _INT32 | _INT64, _READ, t, k)
+    room = None
     if nbytes > 0:
         workspace = _workspace(workspace, nbytes, dev)
-        room = (workspace.data_ptr(), workspace.numel())
-    _run(load_library().muon_moe_sort, dev, t, k, num_experts, ids, experts.element_size(), *to, *room)
+        room, nbytes = workspace.data_ptr(), workspace.numel()
+    _run(load_library().muon_moe_sort, dev, t, k, num_experts, ids, experts.element_size(), *to, room, nbytes)
     return plan
-
-
-def _floats():
-    import torch
-
-    return torch.bfloat16, torch.float32
 
 
 def moe_dispatch(x, plan: MoePlan, out=None):
@@ -1021,13 +1034,16 @@ def moe_dispatch(x, plan: MoePlan, out=None):
     import torch
 
     dev = _device_of(x, "x")
-    t, k, _, _, _, rows, _ = _plan_pointers(plan, dev)
+    t, k = _slots(plan)
+    _pointer(x, "x", dev, _FLOATS, _READ, t, -1)
+    cols, kind = x.shape[1], _kind(x.dtype)
     if out is None:
-        out = torch.empty((t * k, x.shape[-1]), dtype=x.dtype, device=dev)
-    po = _pointer(out, "out", dev, (x.dtype,), (None, x.shape[-1]), True)
-    px = _pointer(x, "x", dev, _floats(), (t, None))
-    _run(load_library().muon_moe_dispatch, dev, t, k, x.shape[1], px, rows, out.shape[0], po,
-         _dtype_code(x.dtype))
+        out = torch.empty((t * k, cols), dtype=x.dtype, device=dev)
+    po = _pointer(out, "out", dev, kind, _WRITTEN, -1, cols)
+    px = _pointer(x, "x", dev, kind, _READ, t, cols)  # where it is now
+    rows = _pointer(plan.rows, "plan.rows", dev, _INT32, _READ, t, k)
+    _run(load_library().muon_moe_dispatch, dev, t, k, cols, px, rows, out.shape[0], po,
+         MUON_BF16 if kind == _BF16 else MUON_FP32)
     return out
 
 
@@ -1043,14 +1059,17 @@ def moe_combine(ys, plan: MoePlan, weights=None, out=None):
     import torch
 
     dev = _device_of(ys, "ys")
-    t, k, _, _, _, rows, _ = _plan_pointers(plan, dev)
+    t, k = _slots(plan)
+    _pointer(ys, "ys", dev, _FLOATS, _READ, -1, -1)
+    (n, cols), kind = ys.shape, _kind(ys.dtype)
     if out is None:
-        out = torch.empty((t, ys.shape[-1]), dtype=ys.dtype, device=dev)
-    po = _pointer(out, "out", dev, (ys.dtype,), (t, ys.shape[-1]), True)
-    py = _pointer(ys, "ys", dev, _floats(), (None, None))
-    pw = None if weights is None else _pointer(weights, "weights", dev, (torch.float32,), (t, k))
-    _run(load_library().muon_moe_combine, dev, t, k, ys.shape[1], ys.shape[0], py, rows, pw, po,
-         _dtype_code(ys.dtype))
+        out = torch.empty((t, cols), dtype=ys.dtype, device=dev)
+    po = _pointer(out, "out", dev, kind, _WRITTEN, t, cols)
+    py = _pointer(ys, "ys", dev, kind, _READ, n, cols)
+    rows = _pointer(plan.rows, "plan.rows", dev, _INT32, _READ, t, k)
+    pw = None if weights is None else _pointer(weights, "weights", dev, _FP32, _READ, t, k)
+    _run(load_library().muon_moe_combine, dev, t, k, cols, n, py, rows, pw, po,
+         MUON_BF16 if kind == _BF16 else MUON_FP32)
     return out
 
 
@@ -1064,19 +1083,23 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
     import torch
 
     dev = _device_of(dout, "dout")
-    t, k, _, _, _, rows, _ = _plan_pointers(plan, dev)
+    t, k = _slots(plan)
+    _pointer(dout, "dout", dev, _FLOATS, _READ, t, -1)
+    cols, kind = dout.shape[1], _kind(dout.dtype)
+    _pointer(ys, "ys", dev, kind, _READ, -1, cols)
+    n = ys.shape[0]
     if dys is None:
         dys = torch.empty_like(ys)
     if dweights is None:
         dweights = torch.empty((t, k), dtype=torch.float32, device=dev)
-    f32 = (torch.float32,)
-    pdy = _pointer(dys, "dys", dev, (dout.dtype,), tuple(ys.shape), True)
-    pdw = _pointer(dweights, "dweights", dev, f32, (t, k), True)
-    pd = _pointer(dout, "dout", dev, _floats(), (t, None))
-    py = _pointer(ys, "ys", dev, (dout.dtype,), (None, dout.shape[1]))
-    pw = _pointer(weights, "weights", dev, f32, (t, k))
-    _run(load_library().muon_moe_combine_backward, dev, t, k, dout.shape[1], pd, ys.shape[0], py, rows,
-         pw, pdy, pdw, _dtype_code(dout.dtype))
+    pdy = _pointer(dys, "dys", dev, kind, _WRITTEN, n, cols)
+    pdw = _pointer(dweights, "dweights", dev, _FP32, _WRITTEN, t, k)
+    pd = _pointer(dout, "dout", dev, kind, _READ, t, cols)
+    py = _pointer(ys, "ys", dev, kind, _READ, n, cols)
+    rows = _pointer(plan.rows, "plan.rows", dev, _INT32, _READ, t, k)
+    pw = _pointer(weights, "weights", dev, _FP32, _READ, t, k)
+    _run(load_library().muon_moe_combine_backward, dev, t, k, cols, pd, n, py, rows, pw, pdy, pdw,
+         MUON_BF16 if kind == _BF16 else MUON_FP32)
     return dys, dweights
 
 
@@ -1109,15 +1132,12 @@ def f4_empty(matrices: int, rows: int, cols: int, device) -> F4Operand:
                      rows, cols)
 
 
-def _f4_pointers(w, name, dev, written=False):
-    import torch
-
+def _f4_pointers(w, name, dev, written):
     q, s, rows, cols = w
     rt, kt = -(-rows // 16), -(-cols // 128)
-    u8 = (torch.uint8,)
-    pq = _pointer(q, name + ".q", dev, u8, (None, rt, kt, 64, 16), written)
-    return q.shape[0], pq, _pointer(s, name + ".scales", dev, u8, (q.shape[0], rt, -(-kt // 4), 16, 16),
-                                    written)
+    pq = _pointer(q, name + ".q", dev, _UINT8, written, -1, rt, kt, 64, 16)
+    n = q.shape[0]
+    return n, pq, _pointer(s, name + ".scales", dev, _UINT8, written, n, rt, -(-kt // 4), 16, 16)
 
 
 @functools.lru_cache(maxsize=None)
@@ -1156,7 +1176,7 @@ def f4_quantize(ws: Sequence, transpose: bool = False, out: Optional[F4Operand] 
     if (out.rows, out.cols) != (rows, cols) or out.q.shape[0] != len(ws):
         raise ValueError(f"out is for {out.q.shape[0]} matrices of {out.rows} x {out.cols}, ws are "
                          f"{len(ws)} of {rows} x {cols}")
-    _, pq, psc = _f4_pointers(out, "out", dev, True)
+    _, pq, psc = _f4_pointers(out, "out", dev, _WRITTEN)
     _, _, _, ptrs = _matrices(ws, "ws")
     workspace = _workspace(workspace, nbytes, dev)
     _call(load_library().muon_f4_quantize, dev, workspace, len(ws), rows, cols, ptrs,
@@ -1180,34 +1200,38 @@ def f4_matmul(x, w: F4Operand, plan: Optional[MoePlan] = None, gather: bool = Fa
     import torch
 
     dev = _device_of(x, "x")
-    if gather and plan is None:
-        raise ValueError("gather needs a plan")
-    top_k, offsets, active, slots = 1, None, None, None
-    m = x.shape[0] if x.dim() == 2 else -1
-    if plan is not None:
-        t, top_k, _, offsets, active, _, slots = _plan_pointers(plan, dev, w.q.shape[0])
+    _pointer(x, "x", dev, _BF16, _READ, -1, w.cols)
+    m = n = x.shape[0]
+    if plan is None:
         if gather:
-            if m != t:
+            raise ValueError("gather needs a plan")
+        if w.q.shape[0] != 1:
+            raise ValueError("without a plan w holds one matrix")
+    else:
+        t, top_k = _slots(plan)
+        if gather:
+            if n != t:
                 raise ValueError(f"x: the rows of {t} tokens")
             m = t * top_k
-        else:
-            slots = None
-            if m > t * top_k:
-                raise ValueError(f"x: at most {t * top_k} sorted rows")
-    elif w.q.shape[0] != 1:
-        raise ValueError("without a plan w holds one matrix")
+        elif n > t * top_k:
+            raise ValueError(f"x: at most {t * top_k} sorted rows")
     if out is None:
-        out = torch.empty((m, w.rows), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
-                          device=dev)
+        dt = torch.bfloat16 if out_dtype is None else out_dtype
+        out = torch.empty((m, w.rows), dtype=dt, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError("out has another dtype than out_dtype")
-    po = _pointer(out, "out", dev, _floats(), (None if gather else m, w.rows), True)
+    po = _pointer(out, "out", dev, _FLOATS, _WRITTEN, -1 if gather else m, w.rows)
     if out.shape[0] > m:
         raise ValueError(f"out: at most {m} rows")
-    px = _pointer(x, "x", dev, (torch.bfloat16,), (None, w.cols))
-    count, pq, psc = _f4_pointers(w, "w", dev)
-    _run(load_library().muon_f4_matmul, dev, count, w.rows, w.cols, pq, psc, out.shape[0], px, x.shape[0],
-         offsets, active, slots, top_k, po, _dtype_code(out.dtype))
+    px = _pointer(x, "x", dev, _BF16, _READ, n, w.cols)  # where it is now
+    count, pq, psc = _f4_pointers(w, "w", dev, _READ)
+    top_k, offsets, active, slots = 1, None, None, None
+    if plan is not None:
+        _, top_k, _, offsets, active, _, slots = _plan_pointers(plan, dev, count)
+        if not gather:
+            slots = None
+    _run(load_library().muon_f4_matmul, dev, count, w.rows, w.cols, pq, psc, out.shape[0], px, n,
+         offsets, active, slots, top_k, po, MUON_BF16 if out.dtype is torch.bfloat16 else MUON_FP32)
     return out
 
 
