@@ -49,12 +49,57 @@ __device__ __forceinline__ bf16x8_t row8(const uint16_t* x, int32_t k, int32_t c
   }
 }
 
+// Four outputs of a row from column r on.
+template <typename To>
+__device__ __forceinline__ void store4_to(To* y, int32_t left, bool whole, const f32x4_t& v) {
+  if (whole) {
+    if constexpr (sizeof(To) == 2) {
+      u32x2_t w;
+      w[0] = Elt<uint16_t>::pack2(v[0], v[1]);
+      w[1] = Elt<uint16_t>::pack2(v[2], v[3]);
+      *(GLOBAL_AS u32x2_t*)(y) = w;
+    } else {
+      st16(y, __builtin_bit_cast(u32x4_t, v));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) y[i] = Elt<To>::from_f32(v[i]);
+  }
+}
+
+// What a wave reads of RT tile rows over four tiles (512 columns).
+template <int RT>
+struct Quad {
+  u32x4_t w[4][RT];
+  u32x4_t s[RT];
+};
+
+template <int RT>
+__device__ __forceinline__ void load_quad(const F4ProdArgs& a, const char* const (&q)[RT],
+                                          const char* const (&s)[RT], int32_t quad, Quad<RT>& to) {
+#pragma unroll
+  for (int i = 0; i < RT; ++i) to.s[i] = ld16(s[i] + static_cast<int64_t>(quad) * 256);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int32_t t = 4 * quad + j;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      to.w[j][i] = u32x4_t{0, 0, 0, 0};
+      if (t < a.ktiles) to.w[j][i] = ld16(q[i] + static_cast<int64_t>(t) * 1024);
+    }
+  }
+}
+
 }  // namespace
 
-template <typename To, bool VEC>
+// A wave sums RT tile rows times MT * 16 rows of x over its share of the columns.
+template <typename To, int RT, int MT, bool VEC>
 __global__ __launch_bounds__(64 * kF4Waves) void k_f4_matmul(F4ProdArgs a) {
-  __shared__ __attribute__((aligned(16))) f32x4_t part[kF4Waves][64];
+  constexpr int kOnce = RT * MT < 4 ? RT * MT : 4;  // result tiles joined at a time
+  __shared__ __attribute__((aligned(16))) f32x4_t part[kOnce][kF4Waves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int waves = blockDim.x >> 6;
   int32_t e = 0;
   int64_t p0 = 0, p1 = a.m;
   if (a.active != nullptr) {
@@ -64,66 +109,115 @@ __global__ __launch_bounds__(64 * kF4Waves) void k_f4_matmul(F4ProdArgs a) {
     p0 = max(a.offsets[e], 0);
     p1 = min(static_cast<int64_t>(a.offsets[e + 1]), a.m);
   }
-  const int64_t strip = static_cast<int64_t>(e) * a.rtiles + blockIdx.x;
-  const char* const q = a.q + (strip * a.ktiles * 64 + lane) * 16;
-  const uint32_t* const s = reinterpret_cast<const uint32_t*>(a.s) +
-                            (strip * ((a.ktiles + 3) / 4) * 16 + (lane & 15)) * 4;
-  const int32_t t0 = a.ktiles * wave / kF4Waves, t1 = a.ktiles * (wave + 1) / kF4Waves;
-  for (; p0 < p1; p0 += 16) {
-    // lanes past the last row take that row's: their results are not stored
-    int64_t row = min(p0 + (lane & 15), p1 - 1);
-    if (a.slots != nullptr) {
-      row = a.slots[row] / a.top_k;
-      if (row < 0 || row >= a.x_rows) row = 0;
-    }
-    const uint16_t* const x = static_cast<const uint16_t*>(a.x) + row * a.cols;
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    for (int32_t t = t0; t < t1; ++t) {
-      const u32x4_t w = ld16(q + static_cast<int64_t>(t) * 1024);
-      const uint32_t sc = s[(t / 4) * 64 + t % 4];
+  const int32_t quads = (a.ktiles + 3) / 4;
+  const char *q[RT], *s[RT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8_t b = row8<VEC>(x, t * kF4Tile + 32 * i + 8 * (lane >> 4), a.cols);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            weights8(w[i], scale_of(sc >> (8 * i) & 255u)), b, acc, 0, 0, 0);
+  for (int i = 0; i < RT; ++i) {
+    // strips past the last take that one's place: their results are not stored
+    const int64_t strip = static_cast<int64_t>(e) * a.rtiles +
+                          min(static_cast<int32_t>(blockIdx.x) * RT + i, a.rtiles - 1);
+    q[i] = a.q + (strip * a.ktiles * 64 + lane) * 16;
+    s[i] = a.s + (strip * quads * 16 + (lane & 15)) * 16;
+  }
+  const int32_t q0 = quads * wave / waves, q1 = quads * (wave + 1) / waves;
+  const int32_t kc = 8 * (lane >> 4);
+  for (; p0 < p1; p0 += 16 * MT) {
+    const uint16_t* x[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      // lanes past the last row take that row's: their results are not stored
+      int64_t row = min(p0 + 16 * j + (lane & 15), p1 - 1);
+      if (a.slots != nullptr) {
+        row = a.slots[row] / a.top_k;
+        if (row < 0 || row >= a.x_rows) row = 0;
+      }
+      x[j] = static_cast<const uint16_t*>(a.x) + row * a.cols;
+    }
+    f32x4_t acc[RT][MT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int32_t quad = q0; quad < q1; ++quad) {
+      Quad<RT> w;
+      load_quad<RT>(a, q, s, quad, w);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          bf16x8_t b[MT];
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            b[j] = row8<VEC>(x[j], quad * 512 + t * kF4Tile + 32 * g + kc, a.cols);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const bf16x8_t v = weights8(w.w[t][i][g], scale_of(w.s[i][t] >> (8 * g) & 255u));
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[j], acc[i][j], 0, 0, 0);
+          }
+        }
       }
     }
-    part[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0) {
-      f32x4_t sum = part[0][lane];
 #pragma unroll
-      for (int w = 1; w < kF4Waves; ++w) sum += part[w][lane];
-      const int64_t p = p0 + (lane & 15);
-      const int32_t r = blockIdx.x * 16 + 4 * (lane >> 4);
-      if (p < p1) {
-        To* const y = static_cast<To*>(a.y) + p * a.rows + r;
+    for (int first = 0; first < RT * MT; first += kOnce) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (r + i < a.rows) y[i] = Elt<To>::from_f32(sum[i]);
+      for (int u = 0; u < kOnce; ++u) part[u][wave][lane] = acc[(first + u) / MT][(first + u) % MT];
+      __syncthreads();
+      for (int u = wave; u < kOnce; u += waves) {
+        f32x4_t sum = part[u][0][lane];
+        for (int w = 1; w < waves; ++w) sum += part[u][w][lane];
+        const int32_t r = (blockIdx.x * RT + (first + u) / MT) * 16 + 4 * (lane >> 4);
+        const int64_t p = p0 + 16 * ((first + u) % MT) + (lane & 15);
+        if (p < p1 && r < a.rows)
+          store4_to(static_cast<To*>(a.y) + p * a.rows + r, a.rows - r, a.rows % 4 == 0, sum);
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
-hipError_t launch_f4_matmul(const F4ProdArgs& a, bool is_bf16, hipStream_t s) {
-  if (a.m <= 0 || a.rows <= 0) return hipSuccess;
+namespace {
+
+template <typename To, int RT, int MT>
+void run(const F4ProdArgs& a, const dim3& grid, const dim3& block, hipStream_t s) {
+  if (a.cols % 8 == 0)
+    hipLaunchKernelGGL((k_f4_matmul<To, RT, MT, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_f4_matmul<To, RT, MT, false>), grid, block, 0, s, a);
+}
+
+template <typename To>
+hipError_t run(const F4ProdArgs& a, hipStream_t s) {
   const int64_t most = a.active != nullptr ? (a.m < a.experts ? a.m : a.experts) : 1;
-  const dim3 grid(a.rtiles, static_cast<uint32_t>(most)), block(64 * kF4Waves);
-  const bool vec = a.cols % 8 == 0;
-  if (is_bf16) {
-    if (vec)
-      hipLaunchKernelGGL((k_f4_matmul<uint16_t, true>), grid, block, 0, s, a);
+  const int32_t quads = (a.ktiles + 3) / 4;
+  const int32_t per = (quads + kF4Waves - 1) / kF4Waves;
+  const dim3 block(quads > 0 ? 64 * ((quads + per - 1) / per) : 64);
+  const int64_t each = (a.m + most - 1) / most;
+  const int rt = most * a.rtiles >= 2048 ? 4 : most * a.rtiles >= 1024 ? 2 : 1;
+  const dim3 grid((a.rtiles + rt - 1) / rt, static_cast<uint32_t>(most));
+  if (each > 12) {
+    if (rt == 4)
+      run<To, 4, 4>(a, grid, block, s);
+    else if (rt == 2)
+      run<To, 2, 4>(a, grid, block, s);
     else
-      hipLaunchKernelGGL((k_f4_matmul<uint16_t, false>), grid, block, 0, s, a);
+      run<To, 1, 4>(a, grid, block, s);
+  } else if (rt == 4) {
+    run<To, 4, 1>(a, grid, block, s);
+  } else if (rt == 2) {
+    run<To, 2, 1>(a, grid, block, s);
   } else {
-    if (vec)
-      hipLaunchKernelGGL((k_f4_matmul<float, true>), grid, block, 0, s, a);
-    else
-      hipLaunchKernelGGL((k_f4_matmul<float, false>), grid, block, 0, s, a);
+    run<To, 1, 1>(a, grid, block, s);
   }
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_f4_matmul(const F4ProdArgs& a, bool is_bf16, hipStream_t s) {
+  if (a.m <= 0 || a.rows <= 0) return hipSuccess;
+  return is_bf16 ? run<uint16_t>(a, s) : run<float>(a, s);
 }
 
 }  // namespace muon
