@@ -9,13 +9,20 @@
 //
 // Bound by the weights' bytes.  The waves of a block share the contracted side of
 // one tile row; their sums are joined in a fixed order through LDS.
+#include <algorithm>
+
 #include "device_common.hpp"
 
 namespace muon {
 
 namespace {
 
-constexpr int kF4Waves = 8;
+constexpr int kF4Waves = 4;  // of a block, 8 where 8 share the columns
+constexpr int kF4MaxSplit = 8;
+// Most rows of an expert, on average, of the kernel without LDS.
+constexpr int64_t kF4FewRows = 16;
+// Waves that keep the memory busy.
+constexpr int64_t kF4Busy = 2048;
 
 // The bf16 pairs that a word of four bytes stands for.
 __device__ __forceinline__ bf16x8_t weights8(uint32_t q, float scale) {
@@ -27,15 +34,18 @@ __device__ __forceinline__ bf16x8_t weights8(uint32_t q, float scale) {
   return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// 2^(byte - 127); byte 255 is a NaN.
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-  return __uint_as_float(byte == 255u ? 0x7fc00000u : byte << 23);
+// 2^(byte - 127) of byte g of a word, by its exponent alone; the conversions make
+// NaN of the exponent 255.
+__device__ __forceinline__ float scale_of(uint32_t word, int g) {
+  return __uint_as_float(g == 3 ? word >> 24 << 23 : (word >> (8 * g) & 255u) << 23);
 }
 
-// Eight values of a row from column k on, zero past its end.
+// Eight values of a row from column k on, zero past its end.  whole (uniform): the
+// wave's columns are all there.
 template <bool VEC>
-__device__ __forceinline__ bf16x8_t row8(const uint16_t* x, int32_t k, int32_t cols) {
+__device__ __forceinline__ bf16x8_t row8(const uint16_t* x, int32_t k, int32_t cols, bool whole) {
   if constexpr (VEC) {
+    if (whole) return __builtin_bit_cast(bf16x8_t, ld16(x + k));
     u32x4_t v = {0, 0, 0, 0};
     if (k < cols) v = ld16(x + k);
     return __builtin_bit_cast(bf16x8_t, v);
@@ -68,148 +78,353 @@ __device__ __forceinline__ void store4_to(To* y, int32_t left, bool whole, const
   }
 }
 
-// What a wave reads of RT tile rows over four tiles (512 columns).
-template <int RT>
-struct Quad {
-  u32x4_t w[4][RT];
-  u32x4_t s[RT];
-};
+}  // namespace
 
-template <int RT>
-__device__ __forceinline__ void load_quad(const F4ProdArgs& a, const char* const (&q)[RT],
-                                          const char* const (&s)[RT], int32_t quad, Quad<RT>& to) {
+namespace {
+
+// What a wave of the kernel below holds: RT strips of 16 weight rows, and 16 rows of
+// x, of which this lane has one.  A ring of four tiles of weights and scales, and of
+// two of x, is in flight.
+template <int RT, bool VEC>
+struct Strips {
+  const char *q[RT], *s[RT];  // uniform
+  uint32_t qat, sat;          // this lane's bytes of a tile, of four tiles' scales
+  const uint16_t* x;
+  int32_t cols, kc;
+  u32x4_t w[4][RT];
+  u32x2_t sc[2][RT];          // of an even tile and the one after it
+  bf16x8_t b[2][4];
+  f32x4_t acc[RT];
+
+  __device__ __forceinline__ void load_w(int u, int32_t t) {
 #pragma unroll
-  for (int i = 0; i < RT; ++i) to.s[i] = ld16(s[i] + static_cast<int64_t>(quad) * 256);
+    for (int i = 0; i < RT; ++i) w[u][i] = ld16_nt(q[i] + static_cast<int64_t>(t) * 1024 + qat);
+  }
+  __device__ __forceinline__ void load_s(int h, int32_t t) {  // t even, h = t / 2 % 2
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int32_t t = 4 * quad + j;
+    for (int i = 0; i < RT; ++i)
+      sc[h][i] = *(const GLOBAL_AS u32x2_t*)(s[i] + static_cast<int64_t>(t) * 64 + (h ? 8 - 128 : 0) + sat);
+  }
+  __device__ __forceinline__ void load_x(int v, int32_t t) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) b[v][g] = row8<true>(x, t * kF4Tile + 32 * g + kc, cols, true);
+  }
+  __device__ __forceinline__ void multiply(int u) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            weights8(w[u][i][g], scale_of(sc[u / 2][i][u % 2], g)), b[u % 2][g], acc[i], 0, 0, 0);
+      // the scheduler would convert everything first, and spill
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  __device__ __forceinline__ void begin(int32_t t) {
+    load_s(0, t);
+    load_s(1, t + 2);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_w(u, t + u);
+  }
+  // Four tiles from t on; MORE: the next four are asked for.
+  template <bool MORE>
+  __device__ __forceinline__ void quad(int32_t t) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (MORE || u < 3) load_x(1 - u % 2, t + u + 1);
+      multiply(u);
+      if (MORE) load_w(u, t + u + 4);
+      if (MORE && u % 2 == 1) load_s(u / 2, t + u + 3);
+    }
+  }
+  // One tile, which may lie partly past the columns.
+  __device__ __forceinline__ void tile(int32_t t) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      to.w[j][i] = u32x4_t{0, 0, 0, 0};
-      if (t < a.ktiles) to.w[j][i] = ld16(q[i] + static_cast<int64_t>(t) * 1024);
+      w[0][i] = ld16_nt(q[i] + static_cast<int64_t>(t) * 1024 + qat);
+      sc[0][i][0] = *(const GLOBAL_AS uint32_t*)(s[i] + static_cast<int64_t>(t / 4) * 256 + t % 4 * 4 + sat);
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) b[0][g] = row8<VEC>(x, t * kF4Tile + 32 * g + kc, cols, false);
+    multiply(0);
+  }
+};
+
+}  // namespace
+
+// A wave sums RT tile rows times 16 rows of x over its share of the columns: the
+// block's waves are `ksplit` shares of the columns times groups of RT tile rows.
+template <typename To, int RT, bool VEC>
+__global__ __launch_bounds__(64 * kF4MaxSplit, 2) void k_f4_matmul(F4ProdArgs a) {
+  __shared__ __attribute__((aligned(16))) f32x4_t part[RT][kF4MaxSplit][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ks = wave % a.ksplit, rs = wave / a.ksplit;
+  int32_t e = 0;
+  int64_t p0 = 0, p1 = a.m;
+  if (a.active != nullptr) {
+    e = load_const(a.active + 1 + blockIdx.y);  // with the next load: one wait for both
+    if (static_cast<int32_t>(blockIdx.y) >= load_const(a.active)) return;
+    if (e < 0 || e >= a.experts) return;
+  }
+  const int32_t quads = (a.ktiles + 3) / 4;
+  const int32_t strip0 = (blockIdx.x * ((blockDim.x >> 6) / a.ksplit) + rs) * RT;
+  Strips<RT, VEC> z;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    // strips past the last take that one's place: their results are not stored
+    const int64_t strip = static_cast<int64_t>(e) * a.rtiles + min(strip0 + i, a.rtiles - 1);
+    z.q[i] = a.q + strip * a.ktiles * 1024;
+    z.s[i] = a.s + strip * quads * 256;
+  }
+  z.qat = lane * 16;
+  z.sat = (lane & 15) * 16;
+  z.cols = a.cols;
+  z.kc = 8 * (lane >> 4);
+  // tiles t0 .. t1 - 1, whole quads of them up to tq
+  const int32_t t0 = quads * ks / a.ksplit * 4, t1 = min(quads * (ks + 1) / a.ksplit * 4, a.ktiles);
+  const int32_t tq = VEC ? max(t0, min(quads * (ks + 1) / a.ksplit, a.cols / (4 * kF4Tile)) * 4) : t0;
+  if (tq > t0) z.begin(t0);  // the weights are on their way before the rows are known
+  if (a.active != nullptr) {
+    p0 = max(load_const(a.offsets + e), 0);
+    p1 = min(static_cast<int64_t>(load_const(a.offsets + e + 1)), a.m);
+  }
+  for (; p0 < p1; p0 += 16) {
+    // lanes past the last row take that row's: their results are not stored
+    int64_t row = min(p0 + (lane & 15), p1 - 1);
+    if (a.slots != nullptr) {
+      row = a.slots[row] / a.top_k;
+      if (row < 0 || row >= a.x_rows) row = 0;
+    }
+    z.x = static_cast<const uint16_t*>(a.x) + row * a.cols;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) z.acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (tq > t0) {
+      z.load_x(0, t0);
+      int32_t t = t0;
+      for (; t + 4 < tq; t += 4) z.template quad<true>(t);
+      z.template quad<false>(t);
+    }
+    for (int32_t t = tq; t < t1; ++t) z.tile(t);
+    if (a.ksplit > 1) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) part[i][wave][lane] = z.acc[i];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      if (a.ksplit > 1) {
+        // each of the waves that share these rows stores some of them
+        if (i % a.ksplit != ks) continue;
+        z.acc[i] = part[i][rs * a.ksplit][lane];
+        for (int k = 1; k < a.ksplit; ++k) z.acc[i] += part[i][rs * a.ksplit + k][lane];
+      }
+      const int32_t r = (strip0 + i) * 16 + 4 * (lane >> 4);
+      const int64_t p = p0 + (lane & 15);
+      if (p < p1 && r < a.rows)
+        store4_to(static_cast<To*>(a.y) + p * a.rows + r, a.rows - r, a.rows % 4 == 0, z.acc[i]);
+    }
+    if (p0 + 16 < p1) {
+      if (a.ksplit > 1) __syncthreads();
+      if (tq > t0) z.begin(t0);
     }
   }
 }
 
+// The same for experts of many rows: 64 rows of x at a time go through LDS, a tile's
+// columns after the other, and serve every wave of the block.  Four waves take RT
+// strips each, `ksplit` (1 or 2) groups of four a share of the columns each.
+namespace {
+constexpr int kManyRows = 64;
+constexpr int kManyTile = kManyRows * kF4Tile * 2;  // bytes of x
 }  // namespace
 
-// A wave sums RT tile rows times MT * 16 rows of x over its share of the columns.
-template <typename To, int RT, int MT, bool VEC>
-__global__ __launch_bounds__(64 * kF4Waves) void k_f4_matmul(F4ProdArgs a) {
-  constexpr int kOnce = RT * MT < 4 ? RT * MT : 4;  // result tiles joined at a time
-  __shared__ __attribute__((aligned(16))) f32x4_t part[kOnce][kF4Waves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int waves = blockDim.x >> 6;
+template <typename To, int RT, int KS, bool VEC>
+__global__ __launch_bounds__(256 * KS, 2) void k_f4_many(F4ProdArgs a) {
+  constexpr int MT = kManyRows / 16;
+  // [group][buffer][row][16 bytes of 8 columns at chunk ^ row % 16], then the sums
+  __shared__ __attribute__((aligned(16))) char xs[KS][2][kManyTile];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ks = wave / 4, rs = wave % 4;
   int32_t e = 0;
   int64_t p0 = 0, p1 = a.m;
   if (a.active != nullptr) {
-    if (static_cast<int32_t>(blockIdx.y) >= a.active[0]) return;
-    e = a.active[1 + blockIdx.y];
+    e = load_const(a.active + 1 + blockIdx.y);
+    if (static_cast<int32_t>(blockIdx.y) >= load_const(a.active)) return;
     if (e < 0 || e >= a.experts) return;
-    p0 = max(a.offsets[e], 0);
-    p1 = min(static_cast<int64_t>(a.offsets[e + 1]), a.m);
+    p0 = max(load_const(a.offsets + e), 0);
+    p1 = min(static_cast<int64_t>(load_const(a.offsets + e + 1)), a.m);
   }
   const int32_t quads = (a.ktiles + 3) / 4;
+  const int32_t strip0 = (blockIdx.x * 4 + rs) * RT;
   const char *q[RT], *s[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
-    // strips past the last take that one's place: their results are not stored
-    const int64_t strip = static_cast<int64_t>(e) * a.rtiles +
-                          min(static_cast<int32_t>(blockIdx.x) * RT + i, a.rtiles - 1);
-    q[i] = a.q + (strip * a.ktiles * 64 + lane) * 16;
-    s[i] = a.s + (strip * quads * 16 + (lane & 15)) * 16;
+    const int64_t strip = static_cast<int64_t>(e) * a.rtiles + min(strip0 + i, a.rtiles - 1);
+    q[i] = a.q + strip * a.ktiles * 1024;
+    s[i] = a.s + strip * quads * 256;
   }
-  const int32_t q0 = quads * wave / waves, q1 = quads * (wave + 1) / waves;
-  const int32_t kc = 8 * (lane >> 4);
-  for (; p0 < p1; p0 += 16 * MT) {
-    const uint16_t* x[MT];
+  const uint32_t qat = lane * 16, sat = (lane & 15) * 16;
+  const int32_t t0 = a.ktiles * ks / KS, t1 = a.ktiles * (ks + 1) / KS;
+  const int32_t steps = (a.ktiles + KS - 1) / KS;  // of the longest share
+  const int at = threadIdx.x & 255, chunk = at & 15;
+  for (p0 += static_cast<int64_t>(blockIdx.z) * kManyRows; p0 < p1;
+       p0 += static_cast<int64_t>(gridDim.z) * kManyRows) {
+    const uint16_t* x[4];
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      // lanes past the last row take that row's: their results are not stored
-      int64_t row = min(p0 + 16 * j + (lane & 15), p1 - 1);
+    for (int j = 0; j < 4; ++j) {
+      int64_t row = min(p0 + 16 * j + (at >> 4), p1 - 1);
       if (a.slots != nullptr) {
         row = a.slots[row] / a.top_k;
         if (row < 0 || row >= a.x_rows) row = 0;
       }
       x[j] = static_cast<const uint16_t*>(a.x) + row * a.cols;
     }
+    u32x4_t w[4][RT], xr[4];
+    uint32_t sc[4][RT];
     f32x4_t acc[RT][MT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int32_t quad = q0; quad < q1; ++quad) {
-      Quad<RT> w;
-      load_quad<RT>(a, q, s, quad, w);
+    // tiles past the share's last are that one again; they are not multiplied
+    auto load_w = [&](int u, int32_t t) {
+      t = min(t, t1 - 1);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int i = 0; i < RT; ++i) {
+        w[u][i] = ld16(q[i] + static_cast<int64_t>(t) * 1024 + qat);
+        sc[u][i] = *(const GLOBAL_AS uint32_t*)(s[i] + static_cast<int64_t>(t / 4) * 256 + t % 4 * 4 + sat);
+      }
+    };
+    auto load_x = [&](int32_t t) {
+      t = min(t, t1 - 1);
+      const bool whole = (t + 1) * kF4Tile <= a.cols;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          bf16x8_t b[MT];
+      for (int j = 0; j < 4; ++j)
+        xr[j] = __builtin_bit_cast(u32x4_t, row8<VEC>(x[j], t * kF4Tile + 8 * chunk, a.cols, whole));
+    };
+    if (t0 < t1) {
+      load_x(t0);
 #pragma unroll
-          for (int j = 0; j < MT; ++j)
-            b[j] = row8<VEC>(x[j], quad * 512 + t * kF4Tile + 32 * g + kc, a.cols);
+      for (int u = 0; u < 4; ++u) load_w(u, t0 + u);
+    }
+    for (int32_t n = 0; n < steps; n += 4) {
 #pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const bf16x8_t v = weights8(w.w[t][i][g], scale_of(w.s[i][t] >> (8 * g) & 255u));
+      for (int u = 0; u < 4; ++u) {
+        if (n + u >= steps) break;
+        const int32_t t = t0 + n + u;
+        char* const buf = xs[ks][u & 1];
 #pragma unroll
-            for (int j = 0; j < MT; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+          const int r = 16 * j + (at >> 4);
+          *reinterpret_cast<u32x4_t*>(buf + r * 256 + ((chunk ^ (r & 15)) << 4)) = xr[j];
+        }
+        if (t + 1 < t1) load_x(t + 1);
+        // the buffer's readers of two steps ago have passed this barrier since
+        __syncthreads();
+        if (t < t1) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            bf16x8_t b[MT];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              const int r = lane & 15;
+              b[j] = *reinterpret_cast<const bf16x8_t*>(buf + (16 * j + r) * 256 +
+                                                        (((4 * g + (lane >> 4)) ^ r) << 4));
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              const bf16x8_t v = weights8(w[u][i][g], scale_of(sc[u][i], g));
+#pragma unroll
+              for (int j = 0; j < MT; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[j], acc[i][j], 0, 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
+        if (t0 < t1) load_w(u, t + 4);
       }
     }
+    if constexpr (KS == 2) {
+      // the second share's sums go through LDS, one strip at a time
+      f32x4_t* const part = reinterpret_cast<f32x4_t*>(xs);
 #pragma unroll
-    for (int first = 0; first < RT * MT; first += kOnce) {
+      for (int i = 0; i < RT; ++i) {
+        __syncthreads();
+        if (ks == 1)
 #pragma unroll
-      for (int u = 0; u < kOnce; ++u) part[u][wave][lane] = acc[(first + u) / MT][(first + u) % MT];
-      __syncthreads();
-      for (int u = wave; u < kOnce; u += waves) {
-        f32x4_t sum = part[u][0][lane];
-        for (int w = 1; w < waves; ++w) sum += part[u][w][lane];
-        const int32_t r = (blockIdx.x * RT + (first + u) / MT) * 16 + 4 * (lane >> 4);
-        const int64_t p = p0 + 16 * ((first + u) % MT) + (lane & 15);
-        if (p < p1 && r < a.rows)
-          store4_to(static_cast<To*>(a.y) + p * a.rows + r, a.rows - r, a.rows % 4 == 0, sum);
+          for (int j = 0; j < MT; ++j) part[(rs * MT + j) * 64 + lane] = acc[i][j];
+        __syncthreads();
+        if (ks == 0)
+#pragma unroll
+          for (int j = 0; j < MT; ++j) acc[i][j] += part[(rs * MT + j) * 64 + lane];
       }
-      __syncthreads();
     }
+    if (ks == 0) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const int32_t r = (strip0 + i) * 16 + 4 * (lane >> 4);
+          const int64_t p = p0 + 16 * j + (lane & 15);
+          if (p < p1 && r < a.rows)
+            store4_to(static_cast<To*>(a.y) + p * a.rows + r, a.rows - r, a.rows % 4 == 0, acc[i][j]);
+        }
+    }
+    __syncthreads();  // before the next rows' first buffer
   }
 }
 
 namespace {
 
-template <typename To, int RT, int MT>
-void run(const F4ProdArgs& a, const dim3& grid, const dim3& block, hipStream_t s) {
+template <typename To, int RT>
+void run(const F4ProdArgs& a, int64_t experts, hipStream_t s) {
+  const int waves = std::max(kF4Waves, a.ksplit), strips = waves / a.ksplit * RT;
+  const dim3 grid((a.rtiles + strips - 1) / strips, static_cast<uint32_t>(experts));
+  const dim3 block(64 * waves);
   if (a.cols % 8 == 0)
-    hipLaunchKernelGGL((k_f4_matmul<To, RT, MT, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_f4_matmul<To, RT, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((k_f4_matmul<To, RT, MT, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_f4_matmul<To, RT, false>), grid, block, 0, s, a);
+}
+
+template <typename To, int RT, int KS>
+void run_many(const F4ProdArgs& a, int64_t experts, int64_t passes, hipStream_t s) {
+  const dim3 grid((a.rtiles + 4 * RT - 1) / (4 * RT), static_cast<uint32_t>(experts),
+                  static_cast<uint32_t>(passes));
+  if (a.cols % 8 == 0)
+    hipLaunchKernelGGL((k_f4_many<To, RT, KS, true>), grid, dim3(256 * KS), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_f4_many<To, RT, KS, false>), grid, dim3(256 * KS), 0, s, a);
 }
 
 template <typename To>
-hipError_t run(const F4ProdArgs& a, hipStream_t s) {
+hipError_t run(F4ProdArgs a, hipStream_t s) {
   const int64_t most = a.active != nullptr ? (a.m < a.experts ? a.m : a.experts) : 1;
-  const int32_t quads = (a.ktiles + 3) / 4;
-  const int32_t per = (quads + kF4Waves - 1) / kF4Waves;
-  const dim3 block(quads > 0 ? 64 * ((quads + per - 1) / per) : 64);
+  const int64_t strips = most * a.rtiles;
   const int64_t each = (a.m + most - 1) / most;
-  const int rt = most * a.rtiles >= 2048 ? 4 : most * a.rtiles >= 1024 ? 2 : 1;
-  const dim3 grid((a.rtiles + rt - 1) / rt, static_cast<uint32_t>(most));
-  if (each > 12) {
-    if (rt == 4)
-      run<To, 4, 4>(a, grid, block, s);
-    else if (rt == 2)
-      run<To, 2, 4>(a, grid, block, s);
+  if (each > kF4FewRows) {
+    const int64_t passes = std::min<int64_t>((each + kManyRows - 1) / kManyRows, 65535);
+    if (strips * passes >= 8 * 512)
+      run_many<To, 2, 1>(a, most, passes, s);
+    else if (strips * passes >= 4 * 512)
+      run_many<To, 1, 1>(a, most, passes, s);
     else
-      run<To, 1, 4>(a, grid, block, s);
-  } else if (rt == 4) {
-    run<To, 4, 1>(a, grid, block, s);
-  } else if (rt == 2) {
-    run<To, 2, 1>(a, grid, block, s);
-  } else {
-    run<To, 1, 1>(a, grid, block, s);
+      run_many<To, 1, 2>(a, most, passes, s);
+    return hipGetLastError();
   }
+  const int32_t quads = (a.ktiles + 3) / 4;
+  const int64_t most_split = std::min<int64_t>(kF4MaxSplit, quads);
+  const int rt = strips * most_split >= 8 * kF4Busy ? 4 : strips * most_split >= kF4Busy ? 2 : 1;
+  a.ksplit = 1;
+  while (a.ksplit < kF4MaxSplit && 2 * a.ksplit <= quads && strips / rt * a.ksplit < kF4Busy) a.ksplit *= 2;
+  if (rt == 4)
+    run<To, 4>(a, most, s);
+  else if (rt == 2)
+    run<To, 2>(a, most, s);
+  else
+    run<To, 1>(a, most, s);
   return hipGetLastError();
 }
 

@@ -341,6 +341,7 @@ struct F4ProdArgs {
   int64_t m, x_rows;
   int32_t experts, rows, cols, top_k;
   int32_t rtiles, ktiles;
+  int32_t ksplit;          // waves of a block that share the columns (set by the launch)
 };
 hipError_t launch_f4_matmul(const F4ProdArgs& a, bool is_bf16, hipStream_t s);
 

@@ -146,16 +146,20 @@ def test_experts(tokens, top_k, experts, rows, cols, dtype):
         assert nsa.f4_matmul(xs, op, plan=plan, out=y) is y
         nsa.f4_matmul(x, op, plan=plan, gather=True, out=y2)
         assert torch.equal(y, y2) and bool((y[n:] == 7).all())
-        for e in range(experts):
-            a, b = offsets[e], offsets[e + 1]
-            if a < b:
-                check(y[a:b], host_f64(x)[slots[a:b] // top_k], ws[e], dtype)
-        # fewer rows: those of xs, and of a smaller out
+        def check_rows(y, n):
+            for e in range(experts):
+                a, b = offsets[e], min(offsets[e + 1], n)
+                if a < b:
+                    check(y[a:b], host_f64(x)[slots[a:b] // top_k], ws[e], dtype)
+
+        check_rows(y, n)
+        # fewer rows: those of xs, and of a smaller out (the order of the sums may be another)
         if n > 1:
-            assert torch.equal(nsa.f4_matmul(xs[:n - 1].contiguous(), op, plan=plan, out_dtype=dtype), y[:n - 1])
+            check_rows(nsa.f4_matmul(xs[:n - 1].contiguous(), op, plan=plan, out_dtype=dtype), n - 1)
             few = torch.full((n, rows), 7.0, dtype=dtype, device="cuda")
             nsa.f4_matmul(x, op, plan=plan, gather=True, out=few[:n - 1])
-            assert torch.equal(few[:n - 1], y[:n - 1]) and bool((few[n - 1] == 7).all())
+            check_rows(few, n - 1)
+            assert bool((few[n - 1] == 7).all())
 
 
 def test_every_code_scale_and_place():
