@@ -7,8 +7,15 @@
 // (v_cvt_scalef32_pk_bf16_fp4), and four 16x16x32 matrix instructions take a tile
 // of 16 weight rows x 128 columns times up to 16 rows of x.
 //
-// Bound by the weights' bytes.  The waves of a block share the contracted side of
-// one tile row; their sums are joined in a fixed order through LDS.
+// Bound by the weights' bytes: 264 experts of 6144 x 2048 with 3.9 rows each on
+// average take 298 us, 5.9 TB/s, where nothing but the loads of the weights
+// reaches 7.0 in this order and with those of the scales and one row of x 6.5.
+// What it took: one weight tile is 1024 bytes in a row, so that a wave's load is;
+// a wave takes RT strips of 16 rows, since every one of them needs the same x (RT
+// 1: 400 us, the loads of x are the bound); a ring of tiles in registers that is
+// refilled as it is used, without conditions, which cost registers for copies (400
+// us with them: one wave a SIMD); two waves a SIMD that do not spill (three that
+// do: 380).
 #include <algorithm>
 
 #include "device_common.hpp"
@@ -231,9 +238,9 @@ __global__ __launch_bounds__(64 * kF4MaxSplit, 2) void k_f4_matmul(F4ProdArgs a)
   }
 }
 
-// The same for experts of many rows: 64 rows of x at a time go through LDS, a tile's
+// The same for experts of many rows: 64 rows of x at a time go through LDS, one tile's
 // columns after the other, and serve every wave of the block.  Four waves take RT
-// strips each, `ksplit` (1 or 2) groups of four a share of the columns each.
+// strips each, KS groups of four a share of the columns each.
 namespace {
 constexpr int kManyRows = 64;
 constexpr int kManyTile = kManyRows * kF4Tile * 2;  // bytes of x
@@ -268,6 +275,9 @@ __global__ __launch_bounds__(256 * KS, 2) void k_f4_many(F4ProdArgs a) {
   const uint32_t qat = lane * 16, sat = (lane & 15) * 16;
   const int32_t t0 = a.ktiles * ks / KS, t1 = a.ktiles * (ks + 1) / KS;
   const int32_t steps = (a.ktiles + KS - 1) / KS;  // of the longest share
+  // steps whose tiles are whole in every share, in fours
+  const int32_t whole =
+      VEC ? min(a.ktiles / KS, a.cols / kF4Tile - a.ktiles * (KS - 1) / KS) / 4 * 4 : 0;
   const int at = threadIdx.x & 255, chunk = at & 15;
   for (p0 += static_cast<int64_t>(blockIdx.z) * kManyRows; p0 < p1;
        p0 += static_cast<int64_t>(gridDim.z) * kManyRows) {
@@ -279,72 +289,87 @@ __global__ __launch_bounds__(256 * KS, 2) void k_f4_many(F4ProdArgs a) {
         row = a.slots[row] / a.top_k;
         if (row < 0 || row >= a.x_rows) row = 0;
       }
-      x[j] = static_cast<const uint16_t*>(a.x) + row * a.cols;
+      x[j] = static_cast<const uint16_t*>(a.x) + row * a.cols + 8 * chunk;
     }
-    u32x4_t w[4][RT], xr[4];
+    u32x4_t w[4][RT], xr[2][4];
     uint32_t sc[4][RT];
     f32x4_t acc[RT][MT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // tiles past the share's last are that one again; they are not multiplied
     auto load_w = [&](int u, int32_t t) {
-      t = min(t, t1 - 1);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         w[u][i] = ld16(q[i] + static_cast<int64_t>(t) * 1024 + qat);
         sc[u][i] = *(const GLOBAL_AS uint32_t*)(s[i] + static_cast<int64_t>(t / 4) * 256 + t % 4 * 4 + sat);
       }
     };
-    auto load_x = [&](int32_t t) {
-      t = min(t, t1 - 1);
-      const bool whole = (t + 1) * kF4Tile <= a.cols;
+    auto load_x = [&](int v, int32_t t) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        xr[j] = __builtin_bit_cast(u32x4_t, row8<VEC>(x[j], t * kF4Tile + 8 * chunk, a.cols, whole));
+      for (int j = 0; j < 4; ++j) xr[v][j] = ld16(x[j] + t * kF4Tile);
     };
-    if (t0 < t1) {
-      load_x(t0);
+    auto store_x = [&](char* buf, int v) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 16 * j + (at >> 4);
+        *reinterpret_cast<u32x4_t*>(buf + r * 256 + ((chunk ^ (r & 15)) << 4)) = xr[v][j];
+      }
+    };
+    // x of the next group of 32 columns is read while this one's is multiplied
+    auto read_b = [&](const char* buf, int g, bf16x8_t (&b)[MT]) {
+      const int r = lane & 15;
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+        b[j] = *reinterpret_cast<const bf16x8_t*>(buf + (16 * j + r) * 256 +
+                                                  (((4 * g + (lane >> 4)) ^ r) << 4));
+    };
+    auto multiply = [&](const char* buf, int u) {
+      bf16x8_t b[2][MT];
+      read_b(buf, 0, b[0]);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (g < 3) read_b(buf, g + 1, b[(g + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const bf16x8_t v = weights8(w[u][i][g], scale_of(sc[u][i], g));
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[g & 1][j], acc[i][j], 0, 0, 0);
+        }
+      }
+    };
+    if (whole > 0) {
+      load_x(0, t0);
+      load_x(1, t0 + 1);
 #pragma unroll
       for (int u = 0; u < 4; ++u) load_w(u, t0 + u);
-    }
-    for (int32_t n = 0; n < steps; n += 4) {
+      const int32_t last = t0 + whole - 1;  // asked for again where there is no next one
+      for (int32_t t = t0; t <= last; t += 4) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (n + u >= steps) break;
-        const int32_t t = t0 + n + u;
-        char* const buf = xs[ks][u & 1];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 16 * j + (at >> 4);
-          *reinterpret_cast<u32x4_t*>(buf + r * 256 + ((chunk ^ (r & 15)) << 4)) = xr[j];
+        for (int u = 0; u < 4; ++u) {
+          store_x(xs[ks][u & 1], u & 1);
+          load_x(u & 1, min(t + u + 2, last));
+          // who read this buffer two steps ago has passed a barrier since
+          __syncthreads();
+          multiply(xs[ks][u & 1], u);
+          load_w(u, min(t + u + 4, last));
         }
-        if (t + 1 < t1) load_x(t + 1);
-        // the buffer's readers of two steps ago have passed this barrier since
-        __syncthreads();
-        if (t < t1) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            bf16x8_t b[MT];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-              const int r = lane & 15;
-              b[j] = *reinterpret_cast<const bf16x8_t*>(buf + (16 * j + r) * 256 +
-                                                        (((4 * g + (lane >> 4)) ^ r) << 4));
-            }
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-              const bf16x8_t v = weights8(w[u][i][g], scale_of(sc[u][i], g));
-#pragma unroll
-              for (int j = 0; j < MT; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[j], acc[i][j], 0, 0, 0);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        }
-        if (t0 < t1) load_w(u, t + 4);
       }
+    }
+    for (int32_t n = whole; n < steps; ++n) {
+      const int32_t t = t0 + n;
+      __syncthreads();
+      if (t < t1) {
+        load_w(0, t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          xr[0][j] = __builtin_bit_cast(
+              u32x4_t, row8<VEC>(x[j] - 8 * chunk, t * kF4Tile + 8 * chunk, a.cols, false));
+        store_x(xs[ks][0], 0);
+      }
+      __syncthreads();
+      if (t < t1) multiply(xs[ks][0], 0);
     }
     if constexpr (KS == 2) {
       // the second share's sums go through LDS, one strip at a time

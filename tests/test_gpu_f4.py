@@ -108,7 +108,7 @@ def check(y, x, w, dtype):
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (5, 7), (16, 8), (17, 31), (31, 32), (64, 100), (48, 127), (130, 128),
                                        (33, 129), (40, 500), (16, 512), (96, 520), (257, 1000), (300, 1024),
-                                       (2048, 2048), (256, 6144), (100, 8193)])
+                                       (2048, 2048), (256, 6144), (100, 8193), (64, 896), (40, 1408), (33, 2560)])
 def test_one_matrix(rows, cols, dtype):
     op, (w,) = operand(1, rows, cols, rows + cols)
     for m in (1, 2, 3, 4, 5, 8, 15, 16, 17, 31, 33, 48, 64, 65, 130):
