@@ -153,7 +153,7 @@ extern "C" int32_t muon_moe_dispatch(int64_t tokens, int32_t top_k, int64_t cols
     a.out = out;
     hipStream_t s = static_cast<hipStream_t>(stream);
     TimedLaunch tl(MUON_K_MOE_DISPATCH, s);
-    return launched(tl, launch_moe_dispatch(a, s), "launch dispatch");
+    return launched(tl, launch_moe_dispatch(a, dtype == MUON_BF16, s), "launch dispatch");
   } catch (...) {
     return fail(MUON_ERR_HIP, "unexpected host exception");
   }

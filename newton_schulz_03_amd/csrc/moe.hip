@@ -11,11 +11,20 @@
 // Nothing depends on the order in which blocks or waves run: equal calls give
 // equal bits.
 //
+// Dispatch, combine and its gradient are bound by the rows' bytes: a token's row is
+// read once, the rows of up to kBatch of its slots are asked for (or stored)
+// together.  4096 tokens x 8 x 6144 bf16: 78, 82 and 160 us (5.8, 5.5 and 5.3 TB/s; a slot
+// after the other, 92, 98 and 184).  Rows whose length is no multiple of 16 bytes are
+// read and written 16 bytes at a time all the same, at element-aligned addresses
+// (16384 x 4 x 1001 bf16: 30, 32 and 58 us; by elements 34, 60 and 121).
+//
 // The sort: up to kSortFew slots in a kernel that compares all of them (8 slots of
 // 384 experts: 2.2 us, the next one 6.6), up to kSortPiece in one block, more in
 // two launches, counts and rows (524288 slots of 8 bytes, 384 experts: 3.2 + 13.2 us;
 // one block for all of them took 880).  Pieces of 2048 slots: 22 us for the rows, since
 // every block adds up the counts of twice as many.
+#include <type_traits>
+
 #include "device_common.hpp"
 
 namespace muon {
@@ -239,115 +248,194 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(MoeSortArgs a) {
 
 namespace {
 
-// A row in pieces of V bytes, the widest that its length allows.
-template <int V> struct Piece;
-template <> struct Piece<16> { typedef u32x4_t type; };
-template <> struct Piece<8> { typedef u32x2_t type; };
-template <> struct Piece<4> { typedef uint32_t type; };
-template <> struct Piece<2> { typedef uint16_t type; };
+// A piece of V bytes of a row: 16, whose address is a multiple of A, or one element.
+typedef u32x4_t u32x4_at4_t __attribute__((aligned(4)));
+typedef u32x4_t u32x4_at2_t __attribute__((aligned(2)));
+template <int V, int A> struct Piece { typedef u32x4_t type; };
+template <> struct Piece<16, 4> { typedef u32x4_at4_t type; };
+template <> struct Piece<16, 2> { typedef u32x4_at2_t type; };
+template <int A> struct Piece<4, A> { typedef uint32_t type; };
+template <int A> struct Piece<2, A> { typedef uint16_t type; };
 
-template <int V>
-__device__ __forceinline__ typename Piece<V>::type ld(const void* p) {
-  return *(const GLOBAL_AS typename Piece<V>::type*)(p);
+template <int V, int A, bool NT>
+__device__ __forceinline__ typename Piece<V, 16>::type ld(const void* p) {
+  const GLOBAL_AS typename Piece<V, A>::type* q = (const GLOBAL_AS typename Piece<V, A>::type*)(p);
+  return NT ? __builtin_nontemporal_load(q) : *q;
 }
-template <int V>
-__device__ __forceinline__ void st(void* p, const typename Piece<V>::type& v) {
-  *(GLOBAL_AS typename Piece<V>::type*)(p) = v;
+template <int V, int A, bool NT>
+__device__ __forceinline__ void st(void* p, const typename Piece<V, 16>::type& v) {
+  GLOBAL_AS typename Piece<V, A>::type* q = (GLOBAL_AS typename Piece<V, A>::type*)(p);
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, q);
+  else
+    *q = v;
 }
 
 // The values of a piece, V / sizeof(T) of them.
 template <typename T, int V>
-__device__ __forceinline__ void unpack(const typename Piece<V>::type& p, float* v) {
-  T x[V / sizeof(T)];
-  __builtin_memcpy(x, &p, V);
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(V / sizeof(T)); ++i) v[i] = Elt<T>::to_f32(x[i]);
+__device__ __forceinline__ void unpack(const typename Piece<V, 16>::type& p, float* v) {
+  if constexpr (V == 16)
+    vec_to_f32<T>(p, v);
+  else
+    v[0] = Elt<T>::to_f32(__builtin_bit_cast(T, p));
 }
 template <typename T, int V>
-__device__ __forceinline__ typename Piece<V>::type pack(const float* v) {
-  T x[V / sizeof(T)];
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(V / sizeof(T)); ++i) x[i] = Elt<T>::from_f32(v[i]);
-  typename Piece<V>::type p;
-  __builtin_memcpy(&p, x, V);
-  return p;
+__device__ __forceinline__ typename Piece<V, 16>::type pack(const float* v) {
+  if constexpr (V == 16)
+    return f32_to_vec<T>(v);
+  else
+    return __builtin_bit_cast(typename Piece<V, 16>::type, Elt<T>::from_f32(v[0]));
 }
 
-__device__ __forceinline__ bool has_row(int row, int64_t rows) {
-  return row >= 0 && row < rows;
+constexpr int kBatch = 8;  // slots whose rows are asked for together
+
+// The sorted rows of slots k .. k + kBatch - 1 of a token, -1 for those that are
+// dropped or past the last slot.  Uniform.
+struct Batch {
+  int32_t row[kBatch];
+  __device__ __forceinline__ Batch(const int32_t* rows, int k, int top_k, int64_t sorted_rows) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      row[j] = load_const(rows + min(k + j, top_k - 1));
+      if (k + j >= top_k || row[j] >= sorted_rows) row[j] = -1;
+    }
+  }
+};
+
+// This wave's token, or -1: a block takes one token (W = 4 waves) or one a wave.
+template <int W>
+__device__ __forceinline__ int64_t token_of(const MoeRowArgs& a) {
+  const int64_t t = W == 1 ? static_cast<int64_t>(blockIdx.x) * (kThreads / 64) +
+                                 __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
+                           : static_cast<int64_t>(blockIdx.x);
+  return t < a.tokens_n ? t : -1;
+}
+template <int W>
+__device__ __forceinline__ int lane_of() {
+  return W == 1 ? threadIdx.x & 63 : threadIdx.x;
+}
+
+// Calls body(offset, V) for this lane's pieces of a row: 16 bytes each, at addresses
+// that are multiples of A, then (A < 16) the last elements, one a lane.
+template <int A, int W, typename F>
+__device__ __forceinline__ void for_pieces(int64_t row_bytes, F body) {
+  for (int64_t i = lane_of<W>() * 16; i + 16 <= row_bytes; i += 64 * W * 16)
+    body(i, std::integral_constant<int, 16>());
+  if constexpr (A < 16) {
+    const int64_t i = row_bytes / 16 * 16 + lane_of<W>() * A;
+    if (i < row_bytes) body(i, std::integral_constant<int, A>());
+  }
 }
 
 }  // namespace
 
-// A block takes one token.
-template <int V>
+// Each piece of the token's row is read once and stored top_k times.
+template <int A, int W, bool NT>
 __global__ __launch_bounds__(kThreads) void k_moe_dispatch(MoeRowArgs a) {
-  const int64_t t = blockIdx.x;
+  const int64_t t = token_of<W>(a);
+  if (t < 0) return;
   const char* const x = static_cast<const char*>(a.tokens) + t * a.row_bytes;
   const int32_t* const rows = a.rows + t * a.top_k;
-  for (int64_t i = static_cast<int64_t>(threadIdx.x) * V; i < a.row_bytes; i += kThreads * V) {
-    const typename Piece<V>::type v = ld<V>(x + i);
-    for (int k = 0; k < a.top_k; ++k)
-      if (has_row(rows[k], a.sorted_rows))
-        st<V>(static_cast<char*>(a.out) + rows[k] * a.row_bytes + i, v);
-  }
-}
-
-template <typename T, int V>
-__global__ __launch_bounds__(kThreads) void k_moe_combine(MoeRowArgs a) {
-  constexpr int kN = V / sizeof(T);
-  const int64_t t = blockIdx.x;
-  const int32_t* const rows = a.rows + t * a.top_k;
-  const float* const w = a.weights + t * a.top_k;
-  for (int64_t i = static_cast<int64_t>(threadIdx.x) * V; i < a.row_bytes; i += kThreads * V) {
-    float acc[kN] = {};
-    for (int k = 0; k < a.top_k; ++k) {
-      if (!has_row(rows[k], a.sorted_rows)) continue;
-      float y[kN];
-      unpack<T, V>(ld<V>(static_cast<const char*>(a.sorted) + rows[k] * a.row_bytes + i), y);
-      const float f = a.weights != nullptr ? w[k] : 1.f;
+  for_pieces<A, W>(a.row_bytes, [&](int64_t i, auto v) {
+    constexpr int V = v();
+    const auto p = ld<V, A, false>(x + i);
+    for (int k = 0; k < a.top_k; k += kBatch) {
+      const Batch b(rows, k, a.top_k, a.sorted_rows);
 #pragma unroll
-      for (int c = 0; c < kN; ++c) acc[c] = __builtin_fmaf(f, y[c], acc[c]);
+      for (int j = 0; j < kBatch; ++j)
+        if (b.row[j] >= 0) st<V, A, NT>(static_cast<char*>(a.out) + b.row[j] * a.row_bytes + i, p);
     }
-    st<V>(static_cast<char*>(a.out) + t * a.row_bytes + i, pack<T, V>(acc));
-  }
+  });
 }
 
-template <typename T, int V>
-__global__ __launch_bounds__(kThreads) void k_moe_backward(MoeRowArgs a) {
-  constexpr int kN = V / sizeof(T);
-  __shared__ float scratch[kThreads / 64];
-  const int64_t t = blockIdx.x;
+template <typename T, int A, int W, bool NT>
+__global__ __launch_bounds__(kThreads) void k_moe_combine(MoeRowArgs a) {
+  const int64_t t = token_of<W>(a);
+  if (t < 0) return;
   const int32_t* const rows = a.rows + t * a.top_k;
-  for (int k = 0; k < a.top_k; ++k) {
-    float dot = 0.f;
-    if (has_row(rows[k], a.sorted_rows)) {
-      const float f = a.weights[t * a.top_k + k];
-      const int64_t at = rows[k] * a.row_bytes;
-      for (int64_t i = static_cast<int64_t>(threadIdx.x) * V; i < a.row_bytes; i += kThreads * V) {
-        float d[kN], y[kN];
-        unpack<T, V>(ld<V>(static_cast<const char*>(a.tokens) + t * a.row_bytes + i), d);
-        unpack<T, V>(ld<V>(static_cast<const char*>(a.sorted) + at + i), y);
+  for_pieces<A, W>(a.row_bytes, [&](int64_t i, auto size) {
+    constexpr int V = size();
+    constexpr int kN = V / sizeof(T);
+    float acc[kN] = {};
+    for (int k = 0; k < a.top_k; k += kBatch) {
+      const Batch b(rows, k, a.top_k, a.sorted_rows);
+      typename Piece<V, 16>::type v[kBatch];
 #pragma unroll
-        for (int c = 0; c < kN; ++c) {
-          dot = __builtin_fmaf(d[c], y[c], dot);
-          d[c] *= f;
-        }
-        st<V>(static_cast<char*>(a.out) + at + i, pack<T, V>(d));
+      for (int j = 0; j < kBatch; ++j)
+        if (b.row[j] >= 0)
+          v[j] = ld<V, A, NT>(static_cast<const char*>(a.sorted) + b.row[j] * a.row_bytes + i);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (b.row[j] < 0) continue;
+        float y[kN];
+        unpack<T, V>(v[j], y);
+        const float f = a.weights != nullptr ? load_const(a.weights + t * a.top_k + k + j) : 1.f;
+#pragma unroll
+        for (int c = 0; c < kN; ++c) acc[c] = __builtin_fmaf(f, y[c], acc[c]);
       }
     }
-    dot = block_sum(dot, scratch);
-    if (threadIdx.x == 0) a.dweights[t * a.top_k + k] = dot;
+    st<V, A, false>(static_cast<char*>(a.out) + t * a.row_bytes + i, pack<T, V>(acc));
+  });
+}
+
+// The products of a token's row with its experts' rows are summed by lanes, then
+// over the wave, then (W = 4) over the waves.
+template <typename T, int A, int W, bool NT>
+__global__ __launch_bounds__(kThreads) void k_moe_backward(MoeRowArgs a) {
+  __shared__ float part[kMoeMaxTopK][kThreads / 64];
+  const int64_t t = token_of<W>(a);
+  if (t < 0) return;  // whole waves; with W = 4 none
+  const int32_t* const rows = a.rows + t * a.top_k;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int k = 0; k < a.top_k; k += kBatch) {
+    const Batch b(rows, k, a.top_k, a.sorted_rows);
+    float dot[kBatch] = {}, f[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      f[j] = b.row[j] >= 0 ? load_const(a.weights + t * a.top_k + k + j) : 0.f;
+    for_pieces<A, W>(a.row_bytes, [&](int64_t i, auto size) {
+      constexpr int V = size();
+      constexpr int kN = V / sizeof(T);
+      const auto dv = ld<V, A, false>(static_cast<const char*>(a.tokens) + t * a.row_bytes + i);
+      typename Piece<V, 16>::type v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (b.row[j] >= 0)
+          v[j] = ld<V, A, NT>(static_cast<const char*>(a.sorted) + b.row[j] * a.row_bytes + i);
+      float d[kN];
+      unpack<T, V>(dv, d);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (b.row[j] < 0) continue;
+        float y[kN], o[kN];
+        unpack<T, V>(v[j], y);
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          dot[j] = __builtin_fmaf(d[c], y[c], dot[j]);
+          o[c] = f[j] * d[c];
+        }
+        st<V, A, NT>(static_cast<char*>(a.out) + b.row[j] * a.row_bytes + i, pack<T, V>(o));
+      }
+    });
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (k + j >= a.top_k) break;
+      const float sum = wave_sum(dot[j]);
+      if (lane == 0) {
+        if constexpr (W == 1)
+          a.dweights[t * a.top_k + k + j] = sum;
+        else
+          part[k + j][wave] = sum;
+      }
+    }
+  }
+  if constexpr (W == 4) {
+    __syncthreads();
+    const int k = threadIdx.x;
+    if (k < a.top_k)
+      a.dweights[t * a.top_k + k] = (part[k][0] + part[k][1]) + (part[k][2] + part[k][3]);
   }
 }
-
-namespace {
-
-int piece_bytes(int64_t row_bytes) {
-  return row_bytes % 16 == 0 ? 16 : row_bytes % 8 == 0 ? 8 : row_bytes % 4 == 0 ? 4 : 2;
-}
-
-}  // namespace
 
 // The plan of up to kSortFew slots, by comparing all of them with each other and
 // with every expert: two barriers and no counts to clear and add up (8 slots of
@@ -450,55 +538,78 @@ hipError_t launch_moe_sort(MoeSortArgs a, int32_t id_bytes, hipStream_t s) {
   return id_bytes == 8 ? run_sort<int64_t>(a, s) : run_sort<int32_t>(a, s);
 }
 
-#define MOE_LAUNCH(kernel) \
-  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(a.tokens_n)), dim3(kThreads), 0, s, a)
+namespace {
 
-hipError_t launch_moe_dispatch(const MoeRowArgs& a, hipStream_t s) {
-  switch (piece_bytes(a.row_bytes)) {
-    case 16: MOE_LAUNCH(k_moe_dispatch<16>); break;
-    case 8: MOE_LAUNCH(k_moe_dispatch<8>); break;
-    case 4: MOE_LAUNCH(k_moe_dispatch<4>); break;
-    default: MOE_LAUNCH(k_moe_dispatch<2>);
-  }
+// Bytes of sorted rows from which they pass the caches by (4096 tokens x 8 x 6144 bf16, 403
+// MB: dispatch 93 us without the hint, 79 with it).
+constexpr int64_t kNtRowBytes = 256ll << 20;
+// Rows of fewer bytes than this are one wave's, of more the block's; with few
+// tokens, whose waves do not fill the chip, already shorter ones are the block's
+// (1000 tokens x 2 x 1001 fp32: combine 4.8 us by blocks, 6.2 by waves; 16384 x 4 x 1024
+// bf16: 26.4 and 25.6).
+constexpr int64_t kBlockRowBytes = 4096, kBlockRowBytesFew = 1024, kFewTokens = 4096;
+
+// Calls `launch` with a token's waves and the hint as constants.
+template <typename F>
+hipError_t with_shape(const MoeRowArgs& a, F launch) {
+  const bool nt = a.tokens_n * a.top_k * a.row_bytes > kNtRowBytes;
+  const bool wide = a.row_bytes >= (a.tokens_n < kFewTokens ? kBlockRowBytesFew : kBlockRowBytes);
+  using std::integral_constant;
+  typedef integral_constant<int, 1> One;
+  typedef integral_constant<int, 4> Four;
+  const int64_t per = wide ? 1 : kThreads / 64;
+  const dim3 grid(static_cast<uint32_t>((a.tokens_n + per - 1) / per));
+  if (wide)
+    nt ? launch(Four(), std::true_type(), grid) : launch(Four(), std::false_type(), grid);
+  else
+    nt ? launch(One(), std::true_type(), grid) : launch(One(), std::false_type(), grid);
   return hipGetLastError();
 }
 
+// Calls `launch` with the alignment of the rows as a constant: 16, or an element's.
+template <typename T, typename F>
+hipError_t with_rows(const MoeRowArgs& a, F launch) {
+  if (a.row_bytes % 16 == 0) return launch(std::integral_constant<int, 16>());
+  return launch(std::integral_constant<int, sizeof(T)>());
+}
+
+template <typename T>
+hipError_t run_dispatch(const MoeRowArgs& a, hipStream_t s) {
+  return with_rows<T>(a, [&](auto align) {
+    return with_shape(a, [&](auto w, auto nt, dim3 grid) {
+      hipLaunchKernelGGL((k_moe_dispatch<align(), w(), nt()>), grid, dim3(kThreads), 0, s, a);
+    });
+  });
+}
+
+template <typename T>
+hipError_t run_combine(const MoeRowArgs& a, hipStream_t s) {
+  return with_rows<T>(a, [&](auto align) {
+    return with_shape(a, [&](auto w, auto nt, dim3 grid) {
+      hipLaunchKernelGGL((k_moe_combine<T, align(), w(), nt()>), grid, dim3(kThreads), 0, s, a);
+    });
+  });
+}
+
+template <typename T>
+hipError_t run_backward(const MoeRowArgs& a, hipStream_t s) {
+  return with_rows<T>(a, [&](auto align) {
+    return with_shape(a, [&](auto w, auto nt, dim3 grid) {
+      hipLaunchKernelGGL((k_moe_backward<T, align(), w(), nt()>), grid, dim3(kThreads), 0, s, a);
+    });
+  });
+}
+
+}  // namespace
+
+hipError_t launch_moe_dispatch(const MoeRowArgs& a, bool is_bf16, hipStream_t s) {
+  return is_bf16 ? run_dispatch<uint16_t>(a, s) : run_dispatch<float>(a, s);
+}
 hipError_t launch_moe_combine(const MoeRowArgs& a, bool is_bf16, hipStream_t s) {
-  const int v = piece_bytes(a.row_bytes);
-  if (is_bf16) {
-    switch (v) {
-      case 16: MOE_LAUNCH((k_moe_combine<uint16_t, 16>)); break;
-      case 8: MOE_LAUNCH((k_moe_combine<uint16_t, 8>)); break;
-      case 4: MOE_LAUNCH((k_moe_combine<uint16_t, 4>)); break;
-      default: MOE_LAUNCH((k_moe_combine<uint16_t, 2>));
-    }
-  } else {
-    switch (v) {
-      case 16: MOE_LAUNCH((k_moe_combine<float, 16>)); break;
-      case 8: MOE_LAUNCH((k_moe_combine<float, 8>)); break;
-      default: MOE_LAUNCH((k_moe_combine<float, 4>));
-    }
-  }
-  return hipGetLastError();
+  return is_bf16 ? run_combine<uint16_t>(a, s) : run_combine<float>(a, s);
 }
-
 hipError_t launch_moe_backward(const MoeRowArgs& a, bool is_bf16, hipStream_t s) {
-  const int v = piece_bytes(a.row_bytes);
-  if (is_bf16) {
-    switch (v) {
-      case 16: MOE_LAUNCH((k_moe_backward<uint16_t, 16>)); break;
-      case 8: MOE_LAUNCH((k_moe_backward<uint16_t, 8>)); break;
-      case 4: MOE_LAUNCH((k_moe_backward<uint16_t, 4>)); break;
-      default: MOE_LAUNCH((k_moe_backward<uint16_t, 2>));
-    }
-  } else {
-    switch (v) {
-      case 16: MOE_LAUNCH((k_moe_backward<float, 16>)); break;
-      case 8: MOE_LAUNCH((k_moe_backward<float, 8>)); break;
-      default: MOE_LAUNCH((k_moe_backward<float, 4>));
-    }
-  }
-  return hipGetLastError();
+  return is_bf16 ? run_backward<uint16_t>(a, s) : run_backward<float>(a, s);
 }
 
 }  // namespace muon

@@ -308,7 +308,7 @@ struct MoeRowArgs {
   int64_t tokens_n, sorted_rows, row_bytes;
   int32_t top_k;
 };
-hipError_t launch_moe_dispatch(const MoeRowArgs& a, hipStream_t s);
+hipError_t launch_moe_dispatch(const MoeRowArgs& a, bool is_bf16, hipStream_t s);
 hipError_t launch_moe_combine(const MoeRowArgs& a, bool is_bf16, hipStream_t s);
 hipError_t launch_moe_backward(const MoeRowArgs& a, bool is_bf16, hipStream_t s);
 
