@@ -37,44 +37,76 @@ struct DropKey {
   float scale;
 };
 
-// Elements j .. j + 3 of a tensor, j a multiple of 4.
-__device__ __forceinline__ void drop4(const DropKey& k, int64_t j, float* v) {
+// Elements j .. j + N - 1 of a tensor, j a multiple of N (4 or 8).
+template <int N>
+__device__ __forceinline__ void drop(const DropKey& k, int64_t j, float* v) {
   uint32_t c[4] = {static_cast<uint32_t>(j / 8), static_cast<uint32_t>(k.tensor),
                    static_cast<uint32_t>(k.offset), static_cast<uint32_t>(k.offset >> 32)};
   philox(c, static_cast<uint32_t>(k.seed), static_cast<uint32_t>(k.seed >> 32));
-  const bool second = (j & 4) != 0;
-  const uint32_t w[2] = {second ? c[2] : c[0], second ? c[3] : c[1]};
+  if constexpr (N == 4) {  // the block's first or second half
+    c[0] = (j & 4) != 0 ? c[2] : c[0];
+    c[1] = (j & 4) != 0 ? c[3] : c[1];
+  }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t u = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
+  for (int e = 0; e < N; ++e) {
+    const uint32_t u = e & 1 ? c[e / 2] >> 16 : c[e / 2] & 0xffffu;
     v[e] = u < k.threshold ? 0.f : v[e] * k.scale;
   }
 }
 
 constexpr int kDropSpan = 4096;  // elements of a block
 
-template <typename Ti, typename To>
+// A lane takes 8 bf16 elements, a whole block of the generator's; where one side is
+// fp32, 4, 16 bytes of it, and the block is formed twice.
+template <typename Ti, typename To, bool NT>
 __device__ __forceinline__ void drop_span(const Ti* x, To* y, int64_t at, int64_t n,
                                           const DropKey& k) {
+  constexpr int N = sizeof(Ti) == 2 && sizeof(To) == 2 ? 8 : 4;
+  constexpr int kIters = kDropSpan / (kThreads * N);
+  if (n == kDropSpan) {
+    float v[kIters][N];
+#pragma unroll
+    for (int u = 0; u < kIters; ++u) {
+      const Ti* const from = x + (u * kThreads + threadIdx.x) * N;
+      if constexpr (N == 8)
+        vec_to_f32<Ti>(NT ? ld16_nt(from) : ld16(from), v[u]);
+      else
+        load4<Ti, NT>(from, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kIters; ++u) {
+      const int i = (u * kThreads + threadIdx.x) * N;
+      drop<N>(k, at + i, v[u]);
+      if constexpr (N == 4)
+        store4<To, NT>(y + i, v[u]);
+      else if constexpr (NT)
+        st16_nt(y + i, f32_to_vec<To>(v[u]));
+      else
+        st16(y + i, f32_to_vec<To>(v[u]));
+    }
+    return;
+  }
   for (int64_t i = static_cast<int64_t>(threadIdx.x) * 4; i < n; i += kThreads * 4) {
     float v[4];
-    if (i + 4 <= n) {
+    const bool whole = i + 4 <= n;
+    if (whole)
       load4<Ti, false>(x + i, v);
-      drop4(k, at + i, v);
-      store4<To, false>(y + i, v);
-    } else {
+    else
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = i + e < n ? Elt<Ti>::to_f32(x[i + e]) : 0.f;
-      drop4(k, at + i, v);
+    drop<4>(k, at + i, v);
+    if (whole)
+      store4<To, false>(y + i, v);
+    else
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (i + e < n) y[i + e] = Elt<To>::from_f32(v[e]);
-    }
   }
 }
 
 }  // namespace
 
+template <bool NT>
 __global__ __launch_bounds__(kThreads) void k_dropout(ArgTable, GradCtx ctx, DropArgs p,
                                                       int32_t chunks) {
   constexpr int kPer = static_cast<int>(kGradSpan / kDropSpan);  // blocks per chunk
@@ -97,21 +129,32 @@ __global__ __launch_bounds__(kThreads) void k_dropout(ArgTable, GradCtx ctx, Dro
   float* yf = static_cast<float*>(c.out) + at;
   if (c.in_bf16) {
     if (c.out_bf16)
-      drop_span(xh, yh, at, n, k);
+      drop_span<uint16_t, uint16_t, NT>(xh, yh, at, n, k);
     else
-      drop_span(xh, yf, at, n, k);
+      drop_span<uint16_t, float, NT>(xh, yf, at, n, k);
   } else {
     if (c.out_bf16)
-      drop_span(xf, yh, at, n, k);
+      drop_span<float, uint16_t, NT>(xf, yh, at, n, k);
     else
-      drop_span(xf, yf, at, n, k);
+      drop_span<float, float, NT>(xf, yf, at, n, k);
   }
 }
 
-hipError_t launch_dropout(const ArgTable& t, const GradCtx& c, int32_t chunks, const DropArgs& p) {
+namespace {
+
+// Bytes read and written from which they pass the caches by, as in the scale pass.
+constexpr int64_t kNtDropBytes = 256ll << 20;
+
+}  // namespace
+
+hipError_t launch_dropout(const ArgTable& t, const GradCtx& c, int32_t chunks, const DropArgs& p,
+                          int64_t bytes) {
   if (chunks <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_dropout, block_grid(chunks * (kGradSpan / kDropSpan)), dim3(kThreads), 0,
-                     c.stream, t, c, p, chunks);
+  const dim3 grid = block_grid(chunks * (kGradSpan / kDropSpan));
+  if (bytes > kNtDropBytes)
+    hipLaunchKernelGGL(k_dropout<true>, grid, dim3(kThreads), 0, c.stream, t, c, p, chunks);
+  else
+    hipLaunchKernelGGL(k_dropout<false>, grid, dim3(kThreads), 0, c.stream, t, c, p, chunks);
   return hipGetLastError();
 }
 

@@ -42,7 +42,7 @@ extern "C" int32_t muon_dropout_batched(int32_t batch, const int64_t* numel, con
     a.threshold = static_cast<uint32_t>(std::nearbyint(p->p * 65536.0));
     a.scale = a.threshold < 65536u ? static_cast<float>(65536.0 / (65536.0 - a.threshold)) : 0.f;
     TimedLaunch tl(MUON_K_DROPOUT, s);
-    const hipError_t e = launch_dropout(t, c, pl.chunks, a);
+    const hipError_t e = launch_dropout(t, c, pl.chunks, a, pl.in_bytes + pl.out_bytes);
     if (e != hipSuccess) return hip_fail(e, "launch dropout");
     tl.done();
     return MUON_OK;

@@ -275,7 +275,9 @@ struct DropArgs {
   uint32_t threshold;      // of 2^16: an element whose 16 bits are below it is dropped
   float scale;             // of those that stay
 };
-hipError_t launch_dropout(const ArgTable& t, const GradCtx& c, int32_t chunks, const DropArgs& p);
+// bytes: read and written.
+hipError_t launch_dropout(const ArgTable& t, const GradCtx& c, int32_t chunks, const DropArgs& p,
+                          int64_t bytes);
 
 // Tokens to the experts and back.
 constexpr int kMoeMaxExperts = 1024;
