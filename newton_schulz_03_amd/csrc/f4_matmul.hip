@@ -85,10 +85,6 @@ __device__ __forceinline__ void store4_to(To* y, int32_t left, bool whole, const
   }
 }
 
-}  // namespace
-
-namespace {
-
 // What a wave of the kernel below holds: RT strips of 16 weight rows, and 16 rows of
 // x, of which this lane has one.  A ring of four tiles of weights and scales, and of
 // two of x, is in flight.
