@@ -47,23 +47,22 @@ __device__ __forceinline__ float scale_of(uint32_t word, int g) {
   return __uint_as_float(g == 3 ? word >> 24 << 23 : (word >> (8 * g) & 255u) << 23);
 }
 
-// Eight values of a row from column k on, zero past its end.  whole (uniform): the
-// wave's columns are all there.
-template <bool VEC>
-__device__ __forceinline__ bf16x8_t row8(const uint16_t* x, int32_t k, int32_t cols, bool whole) {
-  if constexpr (VEC) {
-    if (whole) return __builtin_bit_cast(bf16x8_t, ld16(x + k));
-    u32x4_t v = {0, 0, 0, 0};
-    if (k < cols) v = ld16(x + k);
-    return __builtin_bit_cast(bf16x8_t, v);
-  } else {
-    uint16_t v[8];
+// Eight values of a row from column k on.  Rows of odd length lie at any even
+// address; the load is the same, but slower for many rows (64 experts of 2048
+// weight rows, 1024 rows of x in all: 137 us at 6144 columns, 265 at 6145).
+typedef u32x4_t u32x4_at2_t __attribute__((aligned(2)));
+__device__ __forceinline__ bf16x8_t row8(const uint16_t* x, int32_t k) {
+  return __builtin_bit_cast(bf16x8_t, u32x4_t(*(const GLOBAL_AS u32x4_at2_t*)(x + k)));
+}
+// The same, zero past the row's end.
+__device__ __forceinline__ bf16x8_t row8(const uint16_t* x, int32_t k, int32_t cols) {
+  if (k + 8 <= cols) return row8(x, k);
+  uint16_t v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = k + e < cols ? x[k + e] : 0;
-    bf16x8_t r;
-    __builtin_memcpy(&r, v, 16);
-    return r;
-  }
+  for (int e = 0; e < 8; ++e) v[e] = k + e < cols ? x[k + e] : 0;
+  bf16x8_t r;
+  __builtin_memcpy(&r, v, 16);
+  return r;
 }
 
 // Four outputs of a row from column r on.
@@ -88,7 +87,7 @@ __device__ __forceinline__ void store4_to(To* y, int32_t left, bool whole, const
 // What a wave of the kernel below holds: RT strips of 16 weight rows, and 16 rows of
 // x, of which this lane has one.  A ring of four tiles of weights and scales, and of
 // two of x, is in flight.
-template <int RT, bool VEC>
+template <int RT>
 struct Strips {
   const char *q[RT], *s[RT];  // uniform
   uint32_t qat, sat;          // this lane's bytes of a tile, of four tiles' scales
@@ -110,7 +109,7 @@ struct Strips {
   }
   __device__ __forceinline__ void load_x(int v, int32_t t) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) b[v][g] = row8<true>(x, t * kF4Tile + 32 * g + kc, cols, true);
+    for (int g = 0; g < 4; ++g) b[v][g] = row8(x, t * kF4Tile + 32 * g + kc);
   }
   __device__ __forceinline__ void multiply(int u) {
 #pragma unroll
@@ -148,7 +147,7 @@ struct Strips {
       sc[0][i][0] = *(const GLOBAL_AS uint32_t*)(s[i] + static_cast<int64_t>(t / 4) * 256 + t % 4 * 4 + sat);
     }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) b[0][g] = row8<VEC>(x, t * kF4Tile + 32 * g + kc, cols, false);
+    for (int g = 0; g < 4; ++g) b[0][g] = row8(x, t * kF4Tile + 32 * g + kc, cols);
     multiply(0);
   }
 };
@@ -157,7 +156,7 @@ struct Strips {
 
 // A wave sums RT tile rows times 16 rows of x over its share of the columns: the
 // block's waves are `ksplit` shares of the columns times groups of RT tile rows.
-template <typename To, int RT, bool VEC>
+template <typename To, int RT>
 __global__ __launch_bounds__(64 * kF4MaxSplit, 2) void k_f4_matmul(F4ProdArgs a) {
   __shared__ __attribute__((aligned(16))) f32x4_t part[RT][kF4MaxSplit][64];
   const int lane = threadIdx.x & 63;
@@ -172,7 +171,7 @@ __global__ __launch_bounds__(64 * kF4MaxSplit, 2) void k_f4_matmul(F4ProdArgs a)
   }
   const int32_t quads = (a.ktiles + 3) / 4;
   const int32_t strip0 = (blockIdx.x * ((blockDim.x >> 6) / a.ksplit) + rs) * RT;
-  Strips<RT, VEC> z;
+  Strips<RT> z;
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     // strips past the last take that one's place: their results are not stored
@@ -186,7 +185,7 @@ __global__ __launch_bounds__(64 * kF4MaxSplit, 2) void k_f4_matmul(F4ProdArgs a)
   z.kc = 8 * (lane >> 4);
   // tiles t0 .. t1 - 1, whole quads of them up to tq
   const int32_t t0 = quads * ks / a.ksplit * 4, t1 = min(quads * (ks + 1) / a.ksplit * 4, a.ktiles);
-  const int32_t tq = VEC ? max(t0, min(quads * (ks + 1) / a.ksplit, a.cols / (4 * kF4Tile)) * 4) : t0;
+  const int32_t tq = max(t0, min(quads * (ks + 1) / a.ksplit, a.cols / (4 * kF4Tile)) * 4);
   if (tq > t0) z.begin(t0);  // the weights are on their way before the rows are known
   if (a.active != nullptr) {
     p0 = max(load_const(a.offsets + e), 0);
@@ -242,7 +241,7 @@ constexpr int kManyRows = 64;
 constexpr int kManyTile = kManyRows * kF4Tile * 2;  // bytes of x
 }  // namespace
 
-template <typename To, int RT, int KS, bool VEC>
+template <typename To, int RT, int KS>
 __global__ __launch_bounds__(256 * KS, 2) void k_f4_many(F4ProdArgs a) {
   constexpr int MT = kManyRows / 16;
   // [group][buffer][row][16 bytes of 8 columns at chunk ^ row % 16], then the sums
@@ -272,8 +271,7 @@ __global__ __launch_bounds__(256 * KS, 2) void k_f4_many(F4ProdArgs a) {
   const int32_t t0 = a.ktiles * ks / KS, t1 = a.ktiles * (ks + 1) / KS;
   const int32_t steps = (a.ktiles + KS - 1) / KS;  // of the longest share
   // steps whose tiles are whole in every share, in fours
-  const int32_t whole =
-      VEC ? min(a.ktiles / KS, a.cols / kF4Tile - a.ktiles * (KS - 1) / KS) / 4 * 4 : 0;
+  const int32_t whole = min(a.ktiles / KS, a.cols / kF4Tile - a.ktiles * (KS - 1) / KS) / 4 * 4;
   const int at = threadIdx.x & 255, chunk = at & 15;
   for (p0 += static_cast<int64_t>(blockIdx.z) * kManyRows; p0 < p1;
        p0 += static_cast<int64_t>(gridDim.z) * kManyRows) {
@@ -303,7 +301,7 @@ __global__ __launch_bounds__(256 * KS, 2) void k_f4_many(F4ProdArgs a) {
     };
     auto load_x = [&](int v, int32_t t) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xr[v][j] = ld16(x[j] + t * kF4Tile);
+      for (int j = 0; j < 4; ++j) xr[v][j] = __builtin_bit_cast(u32x4_t, row8(x[j], t * kF4Tile));
     };
     auto store_x = [&](char* buf, int v) {
 #pragma unroll
@@ -361,7 +359,7 @@ __global__ __launch_bounds__(256 * KS, 2) void k_f4_many(F4ProdArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           xr[0][j] = __builtin_bit_cast(
-              u32x4_t, row8<VEC>(x[j] - 8 * chunk, t * kF4Tile + 8 * chunk, a.cols, false));
+              u32x4_t, row8(x[j] - 8 * chunk, t * kF4Tile + 8 * chunk, a.cols));
         store_x(xs[ks][0], 0);
       }
       __syncthreads();
@@ -404,20 +402,14 @@ void run(const F4ProdArgs& a, int64_t experts, hipStream_t s) {
   const int waves = std::max(kF4Waves, a.ksplit), strips = waves / a.ksplit * RT;
   const dim3 grid((a.rtiles + strips - 1) / strips, static_cast<uint32_t>(experts));
   const dim3 block(64 * waves);
-  if (a.cols % 8 == 0)
-    hipLaunchKernelGGL((k_f4_matmul<To, RT, true>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((k_f4_matmul<To, RT, false>), grid, block, 0, s, a);
+  hipLaunchKernelGGL((k_f4_matmul<To, RT>), grid, block, 0, s, a);
 }
 
 template <typename To, int RT, int KS>
 void run_many(const F4ProdArgs& a, int64_t experts, int64_t passes, hipStream_t s) {
   const dim3 grid((a.rtiles + 4 * RT - 1) / (4 * RT), static_cast<uint32_t>(experts),
                   static_cast<uint32_t>(passes));
-  if (a.cols % 8 == 0)
-    hipLaunchKernelGGL((k_f4_many<To, RT, KS, true>), grid, dim3(256 * KS), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_f4_many<To, RT, KS, false>), grid, dim3(256 * KS), 0, s, a);
+  hipLaunchKernelGGL((k_f4_many<To, RT, KS>), grid, dim3(256 * KS), 0, s, a);
 }
 
 template <typename To>
