@@ -208,6 +208,30 @@ def test_nothing_to_sum():
     assert nsa.f4_matmul(x.new_zeros((3, 40)), nsa.f4_empty(1, 0, 40, "cuda")).shape == (3, 0)
 
 
+def test_a_plan_without_tokens():
+    op, _ = operand(3, 20, 40, 1)
+    plan = nsa.moe_sort(torch.zeros((0, 2), dtype=torch.int64, device="cuda"), 3)
+    x = torch.zeros((0, 40), dtype=BF16, device="cuda")
+    assert nsa.f4_matmul(x, op, plan=plan, gather=True).shape == (0, 20)
+    assert nsa.f4_matmul(x, op, plan=plan).shape == (0, 20)
+
+
+def test_more_rows_than_the_products_are_for():
+    # passes of 64 rows: over the grid, and again within a block
+    op, (w,) = operand(1, 40, 136, 3)
+    x = values((1111, 136), BF16, 1)
+    check(nsa.f4_matmul(x, op, out_dtype=FP32), host_f64(x), w, FP32)
+    op, ws = operand(9, 40, 136, 3)
+    ids = torch.zeros((1500, 1), dtype=torch.int32, device="cuda")
+    ids[:8, 0] = torch.arange(1, 9, device="cuda")
+    plan = nsa.moe_sort(ids, 9)
+    x = values((1500, 136), BF16, 2)
+    y = nsa.f4_matmul(x, op, plan=plan, gather=True, out_dtype=FP32)
+    check(y[:1492], host_f64(x)[8:], ws[0], FP32)
+    for e in range(1, 9):
+        check(y[1491 + e:1492 + e], host_f64(x)[e - 1:e], ws[e], FP32)
+
+
 def test_weights_past_4_gb():
     """The last expert's matrix lies past 2^32 bytes of codes."""
     experts, rows, cols = 700, 2048, 6144

@@ -308,6 +308,42 @@ def test_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(plan, p2)) and torch.equal(got, want)
 
 
+def test_a_given_workspace():
+    ids = route(5000, 8, 40, 0.1, 4)
+    nbytes = nsa.moe_workspace_bytes(5000, 8, 40)
+    room = torch.full((nbytes + 512,), 0xEE, dtype=torch.uint8, device="cuda")
+    at = (-room.data_ptr()) % 256
+    check_plan(nsa.moe_sort(ids, 40, workspace=room[at:at + nbytes]), ids, 40)
+    assert bool((room[at + nbytes:] == 0xEE).all()) and bool((room[:at] == 0xEE).all())
+    for bad in (room[at:at + nbytes - 1], room[at + 1:]):
+        with pytest.raises(nsa.MuonError):
+            nsa.moe_sort(ids, 40, workspace=bad)
+    for bad in (torch.empty(nbytes, dtype=torch.uint8), room[::2], room.view(torch.int32)):
+        with pytest.raises(ValueError):
+            nsa.moe_sort(ids, 40, workspace=bad)
+
+
+def test_calls_on_two_streams_at_once():
+    work = []
+    for seed in (1, 2):
+        ids = route(6000, 8, 64, 0.1, seed)
+        x, w = values((6000, 520), BF16, seed), values((6000, 8), FP32, seed)
+        plan = nsa.moe_sort(ids, 64)
+        work.append((ids, x, w, plan, nsa.moe_combine(nsa.moe_dispatch(x, plan), plan, weights=w)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    got = [[], []]
+    for _ in range(10):
+        for s, (ids, x, w, _, _), g in zip(streams, work, got):
+            with torch.cuda.stream(s):
+                plan = nsa.moe_sort(ids, 64)
+                g.append((plan, nsa.moe_combine(nsa.moe_dispatch(x, plan), plan, weights=w)))
+    torch.cuda.synchronize()
+    for (_, _, _, plan, out), g in zip(work, got):
+        for p, o in g:
+            assert all(torch.equal(a, b) for a, b in zip(p, plan)) and torch.equal(o, out)
+
+
 def test_binding_refusals():
     ids = route(10, 2, 4, 0.0, 1)
     plan = nsa.moe_sort(ids, 4)
