@@ -18,11 +18,10 @@
 // read and written 16 bytes at a time all the same, at element-aligned addresses
 // (16384 x 4 x 1001 bf16: 30, 32 and 58 us; by elements 34, 60 and 121).
 //
-// The sort: up to kSortFew slots in a kernel that compares all of them (8 slots of
-// 384 experts: 2.2 us, the next one 6.6), up to kSortPiece in one block, more in
-// two launches, counts and rows (524288 slots of 8 bytes, 384 experts: 3.2 + 13.2 us;
-// one block for all of them took 880).  Pieces of 2048 slots: 22 us for the rows, since
-// every block adds up the counts of twice as many.
+// The sort: a few slots in a kernel that compares all of them, up to kSortPiece in one
+// block, more in two launches, counts and rows (524288 slots of 8 bytes, 384 experts:
+// 3.2 + 13.2 us; one block for all of them took 880).  Pieces of 2048 slots there: 22
+// us for the rows, since every block adds up the counts of twice as many.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -32,7 +31,6 @@ namespace muon {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSteps = kSortPiece / kSortThreads;  // slots of a thread in a piece
 // Words of 16-bit counts, two experts each.
 constexpr int kPairs = kMoeMaxExperts / 2;
 constexpr int kSumBatch = 16;  // loads of a thread in flight while it adds up the blocks' counts
@@ -83,13 +81,13 @@ __device__ __forceinline__ int block_before(int v, int* scratch /* kSortWaves */
 
 namespace {
 
-// This thread's slots of a piece that starts at s0 (of the thread): each wave
-// holds kSortPiece / 16 slots in a row, 64 at a time.
-template <typename I>
-__device__ __forceinline__ void load_ids(const MoeSortArgs& a, int64_t s0, int (&e)[kSteps]) {
+// This thread's slots of a piece, from s0 on: each wave holds 64 * STEPS slots in a
+// row, 64 at a time.
+template <typename I, int STEPS>
+__device__ __forceinline__ void load_ids(const MoeSortArgs& a, int64_t s0, int (&e)[STEPS]) {
   const I* const ids = static_cast<const I*>(a.ids);
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) e[u] = expert_of(ids, s0 + u * 64, a.n, a.experts);
+  for (int u = 0; u < STEPS; ++u) e[u] = expert_of(ids, s0 + u * 64, a.n, a.experts);
 }
 
 // Adds one to expert e's 16 bits.
@@ -101,48 +99,50 @@ __device__ __forceinline__ void count_one(uint32_t* counts, int e) {
 
 // How many slots of each expert a block of the sort will find, two 16-bit counts a
 // word.  Only for lists of more than one block.
-template <typename I>
+template <typename I, int STEPS>
 __global__ __launch_bounds__(kSortThreads) void k_moe_count(MoeSortArgs a) {
+  constexpr int kPiece = STEPS * kSortThreads;
   __shared__ uint32_t counts[kPairs];
   const int me = threadIdx.x, pairs = (a.experts + 1) / 2;
   if (me < pairs) counts[me] = 0;
   __syncthreads();
   const int64_t from = static_cast<int64_t>(blockIdx.x) * a.span;
-  for (int64_t at = from; at < from + a.span && at < a.n; at += kSortPiece) {
-    int e[kSteps];
-    load_ids<I>(a, at + (me >> 6) * (64 * kSteps) + (me & 63), e);
+  for (int64_t at = from; at < from + a.span && at < a.n; at += kPiece) {
+    int e[STEPS];
+    load_ids<I>(a, at + (me >> 6) * (64 * STEPS) + (me & 63), e);
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) count_one(counts, e[u]);
+    for (int u = 0; u < STEPS; ++u) count_one(counts, e[u]);
   }
   __syncthreads();
   if (me < pairs) a.counts[blockIdx.x * pairs + me] = counts[me];
 }
 
-// The rows of the slots.  A block takes `span` slots in pieces of kSortPiece.  The
+// The rows of the slots.  A block takes `span` slots in pieces of 1024 * STEPS.  The
 // waves' counts of each expert in a piece become where their rows begin, and each
 // wave walks its slots 64 at a time: a slot's row is its expert's next one plus
 // the lanes before it with that id.  Where the block's rows begin follows from all
 // blocks' counts, which every block adds up for itself (128 blocks, 384 experts:
 // 98 KB from the L2).
-template <typename I>
+template <typename I, int STEPS>
 __global__ __launch_bounds__(kSortThreads) void k_moe_sort(MoeSortArgs a) {
+  constexpr int kPiece = STEPS * kSortThreads;
   __shared__ int32_t base[kMoeMaxExperts];     // the first row of the piece for each expert
   __shared__ int32_t totals[kMoeMaxExperts];   // slots of each expert in all blocks
   __shared__ uint32_t next[kSortWaves * kPairs];  // each wave's next row after that
   __shared__ int scratch[kSortWaves];
-  static_assert(kMoeMaxExperts <= kSortThreads && kSortPiece < (1 << 16));
+  static_assert(kMoeMaxExperts <= kSortThreads && kPiece < (1 << 16));
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int me = threadIdx.x;  // the expert that a thread counts for
   const int pairs = (a.experts + 1) / 2;
   const int bits = 32 - __builtin_clz((a.experts - 1) | 1);
   const int64_t from = static_cast<int64_t>(blockIdx.x) * a.span;
   const int64_t to = min(a.n, from + a.span);
-  const bool single = gridDim.x == 1 && to - from <= kSortPiece;
+  const bool single = gridDim.x == 1 && to - from <= kPiece;
   uint32_t* const row = next + wave * pairs;
   volatile uint16_t* const mine = reinterpret_cast<volatile uint16_t*>(row);
 
-  int e[kSteps];
-  load_ids<I>(a, from + wave * (64 * kSteps) + lane, e);
+  int e[STEPS];
+  load_ids<I>(a, from + wave * (64 * STEPS) + lane, e);
   for (int i = me; i < kSortWaves * pairs; i += kSortThreads) next[i] = 0;
   base[me] = 0;
   totals[me] = 0;
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(MoeSortArgs a) {
   int64_t piece = from;
   do {
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) count_one(row, e[u]);
+    for (int u = 0; u < STEPS; ++u) count_one(row, e[u]);
     __syncthreads();
     if (me < pairs) {
       uint32_t sum = 0;
@@ -216,8 +216,8 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(MoeSortArgs a) {
       __syncthreads();
     }
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const int64_t s = piece + wave * (64 * kSteps) + u * 64 + lane;
+    for (int u = 0; u < STEPS; ++u) {
+      const int64_t s = piece + wave * (64 * STEPS) + u * 64 + lane;
       const uint64_t same = same_id(e[u], bits);
       const int rank = __popcll(same & ((1ull << lane) - 1));
       int to_row = -1, begun = 0;
@@ -233,9 +233,9 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(MoeSortArgs a) {
         if (to_row >= 0) a.slots[to_row] = static_cast<int32_t>(s);
       }
     }
-    piece += kSortPiece;
+    piece += kPiece;
     if (piece >= to) break;
-    load_ids<I>(a, piece + wave * (64 * kSteps) + lane, e);
+    load_ids<I>(a, piece + wave * (64 * STEPS) + lane, e);
     __syncthreads();
     // the last wave's next rows are past all of the piece's
     const uint32_t last = next[(kSortWaves - 1) * pairs + (me >> 1)];
@@ -501,29 +501,45 @@ namespace {
 
 // The most blocks of a sort: each adds up the counts of all.
 constexpr int64_t kSortBlocks = 320;
+// Pieces of 1024 slots up to kSortShort of them, so that more blocks share the
+// work, but of 4096 where those need one launch instead of two, and beyond (384
+// experts: 1024 slots 5.1 us in pieces of 1024, 7.1 of 4096; 4096 slots 8.8 and 8.1;
+// 32768 slots 9.5 and 12.4; 131072 slots 12.7 either way).
+constexpr int64_t kSortShort = 65536;
 
+int64_t sort_piece(int64_t n) {
+  return n <= kSortThreads || (n > kSortPiece && n <= kSortShort) ? kSortThreads : kSortPiece;
+}
 int64_t sort_span(int64_t n) {
-  const int64_t pieces = (n + kSortPiece - 1) / kSortPiece;
-  return (pieces + kSortBlocks - 1) / kSortBlocks * kSortPiece;
+  const int64_t pieces = (n + sort_piece(n) - 1) / sort_piece(n);
+  return (pieces + kSortBlocks - 1) / kSortBlocks * sort_piece(n);
 }
 int64_t sort_blocks(int64_t n) { return n > 0 ? (n + sort_span(n) - 1) / sort_span(n) : 1; }
 static_assert((kMoeMaxSlots / kSortPiece + kSortBlocks) / kSortBlocks * kSortPiece < (1 << 16),
               "16-bit counts of a block");
 
-template <typename I>
-hipError_t run_sort(const MoeSortArgs& a, hipStream_t s) {
-  if (a.n <= kSortFew) {
-    hipLaunchKernelGGL(k_moe_sort_few<I>, dim3(1), dim3(kFewThreads), 0, s, a);
-    return hipGetLastError();
-  }
+template <typename I, int STEPS>
+hipError_t run_blocks(const MoeSortArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(sort_blocks(a.n)));
   if (grid.x > 1) {
-    hipLaunchKernelGGL(k_moe_count<I>, grid, dim3(kSortThreads), 0, s, a);
+    hipLaunchKernelGGL((k_moe_count<I, STEPS>), grid, dim3(kSortThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(k_moe_sort<I>, grid, dim3(kSortThreads), 0, s, a);
+  hipLaunchKernelGGL((k_moe_sort<I, STEPS>), grid, dim3(kSortThreads), 0, s, a);
   return hipGetLastError();
+}
+
+template <typename I>
+hipError_t run_sort(const MoeSortArgs& a, hipStream_t s) {
+  // 384 experts: 8 slots 2.7 us, by pieces 4.8; 128 slots 12.3 and 4.8
+  if (a.n * ((a.experts + kFewThreads) / kFewThreads) <= kSortFew) {
+    hipLaunchKernelGGL(k_moe_sort_few<I>, dim3(1), dim3(kFewThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  return sort_piece(a.n) == kSortThreads
+             ? run_blocks<I, 1>(a, s)
+             : run_blocks<I, static_cast<int>(kSortPiece / kSortThreads)>(a, s);
 }
 
 }  // namespace
@@ -534,7 +550,7 @@ size_t moe_sort_workspace(int64_t n, int32_t experts) {
 }
 
 hipError_t launch_moe_sort(MoeSortArgs a, int32_t id_bytes, hipStream_t s) {
-  a.span = a.n > 0 ? sort_span(a.n) : kSortPiece;
+  a.span = a.n > 0 ? sort_span(a.n) : kSortThreads;
   return id_bytes == 8 ? run_sort<int64_t>(a, s) : run_sort<int32_t>(a, s);
 }
 

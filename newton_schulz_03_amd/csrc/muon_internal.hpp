@@ -283,8 +283,8 @@ hipError_t launch_dropout(const ArgTable& t, const GradCtx& c, int32_t chunks, c
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 64;
 constexpr int64_t kMoeMaxSlots = (1 << 24) - 1;  // also fewer blocks than a launch holds
-constexpr int kSortFew = 128;   // slots of the sort that compares all of them
-constexpr int kSortPiece = 4096;  // slots that a block of the sort takes at a time
+constexpr int kSortFew = 32;    // most slots of the sort that compares all of them
+constexpr int kSortPiece = 4096;  // slots that a block of the sort takes at a time, or 1024
 struct MoeSortArgs {
   const void* ids;         // n of 4 or 8 bytes
   int32_t* offsets;        // experts + 1

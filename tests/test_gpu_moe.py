@@ -54,7 +54,8 @@ def values(shape, dtype, seed):
 
 
 @pytest.mark.parametrize("tokens,top_k,experts", [
-    (0, 2, 5), (1, 1, 1), (1, 8, 384), (2, 64, 3), (63, 1, 7), (64, 1, 8), (65, 1, 9), (16, 8, 700), (127, 1, 3), (128, 1, 1024), (129, 1, 600), (129, 8, 384),
+    (0, 2, 5), (1, 1, 1), (1, 8, 384), (2, 64, 3), (63, 1, 7), (64, 1, 8), (65, 1, 9), (16, 8, 700), (127, 1, 3), (128, 1, 1024), (4, 8, 384), (33, 1, 511), (16, 1, 512), (17, 1, 512), (10, 1, 1024),
+    (11, 1, 1023), (128, 8, 60), (512, 8, 384), (513, 8, 384), (8192, 8, 100), (8193, 8, 100), (129, 1, 600), (129, 8, 384),
     (1000, 3, 1024), (1024, 8, 1023), (1025, 8, 33), (4096, 8, 384), (3001, 7, 2), (9000, 6, 511)])
 @pytest.mark.parametrize("drop", [0.0, 0.3])
 def test_sort(tokens, top_k, experts, drop):
