@@ -290,7 +290,7 @@ __device__ __forceinline__ typename Piece<V, 16>::type pack(const float* v) {
 constexpr int kBatch = 8;  // slots whose rows are asked for together
 
 // The sorted rows of slots k .. k + kBatch - 1 of a token, -1 for those that are
-// dropped or past the last slot.  Uniform.
+// dropped or past the last slot.
 struct Batch {
   int32_t row[kBatch];
   __device__ __forceinline__ Batch(const int32_t* rows, int k, int top_k, int64_t sorted_rows) {
@@ -302,24 +302,27 @@ struct Batch {
   }
 };
 
-// This wave's token, or -1: a block takes one token (W = 4 waves) or one a wave.
+// The lanes that share a token's row: the block (W = 4 waves), a wave (1) or 16 (0).
+template <int W>
+constexpr int kLanes = W == 0 ? 16 : 64 * W;
+// This lane's token, or -1.
 template <int W>
 __device__ __forceinline__ int64_t token_of(const MoeRowArgs& a) {
-  const int64_t t = W == 1 ? static_cast<int64_t>(blockIdx.x) * (kThreads / 64) +
-                                 __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
-                           : static_cast<int64_t>(blockIdx.x);
+  int part = threadIdx.x / kLanes<W>;
+  if (W > 0) part = __builtin_amdgcn_readfirstlane(part);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / kLanes<W>) + part;
   return t < a.tokens_n ? t : -1;
 }
 template <int W>
 __device__ __forceinline__ int lane_of() {
-  return W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  return threadIdx.x % kLanes<W>;
 }
 
 // Calls body(offset, V) for this lane's pieces of a row: 16 bytes each, at addresses
 // that are multiples of A, then (A < 16) the last elements, one a lane.
 template <int A, int W, typename F>
 __device__ __forceinline__ void for_pieces(int64_t row_bytes, F body) {
-  for (int64_t i = lane_of<W>() * 16; i + 16 <= row_bytes; i += 64 * W * 16)
+  for (int64_t i = lane_of<W>() * 16; i + 16 <= row_bytes; i += kLanes<W> * 16)
     body(i, std::integral_constant<int, 16>());
   if constexpr (A < 16) {
     const int64_t i = row_bytes / 16 * 16 + lane_of<W>() * A;
@@ -379,12 +382,12 @@ __global__ __launch_bounds__(kThreads) void k_moe_combine(MoeRowArgs a) {
 }
 
 // The products of a token's row with its experts' rows are summed by lanes, then
-// over the wave, then (W = 4) over the waves.
+// over the token's lanes of the wave, then (W = 4) over the waves.
 template <typename T, int A, int W, bool NT>
 __global__ __launch_bounds__(kThreads) void k_moe_backward(MoeRowArgs a) {
   __shared__ float part[kMoeMaxTopK][kThreads / 64];
   const int64_t t = token_of<W>(a);
-  if (t < 0) return;  // whole waves; with W = 4 none
+  if (t < 0) return;  // all lanes of a token; with W = 4 none
   const int32_t* const rows = a.rows + t * a.top_k;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int k = 0; k < a.top_k; k += kBatch) {
@@ -420,9 +423,11 @@ __global__ __launch_bounds__(kThreads) void k_moe_backward(MoeRowArgs a) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (k + j >= a.top_k) break;
-      const float sum = wave_sum(dot[j]);
-      if (lane == 0) {
-        if constexpr (W == 1)
+      float sum = dot[j];
+#pragma unroll
+      for (int off = W == 0 ? 8 : 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+      if ((W == 0 ? lane & 15 : lane) == 0) {
+        if constexpr (W < 4)
           a.dweights[t * a.top_k + k + j] = sum;
         else
           part[k + j][wave] = sum;
@@ -564,19 +569,27 @@ constexpr int64_t kNtRowBytes = 256ll << 20;
 // (1000 tokens x 2 x 1001 fp32: combine 4.8 us by blocks, 6.2 by waves; 16384 x 4 x 1024
 // bf16: 26.4 and 25.6).
 constexpr int64_t kBlockRowBytes = 4096, kBlockRowBytesFew = 1024, kFewTokens = 4096;
+// Rows of up to this many bytes are 16 lanes' (65536 tokens x 8 x 64 bf16, dispatch,
+// combine and gradient: 14, 18 and 28 us, by waves 24, 38 and 60; x 200: 47, 54 and 136,
+// by waves 41, 47 and 115).
+constexpr int64_t kShortRowBytes = 256;
 
 // Calls `launch` with a token's waves and the hint as constants.
 template <typename F>
 hipError_t with_shape(const MoeRowArgs& a, F launch) {
   const bool nt = a.tokens_n * a.top_k * a.row_bytes > kNtRowBytes;
   const bool wide = a.row_bytes >= (a.tokens_n < kFewTokens ? kBlockRowBytesFew : kBlockRowBytes);
+  const bool narrow = a.row_bytes <= kShortRowBytes;
   using std::integral_constant;
+  typedef integral_constant<int, 0> Part;
   typedef integral_constant<int, 1> One;
   typedef integral_constant<int, 4> Four;
-  const int64_t per = wide ? 1 : kThreads / 64;
+  const int64_t per = wide ? 1 : kThreads / (narrow ? kLanes<0> : kLanes<1>);
   const dim3 grid(static_cast<uint32_t>((a.tokens_n + per - 1) / per));
   if (wide)
     nt ? launch(Four(), std::true_type(), grid) : launch(Four(), std::false_type(), grid);
+  else if (narrow)
+    nt ? launch(Part(), std::true_type(), grid) : launch(Part(), std::false_type(), grid);
   else
     nt ? launch(One(), std::true_type(), grid) : launch(One(), std::false_type(), grid);
   return hipGetLastError();
