@@ -26,8 +26,11 @@ namespace {
 
 constexpr int kF4Waves = 4;  // of a block, 8 where 8 share the columns
 constexpr int kF4MaxSplit = 8;
-// Most rows of an expert, on average, of the kernel without LDS.
+// Most rows of an expert, on average, of the kernel without LDS, which reads the
+// weights again for every 16 (one matrix 6144 x 6144: 16 rows 10.5 us, by the kernel
+// of many rows 20; 32 rows 27 and 20).
 constexpr int64_t kF4FewRows = 16;
+constexpr int64_t kManyStrips = 1280;
 // Waves that keep the memory busy.
 constexpr int64_t kF4Busy = 2048;
 
@@ -419,16 +422,21 @@ hipError_t run(F4ProdArgs a, hipStream_t s) {
   const int64_t each = (a.m + most - 1) / most;
   if (each > kF4FewRows) {
     const int64_t passes = std::min<int64_t>((each + kManyRows - 1) / kManyRows, 65535);
-    if (strips * passes >= 8 * 512)
+    // Two strips a wave, or two shares of the columns where those blocks would not
+    // fill the chip (256 rows, 6144 x 6144, 1536 strips: 33 us and 41; 2048 x 6144, 512 strips:
+    // 31 and 20; one strip and one share is between them).
+    if (strips * passes >= kManyStrips)
       run_many<To, 2, 1>(a, most, passes, s);
-    else if (strips * passes >= 4 * 512)
-      run_many<To, 1, 1>(a, most, passes, s);
     else
       run_many<To, 1, 2>(a, most, passes, s);
     return hipGetLastError();
   }
   const int32_t quads = (a.ktiles + 3) / 4;
   const int64_t most_split = std::min<int64_t>(kF4MaxSplit, quads);
+  // As many strips a wave as leave enough waves: 8 experts of 2048 x 6144 with two
+  // 12.8 us, with one 15.8; of 6144 x 2048 with two 12.5, with four 14.9; 264 of them with
+  // four 298, with one 400.  Then as many waves to share the columns as make up
+  // kF4Busy (one matrix 2048 x 6144: 5.6 us by eight, 5.8 by four).
   const int rt = strips * most_split >= 8 * kF4Busy ? 4 : strips * most_split >= kF4Busy ? 2 : 1;
   a.ksplit = 1;
   while (a.ksplit < kF4MaxSplit && 2 * a.ksplit <= quads && strips / rt * a.ksplit < kF4Busy) a.ksplit *= 2;
