@@ -465,7 +465,8 @@ int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const int64_t* n
 #define MUON_MOE_MAX_TOP_K 64
 #define MUON_MOE_MAX_SLOTS 16777215
 
-/* Bytes of device workspace of muon_moe_sort; SIZE_MAX on invalid arguments. */
+/* Bytes of device workspace of muon_moe_sort; SIZE_MAX on invalid arguments.  Never
+ * less for more slots or more experts: the workspace of the largest call serves all. */
 size_t muon_moe_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts);
 
 int32_t muon_moe_sort(int64_t tokens, int32_t top_k, int32_t experts, const void* ids,

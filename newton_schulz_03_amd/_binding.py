@@ -986,7 +986,8 @@ def _slots(plan):
 
 @functools.lru_cache(maxsize=256)
 def moe_workspace_bytes(tokens: int, top_k: int, num_experts: int) -> int:
-    """Device workspace bytes of moe_sort."""
+    """Device workspace bytes of moe_sort; enough for every call of no more slots and
+    experts."""
     n = load_library().muon_moe_workspace_bytes(int(tokens), int(top_k), int(num_experts))
     if n == SIZE_MAX:
         raise MuonError(MUON_ERR_INVALID_ARG, "muon_moe_workspace_bytes", last_error_detail())

@@ -22,6 +22,7 @@
 // block, more in two launches, counts and rows (524288 slots of 8 bytes, 384 experts:
 // 3.2 + 13.2 us; one block for all of them took 880).  Pieces of 2048 slots there: 22
 // us for the rows, since every block adds up the counts of twice as many.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -549,9 +550,14 @@ hipError_t run_sort(const MoeSortArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// The most blocks of any list of up to n slots: those of n slots themselves can be
+// fewer, where pieces or spans get longer (65536 slots take 64 blocks, 65537 take
+// 17), and one workspace is to serve shorter lists too.
 size_t moe_sort_workspace(int64_t n, int32_t experts) {
-  const int64_t blocks = sort_blocks(n);
-  return blocks > 1 ? static_cast<size_t>(blocks) * ((experts + 1) / 2) * 4 : 0;
+  if (n <= kSortPiece) return 0;  // one block
+  const int64_t shorter = (std::min(n, kSortShort) + kSortThreads - 1) / kSortThreads;
+  const int64_t longer = std::min((n + kSortPiece - 1) / kSortPiece, kSortBlocks);
+  return static_cast<size_t>(std::max(shorter, longer)) * ((experts + 1) / 2) * 4;
 }
 
 hipError_t launch_moe_sort(MoeSortArgs a, int32_t id_bytes, hipStream_t s) {
