@@ -897,6 +897,12 @@ def dropout_batched(xs: Sequence, p: float, seed: int = 0, offset: int = 0, rng=
 MOE_MAX_EXPERTS, MOE_MAX_TOP_K, MOE_MAX_SLOTS = 1024, 64, (1 << 24) - 1
 
 
+def _int32(n) -> int:
+    """A count for the library, whose limits are far below 2^31: ctypes would pass on
+    the low 32 bits of a larger one."""
+    return max(-1, min(int(n), (1 << 31) - 1))
+
+
 _BF16, _FP32, _INT32, _INT64, _UINT8 = 1, 2, 4, 8, 16  # kinds of elements, as bits
 _FLOATS = _BF16 | _FP32
 _READ, _WRITTEN = 0, 1
@@ -988,7 +994,7 @@ def _slots(plan):
 def moe_workspace_bytes(tokens: int, top_k: int, num_experts: int) -> int:
     """Device workspace bytes of moe_sort; enough for every call of no more slots and
     experts."""
-    n = load_library().muon_moe_workspace_bytes(int(tokens), int(top_k), int(num_experts))
+    n = load_library().muon_moe_workspace_bytes(_int32(tokens), _int32(top_k), _int32(num_experts))
     if n == SIZE_MAX:
         raise MuonError(MUON_ERR_INVALID_ARG, "muon_moe_workspace_bytes", last_error_detail())
     return int(n)
@@ -1144,7 +1150,7 @@ def _f4_pointers(w, name, dev, written):
 @functools.lru_cache(maxsize=None)
 def f4_workspace_bytes(matrices: int) -> int:
     """Device workspace bytes of f4_quantize."""
-    n = load_library().muon_f4_workspace_bytes(int(matrices))
+    n = load_library().muon_f4_workspace_bytes(_int32(matrices))
     if n == SIZE_MAX:
         raise MuonError(MUON_ERR_INVALID_ARG, "muon_f4_workspace_bytes", last_error_detail())
     return int(n)
