@@ -864,7 +864,8 @@ def dropout_batched(xs: Sequence, p: float, seed: int = 0, offset: int = 0, rng=
     offsets (a step's or layer's number).  rng: an int64 tensor (seed, offset) on
     the tensors' device, read on the stream in place of both, for calls that are
     captured into a graph.  xs: contiguous bf16 and fp32 tensors.  In place
-    without `out`; out[i] may have the other dtype.  Returns the outputs.
+    without `out`; out[i] may have the other dtype.  Autograd does not record the
+    call, but notices that a tensor it has saved was written.  Returns the outputs.
     """
     import torch
 
@@ -887,6 +888,7 @@ def dropout_batched(xs: Sequence, p: float, seed: int = 0, offset: int = 0, rng=
     workspace = _workspace(workspace, _grad_table_bytes(len(xs)), dev)
     _call(load_library().muon_dropout_batched, dev, workspace, len(xs), numels, ptrs, codes, optrs,
           ocodes, ctypes.byref(prm), state)
+    _lists().wrote(*out)
     return out
 
 
@@ -1008,7 +1010,9 @@ def moe_sort(experts, num_experts: int, plan: Optional[MoePlan] = None, workspac
     expert keep their order.  Returns the plan (`plan`, if given) that
     moe_dispatch, moe_combine, moe_combine_backward and f4_matmul read; a new one's
     four tensors share an allocation.  Runs on the current HIP stream; nothing
-    waits for the GPU.
+    waits for the GPU.  Autograd records neither this call nor those that read the
+    plan: a training program calls them, and their gradients, from a function of
+    its own.
     """
     dev = _device_of(experts, "experts")
     if experts.dim() != 2:
@@ -1016,7 +1020,8 @@ def moe_sort(experts, num_experts: int, plan: Optional[MoePlan] = None, workspac
     t, k = experts.shape
     num_experts = int(num_experts)
     nbytes = moe_workspace_bytes(t, k, num_experts)
-    if plan is None:
+    given = plan
+    if given is None:
         plan = _lists().room_plan(t, k, num_experts, dev.index, MoePlan)
     pt, pk, _, *to = _plan_pointers(plan, dev, num_experts, _WRITTEN)
     if pt != t or pk != k:
@@ -1027,6 +1032,8 @@ def moe_sort(experts, num_experts: int, plan: Optional[MoePlan] = None, workspac
         workspace = _workspace(workspace, nbytes, dev)
         room, nbytes = workspace.data_ptr(), workspace.numel()
     _run(load_library().muon_moe_sort, dev, t, k, num_experts, ids, experts.element_size(), *to, room, nbytes)
+    if given is not None:
+        _lists().wrote(*plan)
     return plan
 
 
@@ -1044,13 +1051,15 @@ def moe_dispatch(x, plan: MoePlan, out=None):
     t, k = _slots(plan)
     _pointer(x, "x", dev, _FLOATS, _READ, t, -1)
     cols, kind = x.shape[1], _kind(x.dtype)
-    if out is None:
+    given = out
+    if given is None:
         out = torch.empty((t * k, cols), dtype=x.dtype, device=dev)
     po = _pointer(out, "out", dev, kind, _WRITTEN, -1, cols)
     px = _pointer(x, "x", dev, kind, _READ, t, cols)  # where it is now
     rows = _pointer(plan.rows, "plan.rows", dev, _INT32, _READ, t, k)
     _run(load_library().muon_moe_dispatch, dev, t, k, cols, px, rows, out.shape[0], po,
          MUON_BF16 if kind == _BF16 else MUON_FP32)
+    _lists().wrote(given)
     return out
 
 
@@ -1069,7 +1078,8 @@ def moe_combine(ys, plan: MoePlan, weights=None, out=None):
     t, k = _slots(plan)
     _pointer(ys, "ys", dev, _FLOATS, _READ, -1, -1)
     (n, cols), kind = ys.shape, _kind(ys.dtype)
-    if out is None:
+    given = out
+    if given is None:
         out = torch.empty((t, cols), dtype=ys.dtype, device=dev)
     po = _pointer(out, "out", dev, kind, _WRITTEN, t, cols)
     py = _pointer(ys, "ys", dev, kind, _READ, n, cols)
@@ -1077,6 +1087,7 @@ def moe_combine(ys, plan: MoePlan, weights=None, out=None):
     pw = None if weights is None else _pointer(weights, "weights", dev, _FP32, _READ, t, k)
     _run(load_library().muon_moe_combine, dev, t, k, cols, n, py, rows, pw, po,
          MUON_BF16 if kind == _BF16 else MUON_FP32)
+    _lists().wrote(given)
     return out
 
 
@@ -1095,6 +1106,7 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
     cols, kind = dout.shape[1], _kind(dout.dtype)
     _pointer(ys, "ys", dev, kind, _READ, -1, cols)
     n = ys.shape[0]
+    given = dys, dweights
     if dys is None:
         dys = torch.empty_like(ys)
     if dweights is None:
@@ -1107,6 +1119,7 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
     pw = _pointer(weights, "weights", dev, _FP32, _READ, t, k)
     _run(load_library().muon_moe_combine_backward, dev, t, k, cols, pd, n, py, rows, pw, pdy, pdw,
          MUON_BF16 if kind == _BF16 else MUON_FP32)
+    _lists().wrote(*given)
     return dys, dweights
 
 
@@ -1178,7 +1191,8 @@ def f4_quantize(ws: Sequence, transpose: bool = False, out: Optional[F4Operand] 
     rows, cols = shape[::-1] if transpose else shape
     dev = _device_of(ws[0], "ws")
     nbytes = f4_workspace_bytes(len(ws))
-    if out is None:
+    given = out
+    if given is None:
         out = f4_empty(len(ws), rows, cols, dev)
     if (out.rows, out.cols) != (rows, cols) or out.q.shape[0] != len(ws):
         raise ValueError(f"out is for {out.q.shape[0]} matrices of {out.rows} x {out.cols}, ws are "
@@ -1188,6 +1202,8 @@ def f4_quantize(ws: Sequence, transpose: bool = False, out: Optional[F4Operand] 
     workspace = _workspace(workspace, nbytes, dev)
     _call(load_library().muon_f4_quantize, dev, workspace, len(ws), rows, cols, ptrs,
           _dtype_code(ws[0].dtype), 1 if transpose else 0, pq, psc)
+    if given is not None:
+        _lists().wrote(out.q, out.scales)
     return out
 
 
@@ -1222,7 +1238,8 @@ def f4_matmul(x, w: F4Operand, plan: Optional[MoePlan] = None, gather: bool = Fa
             m = t * top_k
         elif n > t * top_k:
             raise ValueError(f"x: at most {t * top_k} sorted rows")
-    if out is None:
+    given = out
+    if given is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
         out = torch.empty((m, w.rows), dtype=dt, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
@@ -1239,6 +1256,7 @@ def f4_matmul(x, w: F4Operand, plan: Optional[MoePlan] = None, gather: bool = Fa
             slots = None
     _run(load_library().muon_f4_matmul, dev, count, w.rows, w.cols, pq, psc, out.shape[0], px, n,
          offsets, active, slots, top_k, po, MUON_BF16 if out.dtype is torch.bfloat16 else MUON_FP32)
+    _lists().wrote(given)
     return out
 
 

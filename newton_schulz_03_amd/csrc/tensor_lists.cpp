@@ -156,6 +156,28 @@ PyObject* expect(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
+// wrote(tensors ...): counts a write to each (None: none was given), as torch's in-place
+// operations do, so that autograd refuses to go back through what it saved of the
+// values before.
+PyObject* wrote(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  for (Py_ssize_t i = 0; i < n; ++i)
+    if (args[i] != Py_None && !THPVariable_Check(args[i])) {
+      PyErr_Format(PyExc_TypeError, "argument %zd is no tensor", i);
+      return nullptr;
+    }
+  try {
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      if (args[i] == Py_None) continue;
+      const at::Tensor& t = THPVariable_Unpack(args[i]);
+      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();  // those have no counter
+    }
+    Py_RETURN_NONE;
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
 // same_shapes(a, b): whether two equally long lists of tensors have equal shapes.
 PyObject* same_shapes(PyObject*, PyObject* args) {
   PyObject *a, *b;
@@ -397,6 +419,8 @@ PyMethodDef methods[] = {
     {"expect", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(expect)), METH_FASTCALL,
      "expect(tensor, device, kinds, written, sizes ...)"},
     {"room_plan", room_plan, METH_VARARGS, "room_plan(tokens, top_k, experts, device, kind)"},
+    {"wrote", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(wrote)), METH_FASTCALL,
+     "wrote(tensors ...)"},
     {"same_shapes", same_shapes, METH_VARARGS, "same_shapes(a, b)"},
     {"scan_f8", scan_f8, METH_VARARGS, "scan_f8(operands, block, written)"},
     {nullptr, nullptr, 0, nullptr},
