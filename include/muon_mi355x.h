@@ -459,7 +459,8 @@ int32_t muon_f8_matmul_batched(int32_t batch, const int64_t* m, const int64_t* n
  * tokens * top_k <= MUON_MOE_MAX_SLOTS, top_k in [1, MUON_MOE_MAX_TOP_K], experts in
  * [1, MUON_MOE_MAX_EXPERTS], cols <= MUON_F8_MAX_DIM (MUON_ERR_UNSUPPORTED beyond).
  * x, y, out, dout and dy are 16-byte aligned, the other arrays at their elements'
- * size.  No output may overlap another array of the call.
+ * size.  No output may overlap another array of the call (rows of an output that do
+ * are refused, and so are dw over w).
  */
 #define MUON_MOE_MAX_EXPERTS 1024
 #define MUON_MOE_MAX_TOP_K 64
@@ -541,7 +542,7 @@ int32_t muon_dropout_batched(int32_t batch, const int64_t* numel, const void* co
  *   slots    null: row p is x's row p (x_rows >= m); else of muon_moe_sort (m entries
  *            at least): row p is x's row slots[p] / top_k, the token's own, which
  *            saves the dispatch.  Needs offsets and active.
- *   y        m x rows, `dtype` (MUON_BF16 or MUON_FP32)
+ *   y        m x rows, `dtype` (MUON_BF16 or MUON_FP32); may not overlap x
  * Products are exact, sums fp32 in an order that the sizes fix, rounded once.
  * Scale bytes are to lie in [2, 252] or be 255.
  * Meant for up to some 64 rows an expert, where the weights' bytes bound it; more

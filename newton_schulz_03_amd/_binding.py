@@ -1012,7 +1012,7 @@ def moe_sort(experts, num_experts: int, plan: Optional[MoePlan] = None, workspac
     four tensors share an allocation.  Runs on the current HIP stream; nothing
     waits for the GPU.  Autograd records neither this call nor those that read the
     plan: a training program calls them, and their gradients, from a function of
-    its own.
+    its own.  No output of theirs may share memory with what the call reads.
     """
     dev = _device_of(experts, "experts")
     if experts.dim() != 2:

@@ -84,8 +84,14 @@ int32_t row_args(int64_t tokens, int32_t top_k, int64_t cols, int64_t sorted_row
   return MUON_OK;
 }
 
-int32_t distinct(const void* out, const void* in, const char* what) {
-  if (out != nullptr && out == in)
+// An output may share no byte with what the call reads.
+int32_t apart(const void* out, int64_t out_bytes, const void* in, int64_t in_bytes,
+              const char* what) {
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+  const bool some = out_bytes > 0 && in_bytes > 0;
+  if (out != nullptr &&
+      (o == i || (some && o < i + static_cast<uintptr_t>(in_bytes) &&
+                  i < o + static_cast<uintptr_t>(out_bytes))))
     return fail(MUON_ERR_INVALID_ARG, "%s must be another buffer", what);
   return MUON_OK;
 }
@@ -147,7 +153,7 @@ extern "C" int32_t muon_moe_dispatch(int64_t tokens, int32_t top_k, int64_t cols
     if (st != MUON_OK) return st;
     if ((st = check_array(x, tokens * cols, 16, "x")) != MUON_OK) return st;
     if ((st = check_array(out, out_rows * cols, 16, "out")) != MUON_OK) return st;
-    if ((st = distinct(out, x, "out")) != MUON_OK) return st;
+    if ((st = apart(out, out_rows * a.row_bytes, x, tokens * a.row_bytes, "out")) != MUON_OK) return st;
     if (tokens == 0 || cols == 0 || out_rows == 0) return MUON_OK;
     a.tokens = x;
     a.out = out;
@@ -170,7 +176,7 @@ extern "C" int32_t muon_moe_combine(int64_t tokens, int32_t top_k, int64_t cols,
     if ((st = check_array(y, y_rows * cols, 16, "y")) != MUON_OK) return st;
     if ((st = check_array(weights, weights != nullptr ? 1 : 0, 4, "weights")) != MUON_OK) return st;
     if ((st = check_array(out, tokens * cols, 16, "out")) != MUON_OK) return st;
-    if ((st = distinct(out, y, "out")) != MUON_OK) return st;
+    if ((st = apart(out, tokens * a.row_bytes, y, y_rows * a.row_bytes, "out")) != MUON_OK) return st;
     if (tokens == 0 || cols == 0) return MUON_OK;
     a.sorted = y;
     a.weights = weights;
@@ -197,9 +203,10 @@ extern "C" int32_t muon_moe_combine_backward(int64_t tokens, int32_t top_k, int6
     if ((st = check_array(weights, tokens, 4, "weights")) != MUON_OK) return st;
     if ((st = check_array(dy, y_rows * cols, 16, "dy")) != MUON_OK) return st;
     if ((st = check_array(dweights, tokens, 4, "dweights")) != MUON_OK) return st;
-    if ((st = distinct(dy, y, "dy")) != MUON_OK) return st;
-    if ((st = distinct(dy, dout, "dy")) != MUON_OK) return st;
-    if ((st = distinct(dweights, weights, "dweights")) != MUON_OK) return st;
+    const int64_t y_bytes = y_rows * a.row_bytes, w_bytes = tokens * top_k * 4;
+    if ((st = apart(dy, y_bytes, y, y_bytes, "dy")) != MUON_OK) return st;
+    if ((st = apart(dy, y_bytes, dout, tokens * a.row_bytes, "dy")) != MUON_OK) return st;
+    if ((st = apart(dweights, w_bytes, weights, w_bytes, "dweights")) != MUON_OK) return st;
     if (tokens == 0) return MUON_OK;
     a.tokens = dout;
     a.sorted = y;
@@ -304,7 +311,8 @@ extern "C" int32_t muon_f4_matmul(int32_t count, int64_t rows, int64_t cols, con
     if ((st = check_array(s, tiles, 16, "s")) != MUON_OK) return st;
     if ((st = check_array(x, tiles, 16, "x")) != MUON_OK) return st;
     if ((st = check_array(y, 1, 16, "y")) != MUON_OK) return st;
-    if ((st = distinct(y, x, "y")) != MUON_OK) return st;
+    const int64_t y_bytes = m * rows * (dtype == MUON_BF16 ? 2 : 4);
+    if ((st = apart(y, y_bytes, x, x_rows * cols * 2, "y")) != MUON_OK) return st;
     a.q = static_cast<const char*>(q);
     a.s = static_cast<const char*>(s);
     a.x = x;
