@@ -495,15 +495,13 @@ def _adamw_table_bytes(batch: int) -> int:
 def _call(fn, dev, workspace, *args) -> None:
     """Runs an entry point whose last arguments are the workspace, its size and
     the stream, on `dev` and its current stream."""
-    _run(fn, dev, *args, workspace.data_ptr(), workspace.numel())
+    _run(fn, dev, args + (workspace.data_ptr(), workspace.numel(), _stream_handle(dev)))
 
 
-def _run(fn, dev, *args) -> None:
-    """Runs an entry point whose last argument is the stream, on `dev` and its
-    current stream."""
+def _run(fn, dev, args) -> None:
+    """Runs an entry point on `dev`; the last of args is the stream."""
     import torch
 
-    args += (_stream_handle(dev),)
     if torch.cuda.current_device() == dev.index:
         st = fn(*args)
     else:
@@ -1031,7 +1029,8 @@ def moe_sort(experts, num_experts: int, plan: Optional[MoePlan] = None, workspac
     if nbytes > 0:
         workspace = _workspace(workspace, nbytes, dev)
         room, nbytes = workspace.data_ptr(), workspace.numel()
-    _run(load_library().muon_moe_sort, dev, t, k, num_experts, ids, experts.element_size(), *to, room, nbytes)
+    _run(load_library().muon_moe_sort, dev, (t, k, num_experts, ids, experts.element_size(), *to, room, nbytes,
+                                             _stream_handle(dev)))
     if given is not None:
         _lists().wrote(*plan)
     return plan
@@ -1057,8 +1056,8 @@ def moe_dispatch(x, plan: MoePlan, out=None):
     po = _pointer(out, "out", dev, kind, _WRITTEN, -1, cols)
     px = _pointer(x, "x", dev, kind, _READ, t, cols)  # where it is now
     rows = _pointer(plan.rows, "plan.rows", dev, _INT32, _READ, t, k)
-    _run(load_library().muon_moe_dispatch, dev, t, k, cols, px, rows, out.shape[0], po,
-         MUON_BF16 if kind == _BF16 else MUON_FP32)
+    _run(load_library().muon_moe_dispatch, dev, (t, k, cols, px, rows, out.shape[0], po,
+                                                 MUON_BF16 if kind == _BF16 else MUON_FP32, _stream_handle(dev)))
     _lists().wrote(given)
     return out
 
@@ -1085,8 +1084,8 @@ def moe_combine(ys, plan: MoePlan, weights=None, out=None):
     py = _pointer(ys, "ys", dev, kind, _READ, n, cols)
     rows = _pointer(plan.rows, "plan.rows", dev, _INT32, _READ, t, k)
     pw = None if weights is None else _pointer(weights, "weights", dev, _FP32, _READ, t, k)
-    _run(load_library().muon_moe_combine, dev, t, k, cols, n, py, rows, pw, po,
-         MUON_BF16 if kind == _BF16 else MUON_FP32)
+    _run(load_library().muon_moe_combine, dev, (t, k, cols, n, py, rows, pw, po,
+                                                MUON_BF16 if kind == _BF16 else MUON_FP32, _stream_handle(dev)))
     _lists().wrote(given)
     return out
 
@@ -1117,8 +1116,9 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
     py = _pointer(ys, "ys", dev, kind, _READ, n, cols)
     rows = _pointer(plan.rows, "plan.rows", dev, _INT32, _READ, t, k)
     pw = _pointer(weights, "weights", dev, _FP32, _READ, t, k)
-    _run(load_library().muon_moe_combine_backward, dev, t, k, cols, pd, n, py, rows, pw, pdy, pdw,
-         MUON_BF16 if kind == _BF16 else MUON_FP32)
+    _run(load_library().muon_moe_combine_backward, dev, (t, k, cols, pd, n, py, rows, pw, pdy, pdw,
+                                                         MUON_BF16 if kind == _BF16 else MUON_FP32,
+                                                         _stream_handle(dev)))
     _lists().wrote(*given)
     return dys, dweights
 
@@ -1254,8 +1254,10 @@ def f4_matmul(x, w: F4Operand, plan: Optional[MoePlan] = None, gather: bool = Fa
         _, top_k, _, offsets, active, _, slots = _plan_pointers(plan, dev, count)
         if not gather:
             slots = None
-    _run(load_library().muon_f4_matmul, dev, count, w.rows, w.cols, pq, psc, out.shape[0], px, n,
-         offsets, active, slots, top_k, po, MUON_BF16 if out.dtype is torch.bfloat16 else MUON_FP32)
+    _run(load_library().muon_f4_matmul, dev, (count, w.rows, w.cols, pq, psc, out.shape[0], px, n,
+                                              offsets, active, slots, top_k, po,
+                                              MUON_BF16 if out.dtype is torch.bfloat16 else MUON_FP32,
+                                              _stream_handle(dev)))
     _lists().wrote(given)
     return out
 
