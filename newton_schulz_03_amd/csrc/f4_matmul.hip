@@ -30,7 +30,7 @@ constexpr int kF4MaxSplit = 8;
 // weights again for every 16 (one matrix 6144 x 6144: 16 rows 10.5 us, by the kernel
 // of many rows 20; 32 rows 27 and 20).
 constexpr int64_t kF4FewRows = 16;
-constexpr int64_t kManyStrips = 1280;
+constexpr int64_t kF4Cus = 256;
 // Waves that keep the memory busy.
 constexpr int64_t kF4Busy = 2048;
 
@@ -422,10 +422,13 @@ hipError_t run(F4ProdArgs a, hipStream_t s) {
   const int64_t each = (a.m + most - 1) / most;
   if (each > kF4FewRows) {
     const int64_t passes = std::min<int64_t>((each + kManyRows - 1) / kManyRows, 65535);
-    // Two strips a wave, or two shares of the columns where those blocks would not
-    // fill the chip (256 rows, 6144 x 6144, 1536 strips: 33 us and 41; 2048 x 6144, 512 strips:
-    // 31 and 20; one strip and one share is between them).
-    if (strips * passes >= kManyStrips)
+    // Two shares of the columns while those blocks, of which a CU holds one, are no
+    // more than the CUs, or two strips a wave, half as many waves a strip (8192 x 8192,
+    // 128 rows, 256 blocks of two shares: 28 us, two strips 39; 6144 x 6144, 192 rows, 288
+    // blocks: 37.5 and 30.4, 256 rows, 384 blocks: 37.7 and 30.5; one strip and one share
+    // lies between them).
+    const int64_t blocks = most * ((a.rtiles + 3) / 4) * passes;
+    if (blocks > kF4Cus)
       run_many<To, 2, 1>(a, most, passes, s);
     else
       run_many<To, 1, 2>(a, most, passes, s);

@@ -88,6 +88,8 @@ EXPERTS = {
     "4 x 4": (21, 1600, 3600, 50, 3, 2),
     "many, 2 x 1": (24, 1000, 515, 120, 4, 1.3),
     "many, 2 x 1, whole tiles": (24, 1000, 1024, 120, 4, 1.3),
+    "many, a block a CU": (16, 1024, 640, 80, 4, 1.3),
+    "many, and one more": (17, 1021, 640, 85, 4, 1.3),
     "many, 2 x 1, passes": (3, 1000, 700, 600, 3, 1.5),
 }
 
