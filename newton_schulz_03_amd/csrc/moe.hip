@@ -567,9 +567,20 @@ hipError_t launch_moe_sort(MoeSortArgs a, int32_t id_bytes, hipStream_t s) {
 
 namespace {
 
-// Bytes of sorted rows from which they pass the caches by (4096 tokens x 8 x 6144 bf16, 403
-// MB: dispatch 93 us without the hint, 79 with it).
+// Bytes of sorted rows from which they pass the caches by.  A call by itself is
+// faster that way from 16 MB on (tokens x 8 x 6144 bf16, dispatch, combine and
+// gradient: 128 MB 27, 29 and 58 us, without the hint 34, 31 and 62; 384 MB 79, 82 and
+// 162, without 92, 93 and 175), but a call that follows then finds no rows in the
+// caches (dispatch and a copy of its rows: 64 MB 41.6 us, without the hint 39.0; 128 MB
+// 80.5 and 78.6; 256 MB 163 and 176; combine after a copy into its rows: 128 MB 73 and 77; 256 MB
+// 153 and 155).
 constexpr int64_t kNtRowBytes = 256ll << 20;
+// Rows that are no whole pieces of 16 bytes share lines with their neighbours, which
+// the hint then moves twice: only rows of this many bytes take it (300 MB of rows,
+// four a token, dispatch, combine and gradient: 200 bytes 269, 172 and 389 us, without the
+// hint 161, 141 and 243; 1000 bytes 114, 97 and 182, without 102, 96 and 175; 2004 bytes 107, 87 and
+// 177, without 105, 89 and 181; 4004 bytes 105, 87 and 173, without 108, 90 and 187).
+constexpr int64_t kNtOddRowBytes = 2000;
 // Rows of fewer bytes than this are one wave's, of more the block's; with few
 // tokens, whose waves do not fill the chip, already shorter ones are the block's
 // (1000 tokens x 2 x 1001 fp32: combine 4.8 us by blocks, 6.2 by waves; 16384 x 4 x 1024
@@ -580,10 +591,10 @@ constexpr int64_t kBlockRowBytes = 4096, kBlockRowBytesFew = 1024, kFewTokens = 
 // by waves 41, 47 and 115).
 constexpr int64_t kShortRowBytes = 256;
 
-// Calls `launch` with a token's waves and the hint as constants.
-template <typename F>
+// Calls `launch` with a token's waves and the hint as constants; A: the rows'
+// alignment.
+template <int A, typename F>
 hipError_t with_shape(const MoeRowArgs& a, F launch) {
-  const bool nt = a.tokens_n * a.top_k * a.row_bytes > kNtRowBytes;
   const bool wide = a.row_bytes >= (a.tokens_n < kFewTokens ? kBlockRowBytesFew : kBlockRowBytes);
   const bool narrow = a.row_bytes <= kShortRowBytes;
   using std::integral_constant;
@@ -592,12 +603,19 @@ hipError_t with_shape(const MoeRowArgs& a, F launch) {
   typedef integral_constant<int, 4> Four;
   const int64_t per = wide ? 1 : kThreads / (narrow ? kLanes<0> : kLanes<1>);
   const dim3 grid(static_cast<uint32_t>((a.tokens_n + per - 1) / per));
+  const bool nt = a.tokens_n * a.top_k * a.row_bytes > kNtRowBytes &&
+                  (A == 16 || a.row_bytes >= kNtOddRowBytes);
+  const auto with_hint = [&](auto w) {
+    if constexpr (A == 16 || w() != 0)  // kNtOddRowBytes is past 16 lanes' rows
+      if (nt) return launch(w, std::true_type(), grid);
+    launch(w, std::false_type(), grid);
+  };
   if (wide)
-    nt ? launch(Four(), std::true_type(), grid) : launch(Four(), std::false_type(), grid);
+    with_hint(Four());
   else if (narrow)
-    nt ? launch(Part(), std::true_type(), grid) : launch(Part(), std::false_type(), grid);
+    with_hint(Part());
   else
-    nt ? launch(One(), std::true_type(), grid) : launch(One(), std::false_type(), grid);
+    with_hint(One());
   return hipGetLastError();
 }
 
@@ -611,7 +629,7 @@ hipError_t with_rows(const MoeRowArgs& a, F launch) {
 template <typename T>
 hipError_t run_dispatch(const MoeRowArgs& a, hipStream_t s) {
   return with_rows<T>(a, [&](auto align) {
-    return with_shape(a, [&](auto w, auto nt, dim3 grid) {
+    return with_shape<align()>(a, [&](auto w, auto nt, dim3 grid) {
       hipLaunchKernelGGL((k_moe_dispatch<align(), w(), nt()>), grid, dim3(kThreads), 0, s, a);
     });
   });
@@ -620,7 +638,7 @@ hipError_t run_dispatch(const MoeRowArgs& a, hipStream_t s) {
 template <typename T>
 hipError_t run_combine(const MoeRowArgs& a, hipStream_t s) {
   return with_rows<T>(a, [&](auto align) {
-    return with_shape(a, [&](auto w, auto nt, dim3 grid) {
+    return with_shape<align()>(a, [&](auto w, auto nt, dim3 grid) {
       hipLaunchKernelGGL((k_moe_combine<T, align(), w(), nt()>), grid, dim3(kThreads), 0, s, a);
     });
   });
@@ -629,7 +647,7 @@ hipError_t run_combine(const MoeRowArgs& a, hipStream_t s) {
 template <typename T>
 hipError_t run_backward(const MoeRowArgs& a, hipStream_t s) {
   return with_rows<T>(a, [&](auto align) {
-    return with_shape(a, [&](auto w, auto nt, dim3 grid) {
+    return with_shape<align()>(a, [&](auto w, auto nt, dim3 grid) {
       hipLaunchKernelGGL((k_moe_backward<T, align(), w(), nt()>), grid, dim3(kThreads), 0, s, a);
     });
   });

@@ -1,7 +1,8 @@
-"""Dispatch, combine and its gradient where the sorted rows hold just over 256 MB and are
-read and written with the nontemporal hint: a block, a wave or 16 lanes a token, rows
-whose length is and is no multiple of 16 bytes.  Copies and rows of the gradient bit for bit, sums
-with the bounds of test_gpu_moe.py, all on the device."""
+"""Dispatch, combine and its gradient where the sorted rows hold just over 256 MB, from
+where rows of whole 16-byte pieces, and others of 2000 bytes and more, are read and
+written with the nontemporal hint: a block, a wave or 16 lanes a token, both kinds of
+length.  Copies and rows of the gradient bit for bit, sums with the bounds of
+test_gpu_moe.py, all on the device."""
 import pytest
 import torch
 
