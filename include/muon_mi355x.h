@@ -545,9 +545,11 @@ int32_t muon_dropout_batched(int32_t batch, const int64_t* numel, const void* co
  *   y        m x rows, `dtype` (MUON_BF16 or MUON_FP32); may not overlap x
  * Products are exact, sums fp32 in an order that the sizes fix, rounded once.
  * Scale bytes are to lie in [2, 252] or be 255.
- * Meant for up to some 64 rows an expert, where the weights' bytes bound it; more
- * are right but read the weights again every 64 (muon_f8_matmul_batched is for
- * those).
+ * Meant for up to some 64 rows an expert, where the weights' bytes bound it.  Where m is
+ * at most 16 min(m, count), an expert's weights are read again for every 16 of its
+ * rows, else for every 64: rows that all fall on a few of many experts take longer
+ * than with an operand of those experts alone.  muon_f8_matmul_batched is for many
+ * rows.
  *
  * count in [1, MUON_MOE_MAX_EXPERTS], rows and cols in [0, MUON_F8_MAX_DIM], m and
  * x_rows at most MUON_MOE_MAX_SLOTS, fewer than 2^28 tiles (MUON_ERR_UNSUPPORTED

@@ -1041,8 +1041,8 @@ def moe_dispatch(x, plan: MoePlan, out=None):
 
     x: tokens x cols, contiguous, bf16 or fp32.  out: rows x cols of the same
     dtype, for as many rows as are wanted (new: tokens * top_k); rows behind the
-    last sorted one are left as they were.  Its gradient is moe_combine without
-    weights.
+    last sorted one are left as they were (of a new one: unwritten).  Its gradient
+    is moe_combine without weights.
     """
     import torch
 
@@ -1095,7 +1095,8 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
     dweights[t, k] = <dout[t], ys[plan.rows[t, k]]> (float32 sums; 0 for dropped slots).
 
     dout: tokens x cols, ys: sorted rows x cols, of one dtype.  Returns (dys,
-    dweights); rows of dys behind the last sorted one are left as they were.
+    dweights); rows of dys behind the last sorted one are left as they were (of a new
+    one: unwritten).
     """
     import torch
 
@@ -1216,9 +1217,11 @@ def f4_matmul(x, w: F4Operand, plan: Optional[MoePlan] = None, gather: bool = Fa
     matrix e; gather: x are the tokens' own rows (as moe_dispatch takes them), read
     through the plan.  Nothing of the plan is read on the host.  out: bf16 or fp32,
     x's rows (gather: up to tokens * top_k) x w.rows; new ones are of out_dtype
-    (bfloat16).  Rows behind the last sorted one are left as they were.  Products
-    are exact, sums fp32, rounded once.  For many rows an expert
-    f8_matmul_batched is faster.
+    (bfloat16).  Rows behind the last sorted one are left as they were (of new
+    ones: unwritten).  Products are exact, sums fp32, rounded once.  An
+    expert's weights are read again for every 16 of its rows, or 64 where the rows
+    are more than 16 times the experts that can have some; f8_matmul_batched, of e4m3
+    operands, is for many rows.
     """
     import torch
 

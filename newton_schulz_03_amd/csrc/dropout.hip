@@ -142,8 +142,11 @@ __global__ __launch_bounds__(kThreads) void k_dropout(ArgTable, GradCtx ctx, Dro
 
 namespace {
 
-// Bytes read and written from which they pass the caches by (inputs from memory: 130 + 130 MB
-// of bf16 49 us without the hint, 43.5 with it; 86 MB of fp32 into 43 of bf16 26 and 22).
+// Bytes read and written from which they pass the caches by.  A call by itself is
+// faster that way from 48 MB on (bf16, inputs from memory: 48 MB 11.1 us, without the
+// hint 12.8; 128 MB 23.8 and 25.6; 256 MB 44 and 48), but one that reads the result next
+// finds it in the caches without it (with a copy of the result: 32 MB 16.0 us, without
+// 14.3; 64 MB 26.9 and 24.5; 128 MB 48.5 and 44.3; 192 MB 69 and 70; 256 MB 91 and 118).
 constexpr int64_t kNtDropBytes = 64ll << 20;
 
 }  // namespace

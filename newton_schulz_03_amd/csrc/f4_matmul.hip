@@ -7,15 +7,16 @@
 // (v_cvt_scalef32_pk_bf16_fp4), and four 16x16x32 matrix instructions take a tile
 // of 16 weight rows x 128 columns times up to 16 rows of x.
 //
-// Bound by the weights' bytes: 264 experts of 6144 x 2048 with 3.9 rows each on
-// average take 298 us, 5.9 TB/s, where nothing but the loads of the weights
-// reaches 7.0 in this order and with those of the scales and one row of x 6.5.
-// What it took: one weight tile is 1024 bytes in a row, so that a wave's load is;
-// a wave takes RT strips of 16 rows, since every one of them needs the same x (RT
-// 1: 400 us, the loads of x are the bound); a ring of tiles in registers that is
-// refilled as it is used, without conditions, which cost registers for copies (400
-// us with them: one wave a SIMD); two waves a SIMD that do not spill (three that
-// do: 380).
+// Bound by the weights' bytes: 128 tokens x 8 of 384 experts, of which 265 have
+// rows, 3.9 on average, take 299 to 318 us of 6144 x 2048 (fp32 results, 5.6 to 5.9
+// TB/s, from machine to machine) and 294 to 299 of 2048 x 6144 (bf16).  Nothing but
+// the loads of the weights reached 7.0 TB/s in this order and with those of the scales
+// and one row of x 6.5.  What it took: one weight tile is 1024 bytes in a row, so that
+// a wave's load is; a wave takes RT strips of 16 rows, since every one of them needs
+// the same x (RT 1: 439 us against 315, the loads of x are the bound); a ring of tiles in
+// registers that is refilled as it is used, without conditions, which cost registers
+// for copies and left one wave a SIMD (a third longer); two waves a SIMD that do not
+// spill (three that do: a quarter longer).
 #include <algorithm>
 
 #include "device_common.hpp"
@@ -27,8 +28,11 @@ namespace {
 constexpr int kF4Waves = 4;  // of a block, 8 where 8 share the columns
 constexpr int kF4MaxSplit = 8;
 // Most rows of an expert, on average, of the kernel without LDS, which reads the
-// weights again for every 16 (one matrix 6144 x 6144: 16 rows 10.5 us, by the kernel
-// of many rows 20; 32 rows 27 and 20).
+// weights again for every 16 (one matrix 6144 x 6144: 16 rows 10.2 us, by the kernel
+// of many rows 19; 32 rows 27 and 19; 256 tokens x 8 of 384 experts 464 and 558; 512 tokens,
+// 10.7 rows on average and 107 at most, 656 and 617 of 2048 x 6144, 571 and 664 of 6144 x
+// 2048).  The host knows the average alone: 1024 rows that all fall on 8 of 384
+// experts, 2.7 on average, take 257 us, and would take 62 by the other kernel.
 constexpr int64_t kF4FewRows = 16;
 constexpr int64_t kF4Cus = 256;
 // Waves that keep the memory busy.
@@ -437,9 +441,9 @@ hipError_t run(F4ProdArgs a, hipStream_t s) {
   const int32_t quads = (a.ktiles + 3) / 4;
   const int64_t most_split = std::min<int64_t>(kF4MaxSplit, quads);
   // As many strips a wave as leave enough waves: 8 experts of 2048 x 6144 with two
-  // 12.8 us, with one 15.8; of 6144 x 2048 with two 12.5, with four 14.9; 264 of them with
-  // four 298, with one 400.  Then as many waves to share the columns as make up
-  // kF4Busy (one matrix 2048 x 6144: 5.6 us by eight, 5.8 by four).
+  // 11.3 us, with one 14.2, with four 13.2; 265 of 6144 x 2048 with four 315, with two 320 to
+  // 334, with one 439.  Then as many waves to share the columns as make up kF4Busy (one
+  // matrix 2048 x 6144: 6.0 us by eight, 6.4 by four; of 16 rows 9.3 and 8.9).
   const int rt = strips * most_split >= 8 * kF4Busy ? 4 : strips * most_split >= kF4Busy ? 2 : 1;
   a.ksplit = 1;
   while (a.ksplit < kF4MaxSplit && 2 * a.ksplit <= quads && strips / rt * a.ksplit < kF4Busy) a.ksplit *= 2;

@@ -13,7 +13,7 @@
 //
 // Dispatch, combine and its gradient are bound by the rows' bytes: a token's row is
 // read once, the rows of up to kBatch of its slots are asked for (or stored)
-// together.  4096 tokens x 8 x 6144 bf16: 78, 82 and 160 us (5.8, 5.5 and 5.3 TB/s; a slot
+// together.  4096 tokens x 8 x 6144 bf16: 79, 82 and 160 us (5.7, 5.5 and 5.3 TB/s; a slot
 // after the other, 92, 98 and 184).  Rows whose length is no multiple of 16 bytes are
 // read and written 16 bytes at a time all the same, at element-aligned addresses
 // (16384 x 4 x 1001 bf16: 30, 32 and 58 us; by elements 34, 60 and 121).
@@ -445,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_backward(MoeRowArgs a) {
 
 // The plan of up to kSortFew slots, by comparing all of them with each other and
 // with every expert: two barriers and no counts to clear and add up (8 slots of
-// 384 experts 3.6 us; the kernel above 6.6).
+// 384 experts 2.2 us; the kernel above 4.2).
 constexpr int kFewThreads = 512;
 template <typename I>
 __global__ __launch_bounds__(kFewThreads) void k_moe_sort_few(MoeSortArgs a) {
@@ -538,7 +538,8 @@ hipError_t run_blocks(const MoeSortArgs& a, hipStream_t s) {
 
 template <typename I>
 hipError_t run_sort(const MoeSortArgs& a, hipStream_t s) {
-  // 384 experts: 8 slots 2.7 us, by pieces 4.8; 128 slots 12.3 and 4.8
+  // 384 experts: 8 slots 2.2 us, by pieces 4.2; 32 slots 4.1 and 4.2; 64 slots 6.6 and 4.3;
+  // 16 slots of 512 experts 3.4 and 4.4, 10 of 1024 3.4 and 4.8
   if (a.n * ((a.experts + kFewThreads) / kFewThreads) <= kSortFew) {
     hipLaunchKernelGGL(k_moe_sort_few<I>, dim3(1), dim3(kFewThreads), 0, s, a);
     return hipGetLastError();
@@ -583,12 +584,15 @@ constexpr int64_t kNtRowBytes = 256ll << 20;
 constexpr int64_t kNtOddRowBytes = 2000;
 // Rows of fewer bytes than this are one wave's, of more the block's; with few
 // tokens, whose waves do not fill the chip, already shorter ones are the block's
-// (1000 tokens x 2 x 1001 fp32: combine 4.8 us by blocks, 6.2 by waves; 16384 x 4 x 1024
-// bf16: 26.4 and 25.6).
+// (combine, 1000 tokens x 2 x 1001 fp32: 5.2 us by blocks, 6.6 by waves; 16384 x 4 x 1024 bf16
+// 25.4 and 25.0, x 2048 63 and 80).
 constexpr int64_t kBlockRowBytes = 4096, kBlockRowBytesFew = 1024, kFewTokens = 4096;
-// Rows of up to this many bytes are 16 lanes' (65536 tokens x 8 x 64 bf16, dispatch,
-// combine and gradient: 14, 18 and 28 us, by waves 24, 38 and 60; x 200: 47, 54 and 136,
-// by waves 41, 47 and 115).
+// Rows of up to this many bytes are 16 lanes' (65536 tokens x 8 bf16, dispatch, combine
+// and gradient: 64 columns 13, 18 and 27 us, by waves 24, 38 and 60; 128 columns 24, 27 and
+// 51, by waves 25, 39 and 76; 160 columns 32, 44 and 83, by waves 31, 41 and 87; 200 columns 47, 54
+// and 137, by waves 40, 47 and 119).  With one or two choices a token the waves would
+// win later only: 256 columns 12, 14 and 20 us by 16 lanes, 20, 23 and 39 by waves, which
+// have one row to ask for.
 constexpr int64_t kShortRowBytes = 256;
 
 // Calls `launch` with a token's waves and the hint as constants; A: the rows'
